@@ -288,6 +288,139 @@ cai_status cai_mqa_prefill_varlen(const cai_kv_pool* pool, const uint16_t* q, in
                                   int32_t window, float softmax_scale, void* workspace, size_t workspace_bytes,
                                   float* out, float* lse_out, int32_t* err_flag, void* stream);
 
+/* ---- Rotated appends, reading back, and the 4-bit cache --------------------
+ * The calls of this section take one pool per K/V head (num_kv_heads of them, 1..8,
+ * as cai_gqa_decode: the same page size, block table and lengths for all) and give
+ * new tokens as rows.  Rows are either `n_new` per sequence (q_offsets null, sequence b
+ * owning rows [b * n_new, (b + 1) * n_new); total_new is not read), or packed as in
+ * cai_mqa_prefill_varlen: sequence b owns rows [q_offsets[b], q_offsets[b + 1]) of
+ * total_new, at most n_new of them.  A sequence whose offsets are out of order, beyond
+ * total_new or longer than n_new sets CAI_DEVERR_LENGTH and none of its rows is touched.
+ *
+ * The 4-bit cache holds a token's K (and V) as 128 4-bit codes and four scales, one
+ * per 32 channels: s = fp16(bf16(max |x| / 7)) (both roundings to nearest even, the
+ * division IEEE fp32; at most 9344, so magnitudes above 65408 saturate), code =
+ * clamp(round_half_even(x / s), -7, 7), codes 0 when s is 0.  A code stands for
+ * code * s, exactly an fp16 number.  A token takes 144 bytes per K/V head, against 264
+ * in the int8 cache. */
+
+/* One buffer of the 4-bit cache.  A page is page_size / 16 blocks of 2304 bytes, 16
+ * tokens each: K codes (1024 bytes), V codes (1024), K scales fp16 [16][4] (128), V
+ * scales fp16 (128).  Codes are stored as code + 8 in a byte:
+ *   K of token r: bits 4 i + 16 e (i = 0..3, e = 0, 1) of the 32-bit word at
+ *     64 r + 16 t + 4 j hold channel 32 j + 8 t + 2 i + e;
+ *   V: bits 4 i + 16 e of the word at 1024 + 4 ((32 h + 4 g + t) 4 + w) hold channel
+ *     16 (4 h + w) + g + 8 (i mod 2) of token 8 (i div 2) + 2 t + e;
+ *   V scales: token 8 b + 2 t + e, channels 32 j .. 32 j + 31 at 2176 + 2 (16 t + 8 b + 2 j + e).
+ * `pages` must be 16-byte aligned; it holds num_pages * cai_kv4_page_bytes(P, d) bytes. */
+typedef struct cai_kv4_pool {
+  void* pages;
+  int32_t num_pages;
+  int32_t page_size; /* 16, 32 or 64 tokens */
+  int32_t head_dim;  /* 128 */
+} cai_kv4_pool;
+
+/* Bytes of one page of the 4-bit cache: page_size * (head_dim + head_dim / 8).  0 unless
+ * page_size is a positive multiple of 16 and head_dim one of 32. */
+size_t cai_kv4_page_bytes(int32_t page_size, int32_t head_dim);
+
+/* Position rotation.  Channels [0, rot_dim) pair up, i with i + rot_dim / 2, or 2 i with
+ * 2 i + 1 if `interleaved` is not 0; at position p a pair (a, b) becomes
+ * (a c - b s, b c + a s) with c = cos[p][i], s = sin[p][i], every product and sum
+ * rounded to fp32 on its own.  The other channels pass.
+ *   cos, sin       device fp32 [num_positions][rot_dim / 2], 4-byte aligned
+ *   rot_dim        even, 2..128
+ * A token at a position of num_positions or beyond sets CAI_DEVERR_LENGTH and is left out. */
+typedef struct cai_rope {
+  const float* cos;
+  const float* sin;
+  int32_t num_positions;
+  int32_t rot_dim;
+  int32_t interleaved;
+} cai_rope;
+
+/* Element type of K/V rows. */
+typedef enum cai_dtype { CAI_FP32 = 0, CAI_BF16 = 1 } cai_dtype;
+
+/* Rotate, quantize and append new tokens, and rotate their queries, in one launch.
+ * Without a rotation cai_kv_append_rope writes the bytes that cai_kv_append writes for
+ * every K/V head; cai_kv4_append is the same into the 4-bit cache.
+ *   kv_pools      host array [num_kv_heads]
+ *   rope          host pointer, null for no rotation (V is never rotated)
+ *   k_new, v_new  kv_type [rows][num_kv_heads][128], rows k_stride / v_stride ELEMENTS
+ *                 apart (so that they may be slices of one projection's output); 16-byte
+ *                 aligned, strides a multiple of 16 bytes and at least num_kv_heads * 128
+ *   q, q_out      bf16 bits: [rows][num_q_heads][128], rows q_stride elements apart, to
+ *                 [rows][num_q_heads][128] contiguous; both null (num_q_heads 0) for none,
+ *                 otherwise rope must be given.  16-byte aligned, q_stride a multiple of 8;
+ *                 q_out may be q itself when q_stride is num_q_heads * 128, otherwise they
+ *                 must not overlap
+ *   start_pos     int32 [batch]: row i of sequence b goes to position start_pos[b] + i
+ * Bad positions and page ids as in cai_kv_append (a token whose position is bad gets no
+ * q_out row; one whose page is bad does). */
+cai_status cai_kv_append_rope(const cai_kv_pool* kv_pools, int32_t num_kv_heads, const cai_rope* rope,
+                              const void* k_new, const void* v_new, cai_dtype kv_type, int64_t k_stride,
+                              int64_t v_stride, const uint16_t* q, int64_t q_stride, uint16_t* q_out,
+                              int32_t num_q_heads, int32_t batch, int32_t n_new, const int32_t* q_offsets,
+                              int32_t total_new, const int32_t* block_table, int32_t max_pages_per_seq,
+                              const int32_t* start_pos, int32_t* err_flag, void* stream);
+cai_status cai_kv4_append(const cai_kv4_pool* kv_pools, int32_t num_kv_heads, const cai_rope* rope,
+                          const void* k_new, const void* v_new, cai_dtype kv_type, int64_t k_stride,
+                          int64_t v_stride, const uint16_t* q, int64_t q_stride, uint16_t* q_out,
+                          int32_t num_q_heads, int32_t batch, int32_t n_new, const int32_t* q_offsets,
+                          int32_t total_new, const int32_t* block_table, int32_t max_pages_per_seq,
+                          const int32_t* start_pos, int32_t* err_flag, void* stream);
+
+/* Read cached tokens back as the values they stand for (code * scale in fp32; bf16 rounds
+ * that once more): for an attention that the library does not have, or to move a dialogue
+ * from one cache to the other.  Row i of sequence b comes from position start_pos[b] + i.
+ *   k_out, v_out  out_type [rows][num_kv_heads][128], 16-byte aligned; one may be null
+ * A bad position or page id sets its bit in *err_flag and its rows become 0. */
+cai_status cai_kv_read(const cai_kv_pool* kv_pools, int32_t num_kv_heads, void* k_out, void* v_out,
+                       cai_dtype out_type, int32_t batch, int32_t n_new, const int32_t* q_offsets,
+                       int32_t total_new, const int32_t* block_table, int32_t max_pages_per_seq,
+                       const int32_t* start_pos, int32_t* err_flag, void* stream);
+cai_status cai_kv4_read(const cai_kv4_pool* kv_pools, int32_t num_kv_heads, void* k_out, void* v_out,
+                        cai_dtype out_type, int32_t batch, int32_t n_new, const int32_t* q_offsets,
+                        int32_t total_new, const int32_t* block_table, int32_t max_pages_per_seq,
+                        const int32_t* start_pos, int32_t* err_flag, void* stream);
+
+/* One decode step of one layer over the 4-bit cache: cai_gqa_decode's attention, reading
+ * 144 bytes a token and K/V head.
+ *   num_q_heads   a multiple of num_kv_heads; up to 128 query heads per K/V head
+ *   out           bf16 bits [batch][num_q_heads][128], 16-byte aligned (fp32 sums, rounded
+ *                 once)
+ *   workspace     cai_kv4_decode_workspace_size() bytes, 256-byte aligned; may be null when
+ *                 that is 0.  It needs no preparation; calls that share it must not overlap
+ *                 on the GPU.
+ *   q, block_table, ctx_len, window, softmax_scale, num_splits, lse_out as cai_gqa_decode
+ * A sequence with nothing to attend, or of an invalid length (flagged), gets out = 0 and
+ * lse = -inf.  Slots past a sequence's length are not looked at, whatever they hold. */
+size_t cai_kv4_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                     int32_t max_pages_per_seq, int32_t page_size, int32_t window,
+                                     int32_t num_splits);
+cai_status cai_kv4_decode(const cai_kv4_pool* kv_pools, int32_t num_kv_heads, const uint16_t* q, int32_t batch,
+                          int32_t num_q_heads, const int32_t* block_table, int32_t max_pages_per_seq,
+                          const int32_t* ctx_len, int32_t window, float softmax_scale, int32_t num_splits,
+                          void* workspace, size_t workspace_bytes, uint16_t* out, float* lse_out,
+                          int32_t* err_flag, void* stream);
+
+/* Attention of new tokens on a reused prefix over the 4-bit cache: cai_mqa_prefill_chunk
+ * (q_offsets null) and cai_mqa_prefill_varlen (packed rows, decode rows among them) for
+ * num_kv_heads K/V heads.  The new tokens' K/V must already be appended.
+ *   num_q_heads   num_kv_heads times a power of two from 1 to 128
+ *   q             bf16 bits [rows][num_q_heads][128]; prefix_len int32 [batch]
+ *   out           bf16 bits [rows][num_q_heads][128]; lse_out fp32 [rows][num_q_heads], nullable
+ *   workspace     cai_kv4_prefill_workspace_size() bytes, 256-byte aligned (no preparation)
+ * Other arguments and errors as for the int8 calls. */
+size_t cai_kv4_prefill_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
+                                      int32_t max_pages_per_seq, int32_t page_size);
+cai_status cai_kv4_prefill(const cai_kv4_pool* kv_pools, int32_t num_kv_heads, const uint16_t* q, int32_t batch,
+                           int32_t n_new, const int32_t* q_offsets, int32_t total_new, int32_t num_q_heads,
+                           const int32_t* block_table, int32_t max_pages_per_seq, const int32_t* prefix_len,
+                           int32_t window, float softmax_scale, void* workspace, size_t workspace_bytes,
+                           uint16_t* out, float* lse_out, int32_t* err_flag, void* stream);
+
 /* ---- Cross-turn KV cache in host memory ----------------------------------
  * "Character.AI: inference optimization", 04 Cache between turns: the KV of
  * every processed prefix and generated message is kept in host memory in an

@@ -25,6 +25,8 @@ __all__ = [
     "CAI_DEVERR_PAGE", "CAI_DEVERR_LENGTH", "CAI_DEVERR_TIMEOUT", "HEAD_DIM", "cai_host_cache_create",
     "cai_host_cache_destroy", "cai_host_cache_match", "cai_host_cache_restore", "cai_host_cache_store",
     "cai_host_cache_stats", "cai_host_cache_restore_batch", "cai_set_wait_limit_ns", "cai_set_fault_injection", "cai_ring_pages", "cai_ring_table_row",
+    "KV4Pool", "Rope", "cai_kv4_page_bytes", "cai_kv_append_rope", "cai_kv4_append", "cai_kv_read", "cai_kv4_read",
+    "cai_kv4_decode_workspace_size", "cai_kv4_decode", "cai_kv4_prefill_workspace_size", "cai_kv4_prefill",
 ]
 
 HEAD_DIM = 128
@@ -49,6 +51,15 @@ class CaiError(RuntimeError):
 class cai_kv_pool(ctypes.Structure):
     _fields_ = [("pages", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32)]
+
+
+class cai_kv4_pool(ctypes.Structure):
+    _fields_ = cai_kv_pool._fields_
+
+
+class cai_rope(ctypes.Structure):
+    _fields_ = [("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("num_positions", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
 
 
 def library_path() -> str:
@@ -109,6 +120,28 @@ def load():
     lib.cai_gqa_decode.argtypes = [pool_p, i32, vp, i32, i32, vp, i32, vp, i32, ctypes.c_float, i32, vp, sz, vp, vp,
                                    vp, vp]
     lib.cai_gqa_decode.restype = ctypes.c_int
+    pool4_p, rope_p, i64 = ctypes.POINTER(cai_kv4_pool), ctypes.POINTER(cai_rope), ctypes.c_int64
+    lib.cai_kv4_page_bytes.argtypes = [i32, i32]
+    lib.cai_kv4_page_bytes.restype = sz
+    for name, pp in (("cai_kv_append_rope", pool_p), ("cai_kv4_append", pool4_p)):
+        f = getattr(lib, name)
+        f.argtypes = [pp, i32, rope_p, vp, vp, ctypes.c_int, i64, i64, vp, i64, vp, i32, i32, i32, vp, i32, vp, i32, vp,
+                      vp, vp]
+        f.restype = ctypes.c_int
+    for name, pp in (("cai_kv_read", pool_p), ("cai_kv4_read", pool4_p)):
+        f = getattr(lib, name)
+        f.argtypes = [pp, i32, vp, vp, ctypes.c_int, i32, i32, vp, i32, vp, i32, vp, vp, vp]
+        f.restype = ctypes.c_int
+    lib.cai_kv4_decode_workspace_size.argtypes = [i32] * 7
+    lib.cai_kv4_decode_workspace_size.restype = sz
+    lib.cai_kv4_decode.argtypes = [pool4_p, i32, vp, i32, i32, vp, i32, vp, i32, ctypes.c_float, i32, vp, sz, vp, vp, vp,
+                                   vp]
+    lib.cai_kv4_decode.restype = ctypes.c_int
+    lib.cai_kv4_prefill_workspace_size.argtypes = [i32] * 5
+    lib.cai_kv4_prefill_workspace_size.restype = sz
+    lib.cai_kv4_prefill.argtypes = [pool4_p, i32, vp, i32, i32, vp, i32, i32, vp, i32, vp, i32, ctypes.c_float, vp, sz, vp,
+                                    vp, vp, vp]
+    lib.cai_kv4_prefill.restype = ctypes.c_int
     lib.cai_host_cache_create.argtypes = [i32, i32, i32, ctypes.c_int64]
     lib.cai_host_cache_create.restype = vp
     lib.cai_host_cache_destroy.argtypes = [vp]
@@ -462,3 +495,231 @@ def cai_ring_table_row(ring_ids, hi: int, page_size: int, max_pages_per_seq: int
     st = load().cai_ring_table_row(row.ctypes.data, max_pages_per_seq, ids.ctypes.data, len(ids), hi, page_size)
     _check(st, "cai_ring_table_row")
     return row
+
+
+# ---- Rotated appends, reading back, and the 4-bit cache ------------------------------------
+
+def cai_kv4_page_bytes(page_size: int, head_dim: int = HEAD_DIM) -> int:
+    return int(load().cai_kv4_page_bytes(page_size, head_dim))
+
+
+class KV4Pool:
+    """One buffer of the 4-bit cache: ``num_pages`` pages of ``page_size`` tokens in one uint8 CUDA tensor
+    (cai_kv4_page_bytes each).  ``pages`` may be given, as for KVPool."""
+
+    def __init__(self, num_pages: int, page_size: int, head_dim: int = HEAD_DIM, device=None,
+                 pages: Optional[torch.Tensor] = None):
+        nbytes = num_pages * cai_kv4_page_bytes(page_size, head_dim)
+        if pages is None:
+            pages = torch.empty(nbytes, dtype=torch.uint8, device=device or "cuda")
+        if pages.dtype != torch.uint8 or pages.numel() != nbytes or not pages.is_cuda or not pages.is_contiguous():
+            raise ValueError("pages must be a contiguous uint8 CUDA tensor of num_pages * page_bytes bytes")
+        self.pages = pages
+        self.num_pages, self.page_size, self.head_dim = num_pages, page_size, head_dim
+        self.struct = cai_kv4_pool(pages.data_ptr(), num_pages, page_size, head_dim)
+
+
+class Rope:
+    """Position rotation: cos and sin fp32 CUDA tensors [positions][rot_dim / 2]; channel i pairs with
+    i + rot_dim / 2, or 2 i with 2 i + 1 when ``interleaved``."""
+
+    def __init__(self, cos: torch.Tensor, sin: torch.Tensor, interleaved: bool = False):
+        if cos.dim() != 2 or cos.shape != sin.shape:
+            raise ValueError("cos and sin must have one shape [positions][rot_dim / 2]")
+        self.cos, self.sin = cos, sin
+        self.struct = cai_rope(_ptr(cos, "cos", torch.float32), _ptr(sin, "sin", torch.float32), cos.shape[0],
+                               2 * cos.shape[1], int(interleaved))
+
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1}
+
+
+def _pools_of(pools, kind):
+    pools = list(pools) if isinstance(pools, (list, tuple)) else [pools]
+    for p in pools:
+        if not isinstance(p, kind):
+            raise TypeError(f"pools must be {kind.__name__} objects, got {type(p).__name__}")
+    struct = cai_kv_pool if kind is KVPool else cai_kv4_pool
+    return (struct * len(pools))(*[p.struct for p in pools]), len(pools)
+
+
+def _rows_shape(t: torch.Tensor, packed: bool, name: str):
+    """(rows, batch or None, n_new or None, heads) of new-token rows: [rows][heads][128] packed,
+    [batch][n_new][heads][128] otherwise."""
+    if t.dim() != (3 if packed else 4) or t.shape[-1] != HEAD_DIM:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
+                         + ("[rows][heads][128] with q_offsets" if packed else "[batch][n_new][heads][128]"))
+    if packed:
+        return t.shape[0], None, None, t.shape[1]
+    return t.shape[0] * t.shape[1], t.shape[0], t.shape[1], t.shape[2]
+
+
+def _row_stride(t: torch.Tensor, name: str) -> int:
+    """Elements between rows of [..rows..][heads][128] whose heads are contiguous."""
+    s, n = t.stride(), t.shape
+    if t.numel() == 0:
+        return n[-2] * HEAD_DIM
+    ok = s[-1] == 1 and (n[-2] == 1 or s[-2] == HEAD_DIM)
+    if t.dim() == 4 and n[0] > 1 and n[1] > 1:
+        ok = ok and s[0] == n[1] * s[1]
+    if not ok:
+        raise ValueError(f"{name}: the heads of a row must be contiguous and rows equally spaced")
+    rows = n[0] * n[1] if t.dim() == 4 else n[0]
+    if rows == 1:
+        return n[-2] * HEAD_DIM
+    return s[0] if t.dim() == 3 or n[1] == 1 else s[1]
+
+
+def _cuda(t: Optional[torch.Tensor], name: str) -> Optional[int]:
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    return t.data_ptr()
+
+
+def _table(block_table: torch.Tensor, batch: int):
+    if block_table.dim() != 2 or block_table.shape[0] != batch:
+        raise ValueError(f"block_table has shape {tuple(block_table.shape)}, expected [{batch}][max_pages]")
+    return _ptr(block_table, "block_table", torch.int32), block_table.shape[1]
+
+
+def _packing(t: torch.Tensor, name: str, q_offsets, max_new, start_pos: torch.Tensor):
+    """(rows, batch, n_new, heads) of a call whose rows are those of t."""
+    rows, batch, n_new, heads = _rows_shape(t, q_offsets is not None, name)
+    if q_offsets is not None:
+        if max_new is None:
+            raise ValueError("packed rows (q_offsets) need max_new")
+        batch, n_new = start_pos.shape[0], int(max_new)
+        _ptr(q_offsets, "q_offsets", torch.int32, (batch + 1,))
+    elif max_new is not None:
+        raise ValueError("max_new goes with q_offsets")
+    return rows, batch, n_new, heads
+
+
+def _append_rows(entry: str, kind, pools, k_new, v_new, block_table, start_pos, rope, q, q_out, q_offsets, max_new,
+                 err_flag, stream) -> None:
+    arr, hkv = _pools_of(pools, kind)
+    rows, batch, n_new, heads = _packing(k_new, "k_new", q_offsets, max_new, start_pos)
+    if heads != hkv or v_new.shape != k_new.shape:
+        raise ValueError(f"k_new and v_new must have one shape with {hkv} heads, got {tuple(k_new.shape)} and "
+                         f"{tuple(v_new.shape)}")
+    if k_new.dtype not in _DTYPES or v_new.dtype != k_new.dtype:
+        raise TypeError(f"k_new and v_new must both be fp32 or bf16, got {k_new.dtype} and {v_new.dtype}")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    hq, q_stride = 0, 0
+    if q is not None:
+        q_rows, _, _, hq = _rows_shape(q, q_offsets is not None, "q")
+        if q_rows != rows or q_out.shape != q.shape or q.dtype != torch.bfloat16:
+            raise ValueError("q must be bf16 with the rows of k_new, and q_out of its shape")
+        q_stride = _row_stride(q, "q")
+    table, width = _table(block_table, batch)
+    st = getattr(load(), entry)(
+        arr, hkv, ctypes.byref(rope.struct) if rope is not None else None, _cuda(k_new, "k_new"), _cuda(v_new, "v_new"),
+        _DTYPES[k_new.dtype], _row_stride(k_new, "k_new"), _row_stride(v_new, "v_new"), _cuda(q, "q"), q_stride,
+        _ptr(q_out, "q_out", torch.bfloat16), hq, batch, n_new, q_offsets.data_ptr() if q_offsets is not None else None,
+        rows, table, width, _ptr(start_pos, "start_pos", torch.int32, (batch,)),
+        _ptr(err_flag, "err_flag", torch.int32), _stream(stream))
+    _check(st, entry)
+
+
+def cai_kv_append_rope(pools: Sequence[KVPool], k_new: torch.Tensor, v_new: torch.Tensor, block_table: torch.Tensor,
+                       start_pos: torch.Tensor, rope: Optional[Rope] = None, q: Optional[torch.Tensor] = None,
+                       q_out: Optional[torch.Tensor] = None, q_offsets: Optional[torch.Tensor] = None,
+                       max_new: Optional[int] = None, err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Rotate and quantize k_new/v_new (fp32 or bf16) into the int8 pools of the K/V heads, and rotate q (bf16)
+    into q_out.  Rows: [batch][n_new][heads][128], or [rows][heads][128] packed by q_offsets (at most max_new a
+    sequence); k_new, v_new and q may be slices of one projection's output."""
+    _append_rows("cai_kv_append_rope", KVPool, pools, k_new, v_new, block_table, start_pos, rope, q, q_out, q_offsets,
+                 max_new, err_flag, stream)
+
+
+def cai_kv4_append(pools: Sequence[KV4Pool], k_new: torch.Tensor, v_new: torch.Tensor, block_table: torch.Tensor,
+                   start_pos: torch.Tensor, rope: Optional[Rope] = None, q: Optional[torch.Tensor] = None,
+                   q_out: Optional[torch.Tensor] = None, q_offsets: Optional[torch.Tensor] = None,
+                   max_new: Optional[int] = None, err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """cai_kv_append_rope into the 4-bit cache."""
+    _append_rows("cai_kv4_append", KV4Pool, pools, k_new, v_new, block_table, start_pos, rope, q, q_out, q_offsets,
+                 max_new, err_flag, stream)
+
+
+def _read_rows(entry: str, kind, pools, k_out, v_out, block_table, start_pos, q_offsets, max_new, err_flag,
+               stream) -> None:
+    arr, hkv = _pools_of(pools, kind)
+    one = k_out if k_out is not None else v_out
+    if one is None:
+        raise ValueError("one of k_out and v_out must be given")
+    rows, batch, n_new, heads = _packing(one, "k_out", q_offsets, max_new, start_pos)
+    if heads != hkv or (k_out is not None and v_out is not None and (v_out.shape != k_out.shape or v_out.dtype != k_out.dtype)):
+        raise ValueError(f"k_out and v_out must have one shape and dtype, with {hkv} heads")
+    if one.dtype not in _DTYPES:
+        raise TypeError(f"outputs must be fp32 or bf16, got {one.dtype}")
+    table, width = _table(block_table, batch)
+    st = getattr(load(), entry)(
+        arr, hkv, _ptr(k_out, "k_out"), _ptr(v_out, "v_out"), _DTYPES[one.dtype], batch, n_new,
+        q_offsets.data_ptr() if q_offsets is not None else None, rows, table, width,
+        _ptr(start_pos, "start_pos", torch.int32, (batch,)), _ptr(err_flag, "err_flag", torch.int32), _stream(stream))
+    _check(st, entry)
+
+
+def cai_kv_read(pools: Sequence[KVPool], k_out: Optional[torch.Tensor], v_out: Optional[torch.Tensor],
+                block_table: torch.Tensor, start_pos: torch.Tensor, q_offsets: Optional[torch.Tensor] = None,
+                max_new: Optional[int] = None, err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Cached tokens of the int8 pools as the values they stand for, fp32 or bf16; rows as in cai_kv_append_rope."""
+    _read_rows("cai_kv_read", KVPool, pools, k_out, v_out, block_table, start_pos, q_offsets, max_new, err_flag, stream)
+
+
+def cai_kv4_read(pools: Sequence[KV4Pool], k_out: Optional[torch.Tensor], v_out: Optional[torch.Tensor],
+                 block_table: torch.Tensor, start_pos: torch.Tensor, q_offsets: Optional[torch.Tensor] = None,
+                 max_new: Optional[int] = None, err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """cai_kv_read of the 4-bit cache."""
+    _read_rows("cai_kv4_read", KV4Pool, pools, k_out, v_out, block_table, start_pos, q_offsets, max_new, err_flag, stream)
+
+
+def cai_kv4_decode_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, max_pages_per_seq: int,
+                                  page_size: int, window: int, num_splits: int = 0) -> int:
+    return int(load().cai_kv4_decode_workspace_size(batch, num_q_heads, num_kv_heads, max_pages_per_seq, page_size,
+                                                    window, num_splits))
+
+
+def cai_kv4_decode(pools: Sequence[KV4Pool], q: torch.Tensor, block_table: torch.Tensor, ctx_len: torch.Tensor,
+                   window: int, softmax_scale: float, num_splits: int, workspace: Optional[torch.Tensor],
+                   out: torch.Tensor, lse_out: Optional[torch.Tensor] = None,
+                   err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """One decode step of one layer over the 4-bit cache: q bf16 [batch][Hq][128] -> out bf16, one pool per K/V head."""
+    arr, hkv = _pools_of(pools, KV4Pool)
+    batch, hq = q.shape[0], q.shape[1]
+    shape = (batch, hq, HEAD_DIM)
+    table, width = _table(block_table, batch)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    st = load().cai_kv4_decode(
+        arr, hkv, _ptr(q, "q", torch.bfloat16, shape), batch, hq, table, width,
+        _ptr(ctx_len, "ctx_len", torch.int32, (batch,)), window, float(softmax_scale), num_splits,
+        _ptr(workspace, "workspace"), ws_bytes, _ptr(out, "out", torch.bfloat16, shape),
+        _ptr(lse_out, "lse_out", torch.float32, (batch, hq)), _ptr(err_flag, "err_flag", torch.int32), _stream(stream))
+    _check(st, "cai_kv4_decode")
+
+
+def cai_kv4_prefill_workspace_size(batch: int, num_q_heads: int, num_kv_heads: int, max_pages_per_seq: int,
+                                   page_size: int) -> int:
+    return int(load().cai_kv4_prefill_workspace_size(batch, num_q_heads, num_kv_heads, max_pages_per_seq, page_size))
+
+
+def cai_kv4_prefill(pools: Sequence[KV4Pool], q: torch.Tensor, block_table: torch.Tensor, prefix_len: torch.Tensor,
+                    window: int, softmax_scale: float, workspace: torch.Tensor, out: torch.Tensor,
+                    lse_out: Optional[torch.Tensor] = None, err_flag: Optional[torch.Tensor] = None,
+                    q_offsets: Optional[torch.Tensor] = None, max_new: Optional[int] = None, stream=None) -> None:
+    """Attention of appended new tokens over the 4-bit cache: q bf16 [batch][n_new][Hq][128], or packed
+    [rows][Hq][128] with q_offsets and max_new -> out bf16 of the same shape, lse_out without the last dimension."""
+    arr, hkv = _pools_of(pools, KV4Pool)
+    rows, batch, n_new, hq = _packing(q, "q", q_offsets, max_new, prefix_len)
+    table, width = _table(block_table, batch)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    st = load().cai_kv4_prefill(
+        arr, hkv, _ptr(q, "q", torch.bfloat16), batch, n_new, q_offsets.data_ptr() if q_offsets is not None else None,
+        rows, hq, table, width, _ptr(prefix_len, "prefix_len", torch.int32, (batch,)), window, float(softmax_scale),
+        _ptr(workspace, "workspace"), ws_bytes, _ptr(out, "out", torch.bfloat16, tuple(q.shape)),
+        _ptr(lse_out, "lse_out", torch.float32, tuple(q.shape[:-1])), _ptr(err_flag, "err_flag", torch.int32),
+        _stream(stream))
+    _check(st, "cai_kv4_prefill")

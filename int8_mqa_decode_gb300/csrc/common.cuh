@@ -106,6 +106,68 @@ __host__ __device__ inline SeqSplits seq_splits(int32_t L, int32_t window, int32
   return s;
 }
 
+// Append of rows with a rotation, and reading rows back (one pool per K/V head; rows packed by q_off,
+// or n_new per sequence when it is null).
+struct AppendRowsParams {
+  uint8_t* pages[kMaxKvHeads];
+  int32_t num_pages[kMaxKvHeads];
+  int32_t num_kv_heads, num_q_heads, page_size, max_pages;
+  int32_t batch, n_new, total_new;
+  const int32_t* q_off;
+  const int32_t* table;
+  const int32_t* start_pos;
+  const void* k;                // fp32 or bf16 [rows][Hkv][128], rows k_stride elements apart
+  const void* v;
+  int64_t k_stride, v_stride, q_stride;
+  const uint16_t* q;            // bf16 bits
+  uint16_t* q_out;              // bf16 bits [rows][Hq][128]
+  const float* cos;             // [num_positions][rot / 2]
+  const float* sin;
+  int32_t num_positions, rot, interleaved;  // rot 0: no rotation
+  int32_t* err;
+};
+
+struct ReadRowsParams {
+  const uint8_t* pages[kMaxKvHeads];
+  int32_t num_pages[kMaxKvHeads];
+  int32_t num_kv_heads, page_size, max_pages;
+  int32_t batch, n_new, total_new;
+  const int32_t* q_off;
+  const int32_t* table;
+  const int32_t* start_pos;
+  void* k_out;                  // fp32 or bf16 [rows][Hkv][128]; either may be null
+  void* v_out;
+  int32_t* err;
+};
+
+// One decode launch over the 4-bit cache.  q_off / total_rows: as in DecodeJob.
+struct Decode4Params {
+  const uint8_t* pages[kMaxKvHeads];  // one pool per K/V head
+  int32_t num_pages[kMaxKvHeads];
+  int32_t num_heads, num_kv_heads, batch;
+  int32_t page_size, max_pages, window;
+  const int32_t* table;    // [B][max_pages]
+  const int32_t* ctx_len;  // [B]
+  const int32_t* q_off;    // nullable
+  int32_t total_rows;
+  const uint16_t* q;       // bf16 bits
+  uint16_t* out;           // bf16 bits
+  float* lse_out;          // natural log, nullable
+  // Work split (plan_decode4).  chunk 0: the keys of all sequences and K/V heads, in tiles of 128, are
+  // cut into `ranges` equal parts, one per block; piece of block c: slot 2 c + 1 where it holds a
+  // sequence's first tile, 2 c otherwise; meta[b * num_kv_heads + K/V head] = {first block, last block}.
+  // chunk > 0: every sequence is cut into `splits` ranges of chunk keys; slot (unit * splits + range).
+  int32_t head_groups, ranges, chunk, splits;
+  int2* meta;
+  float* ws_o;             // [slot][query heads of a K/V head][128] normalised partial outputs
+  float* ws_lse;           // [slot][query heads of a K/V head] log2 units
+  float scale_log2;
+  int32_t* err;
+  uint64_t wait_ns;
+  int32_t drop_stage;
+  int32_t overlap_prev;    // as in DecodeParams
+};
+
 struct PrefillLaunch {
   const uint8_t* pages;
   int32_t num_pages, page_size, max_pages;
@@ -120,6 +182,13 @@ struct PrefillLaunch {
   float* lse_out;
   int32_t* err;
   bool skip_single;      // with q_off: sequences with one new token are decoded elsewhere
+  // The 4-bit cache (four): one pool per K/V head, num_heads then being the query heads of one K/V head
+  // and q_heads all of them; the output is bf16.  Otherwise num_kv_heads = 1, q_heads = num_heads.
+  bool four = false;
+  const uint8_t* pages4[kMaxKvHeads];
+  int32_t num_pages4[kMaxKvHeads];
+  int32_t num_kv_heads = 1, q_heads = 0;
+  uint16_t* out16 = nullptr;
 };
 
 // Limit of the kernels' bounded waits (cai_set_wait_limit_ns), read at every launch.
@@ -156,6 +225,10 @@ DecodePlan plan_decode(int32_t batch, int32_t max_pages_per_seq, int32_t page_si
                        int32_t num_splits, int32_t num_sms, int32_t items_per_sm);
 int num_sms();
 
+// Entry-point helpers shared by the caches.
+inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+inline bool page_size_ok(int32_t P) { return P == 16 || P == 32 || P == 64; }
+
 // CAI_OK for cudaSuccess; otherwise CAI_ERR_CUDA, with the error kept for
 // cai_last_cuda_error() on this thread.
 cai_status cuda_status(cudaError_t e);
@@ -163,5 +236,12 @@ cai_status cuda_status(cudaError_t e);
 // Kernel launchers (return cudaGetLastError()).
 cudaError_t launch_append(const AppendParams* ps, int n, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeParams& p, int page_size, cudaStream_t stream);
+cudaError_t launch_append_rows(const AppendRowsParams& p, bool four, bool bf16, cudaStream_t stream);
+cudaError_t launch_read_rows(const ReadRowsParams& p, bool four, bool bf16, cudaStream_t stream);
+cudaError_t launch_decode4(const Decode4Params& p, cudaStream_t stream);
+// Fills the split fields of p (batch, heads, page_size, max_pages and window given; num_splits 0: automatic) and
+// returns the workspace bytes that they need; place_decode4 then sets the workspace's pointers.
+size_t plan_decode4(Decode4Params& p, int32_t num_splits);
+void place_decode4(Decode4Params& p, void* workspace);
 
 }  // namespace cai

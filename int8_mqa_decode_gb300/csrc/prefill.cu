@@ -27,11 +27,18 @@
 //     boundary tiles only, raises the reference lazily (when a logit exceeds it
 //     by 2^8), and writes P (fp16) into tensor memory, where it is the A operand
 //     of O_h += P_h V_h (V from shared memory, MN-major).
+//
+// The 4-bit cache runs through the same kernels (kFour): there the copy's K is the fp16 value that a
+// code stands for (exact, so no per-key scale is left), the query is converted to fp16 as it is staged,
+// the copy holds one "sequence" per (sequence, K/V head), whose rows are (token, query head of that K/V
+// head) pairs, and the output is bf16.
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <type_traits>
 
 #include "common.cuh"
+#include "kv4.cuh"
 #include "ptx.cuh"
 
 namespace cai {
@@ -114,6 +121,11 @@ struct PrefillParams {
   float* out;
   float* lse_out;
   int32_t* err;
+  // The 4-bit cache; elsewhere one K/V head and q_heads = num_heads.
+  int32_t num_kv_heads, q_heads;
+  const uint8_t* pages4[kMaxKvHeads];
+  int32_t num_pages4[kMaxKvHeads];
+  uint16_t* out16;
 };
 
 // New tokens of sequence b: rows [r0, r0 + n) of q / out, or n = -1 when its offsets
@@ -251,6 +263,81 @@ __device__ __forceinline__ void dequant_tile(const PrefillParams& p, int b, int 
   }
 }
 
+// The same for K/V head kvh of a 4-bit cache: warp w takes block w (16 keys) of the tile.  A lane's two
+// 16-byte loads of K hold channels 8 c .. 8 c + 7 of two keys for four chunks c, and are written as they
+// come; V, a channel per lane there, is transposed 8 x 8 in registers.  (V comes out as 4-byte stores
+// of whole 128-byte lines.)
+__device__ __forceinline__ void dequant_tile4(const PrefillParams& p, int b, int kvh, int tile) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int32_t p0 = p.prefix_len[b];
+  const SeqRows sr = seq_rows(p, b);
+  if (!seq_ok(p, p0, sr.n)) {
+    if (tile == 0 && threadIdx.x == 0 && p.err) atomicOr(p.err, CAI_DEVERR_LENGTH);
+    return;
+  }
+  const int len = p0 + sr.n;
+  const int lo_min = p.window > 0 ? max(0, p0 + 1 - p.window) : 0;
+  if (sr.n == 0 || tile * kKeys >= len || tile < lo_min / kKeys) return;  // never read
+  const int warp = threadIdx.x >> 5;
+  const int key0 = tile * kKeys + warp * kBlk;
+  const uint8_t* blk = nullptr;
+  if (key0 < len && key0 + kBlk > lo_min) {
+    const int P = p.page_size;
+    const int32_t page = p.table[(int64_t)b * p.max_pages + key0 / P];
+    if (page >= 0 && page < p.num_pages4[kvh])
+      blk = p.pages4[kvh] + (int64_t)page * page_bytes4(P) + (key0 % P) / kBlk * kBlkBytes;
+    else if (lane == 0 && p.err)
+      atomicOr(p.err, CAI_DEVERR_PAGE);
+  }
+  const int64_t base = (((int64_t)b * p.num_kv_heads + kvh) * p.kt_rows + tile * kKeys) * kHeadDim;
+  uint16_t* kt = p.kb + base + warp * kBlk * 8;
+  uint16_t* vt = p.vh + base + warp * kBlk * 8;
+  auto keep = [&](int key) { return blk && key < len && key >= lo_min; };  // other slots may hold anything
+#pragma unroll
+  for (int r = 0; r < 2; ++r) {
+    const bool live = keep(key0 + r * 8 + g);
+    uint4 kw = make_uint4(0u, 0u, 0u, 0u);
+    uint2 sc = make_uint2(0u, 0u);
+    if (live) {
+      kw = *reinterpret_cast<const uint4*>(blk + r * 512 + lane * 16);
+      sc = *reinterpret_cast<const uint2*>(blk + kBlkKs + (r * 8 + g) * 8);
+    }
+    const uint32_t w[4] = {kw.x, kw.y, kw.z, kw.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t s = __byte_perm(j < 2 ? sc.x : sc.y, 0u, j & 1 ? 0x3232u : 0x1010u);
+      uint32_t x[4];
+      values_f16(w[j], s, s, x);
+      *reinterpret_cast<uint4*>(kt + (4 * j + t) * 1024 + (r * 8 + g) * 8) = make_uint4(x[0], x[1], x[2], x[3]);
+    }
+  }
+  uint32_t s0[4] = {0u, 0u, 0u, 0u}, s1[4] = {0u, 0u, 0u, 0u}, w[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+  if (blk) {
+    const uint32_t m0 = (keep(key0 + 2 * t) ? 0xFFFFu : 0u) | (keep(key0 + 2 * t + 1) ? 0xFFFF0000u : 0u);
+    const uint32_t m1 = (keep(key0 + 2 * t + 8) ? 0xFFFFu : 0u) | (keep(key0 + 2 * t + 9) ? 0xFFFF0000u : 0u);
+    const uint4 a = *reinterpret_cast<const uint4*>(blk + kBlkVs + t * 32);
+    const uint4 c = *reinterpret_cast<const uint4*>(blk + kBlkVs + t * 32 + 16);
+    const uint4 v0 = *reinterpret_cast<const uint4*>(blk + kBlkV + lane * 16);
+    const uint4 v1 = *reinterpret_cast<const uint4*>(blk + kBlkV + 512 + lane * 16);
+    s0[0] = a.x & m0, s0[1] = a.y & m0, s0[2] = a.z & m0, s0[3] = a.w & m0;
+    s1[0] = c.x & m1, s1[1] = c.y & m1, s1[2] = c.z & m1, s1[3] = c.w & m1;
+    w[0] = v0.x, w[1] = v0.y, w[2] = v0.z, w[3] = v0.w;
+    w[4] = v1.x, w[5] = v1.y, w[6] = v1.z, w[7] = v1.w;
+  }
+#pragma unroll
+  for (int m = 0; m < 8; ++m) {
+    const int j = m >> 1;
+    uint32_t x[4];
+    values_f16(w[m], s0[j], s1[j], x);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {  // channels 16 m + 8 (i % 2) .. + 7 of keys 8 (i / 2) .. + 7
+      uint32_t y;
+      asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x[i]));
+      *reinterpret_cast<uint32_t*>(vt + (2 * m + (i & 1)) * 1024 + ((i >> 1) * 8 + g) * 8 + 2 * t) = y;
+    }
+  }
+}
+
 // Tiles of sequence b's copy that the dequant pass writes: [*lo, *lo + count).  A sequence
 // whose lengths are invalid writes none (and is flagged).
 __device__ __forceinline__ int dequant_tiles(const PrefillParams& p, int b, int* lo) {
@@ -268,9 +355,11 @@ __device__ __forceinline__ int dequant_tiles(const PrefillParams& p, int b, int*
   return (len + kKeys - 1) / kKeys - *lo;
 }
 
-// One block per 128-key tile of a sequence (blockIdx.y = sequence).
-__global__ void __launch_bounds__(256) dequant_kernel(const PrefillParams p) {
-  dequant_tile(p, blockIdx.y, blockIdx.x);
+// One block per 128-key tile of a sequence (blockIdx.y = sequence, blockIdx.z = K/V head of a 4-bit cache).
+template <bool kFour>
+__global__ void __launch_bounds__(256) dequant_kernel(const __grid_constant__ PrefillParams p) {
+  if constexpr (kFour) dequant_tile4(p, blockIdx.y, blockIdx.z, blockIdx.x);
+  else dequant_tile(p, blockIdx.y, blockIdx.x);
 }
 
 // Varlen calls: a grid-stride loop over only the tiles some query reads.  Each block
@@ -278,7 +367,8 @@ __global__ void __launch_bounds__(256) dequant_kernel(const PrefillParams p) {
 // shared memory, first[b] = number of sequence b's first tile, first[batch] = total);
 // the dense grid of the chunk calls would launch a block for every tile slot of every
 // sequence, most of them idle for the one-token rows of a mixed batch.
-__global__ void __launch_bounds__(256) dequant_compact_kernel(const PrefillParams p) {
+template <bool kFour>
+__global__ void __launch_bounds__(256) dequant_compact_kernel(const __grid_constant__ PrefillParams p) {
   extern __shared__ int32_t first[];
   __shared__ int32_t warp_sum[8];
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -304,8 +394,10 @@ __global__ void __launch_bounds__(256) dequant_compact_kernel(const PrefillParam
   }
   if (t == 255) first[B] = before + incl;
   __syncthreads();
-  const int total = first[B];
-  for (int w = blockIdx.x; w < total; w += gridDim.x) {
+  using Index = std::conditional_t<kFour, int64_t, int>;  // (tile, K/V head) pairs of a 4-bit cache
+  const Index total = kFour ? (Index)first[B] * p.num_kv_heads : first[B];
+  for (Index ww = blockIdx.x; ww < total; ww += gridDim.x) {
+    const int w = kFour ? (int)(ww / p.num_kv_heads) : (int)ww;
     int l = 0, h = B - 1;  // the last sequence whose first tile is <= w
     while (l < h) {
       const int mid = (l + h + 1) >> 1;
@@ -313,7 +405,8 @@ __global__ void __launch_bounds__(256) dequant_compact_kernel(const PrefillParam
       else h = mid - 1;
     }
     dequant_tiles(p, l, &lo);
-    dequant_tile(p, l, lo + (w - first[l]));
+    if constexpr (kFour) dequant_tile4(p, l, (int)(ww % p.num_kv_heads), lo + (w - first[l]));
+    else dequant_tile(p, l, lo + (w - first[l]));
   }
 }
 
@@ -322,15 +415,18 @@ __global__ void __launch_bounds__(256) dequant_compact_kernel(const PrefillParam
 // item's rows below `rows` (an invalid sequence) or nothing (rows beyond the chunk).
 struct PItem {
   int b, row0, kt0, nkt;
+  int kvh;        // K/V head (4-bit cache)
   int64_t qrow0;  // first packed new-token row of the sequence
   int rows;       // (token, head) rows of the sequence, 0 if its offsets are invalid
   bool ok;
   int piece;      // -1: the whole key range; otherwise the piece's slot in piece_o / piece_lse
 };
 
-// q-tiles holding rows of sequence b (0 when it has no rows in this call).
+// q-tiles holding rows of sequence b (0 when it has no rows in this call); with the 4-bit cache, of
+// (sequence, K/V head) b.
+template <bool kFour>
 __device__ __forceinline__ int seq_qtiles(const PrefillParams& p, int b) {
-  const SeqRows sr = seq_rows(p, b);
+  const SeqRows sr = seq_rows(p, kFour ? b / p.num_kv_heads : b);
   return sr.n > 0 ? (int)(((int64_t)sr.n * p.num_heads + kRows - 1) / kRows) : 0;
 }
 
@@ -355,6 +451,7 @@ __host__ __device__ inline WorkSplit work_split(int64_t total, int grid) {
 }
 
 // list: a varlen call's q-tile numbers (entry i for q-tile i - list_first), or null.
+template <bool kFour>
 __device__ __forceinline__ PItem prefill_item(const PrefillParams& p, int idx, const int32_t* list,
                                               const WorkSplit& ws, int list_first = 0) {
   PItem it;
@@ -370,8 +467,10 @@ __device__ __forceinline__ PItem prefill_item(const PrefillParams& p, int idx, c
   const int qt = list ? list[qti - list_first] : qti;
   it.b = qt / p.qtiles;
   it.row0 = (qt - it.b * p.qtiles) * (kQT * kRows);
-  const int32_t p0 = p.prefix_len[it.b];
-  const SeqRows sr = seq_rows(p, it.b);
+  const int seq = kFour ? it.b / p.num_kv_heads : it.b;
+  it.kvh = kFour ? it.b - seq * p.num_kv_heads : 0;
+  const int32_t p0 = p.prefix_len[seq];
+  const SeqRows sr = seq_rows(p, seq);
   it.qrow0 = sr.r0;
   it.rows = sr.n > 0 ? sr.n * p.num_heads : 0;
   it.ok = seq_ok(p, p0, sr.n) && it.row0 < it.rows;
@@ -411,8 +510,8 @@ __device__ __forceinline__ PItem prefill_item(const PrefillParams& p, int idx, c
 // the end of the item (channel half each).
 // kCompact: a varlen call's launch (p.compact): its items go through the item list.
 // Chunk calls compile without that path (its one branch per item cost them 2%).
-template <bool kCompact>
-__global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParams p) {
+template <bool kCompact, bool kFour>
+__global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ PrefillParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + kOffBars);
@@ -472,10 +571,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
     // (the dense numbering) when they do not fit.
     int32_t* hdr = reinterpret_cast<int32_t*>(smem + kOffTable);
     int32_t* list = hdr + 4;
-    const int per = (p.batch + 31) / 32;
-    const int b0 = min(p.batch, lane * per), b1 = min(p.batch, b0 + per);
+    const int nb = kFour ? p.batch * p.num_kv_heads : p.batch;
+    const int per = (nb + 31) / 32;
+    const int b0 = min(nb, lane * per), b1 = min(nb, b0 + per);
     int sum = 0;
-    for (int b = b0; b < b1; ++b) sum += seq_qtiles(p, b);
+    for (int b = b0; b < b1; ++b) sum += seq_qtiles<kFour>(p, b);
     int incl = sum;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -486,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
     if (total <= kMaxCompactItems) {
       int run = incl - sum;
       for (int b = b0; b < b1; ++b) {
-        const int n = seq_qtiles(p, b);
+        const int n = seq_qtiles<kFour>(p, b);
         for (int j = 0; j < n; ++j) list[run + j] = b * p.qtiles + j;
         run += n;
       }
@@ -519,7 +619,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
     if (lane == 0) {
       int g = 0, gk = 0, gv = 0;  // tiles; tiles whose K and V loads were issued (or dropped)
       for (int idx = blockIdx.x; idx < num_items && !*abort_flag; idx += gridDim.x) {
-        const PItem it = prefill_item(p, idx, table, ws);
+        const PItem it = prefill_item<kFour>(p, idx, table, ws);
         const int64_t seq_row0 = (int64_t)it.b * p.kt_rows;
         for (int j = 0; j < it.nkt; ++j, ++g) {
           const int sk = g % kStagesK, sv = g % kStagesV;
@@ -532,9 +632,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
           gk = g + 1;
           if (g >= kStagesV && !mbar_wait_polled(&v_empty[sv], ((g / kStagesV) - 1) & 1, wctl)) break;
           uint8_t* vs = smem + kOffV + sv * kVSlotBytes;
-          mbar_arrive_expect_tx(&v_full[sv], kVSlotBytes);
+          mbar_arrive_expect_tx(&v_full[sv], kFour ? kTileBytes : kVSlotBytes);
           bulk_g2s(vs, p.vh + row * kHeadDim, kTileBytes, &v_full[sv]);
-          bulk_g2s(vs + kTileBytes, p.ks + row, kKeys * 4, &v_full[sv]);
+          if constexpr (!kFour) bulk_g2s(vs + kTileBytes, p.ks + row, kKeys * 4, &v_full[sv]);
           gv = g + 1;
         }
       }
@@ -552,7 +652,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
     // the softmax has read S(g - 1) into registers, so it runs during that softmax's
     // exponentials; P has buffers of its own.
     if (lane == 0) {
-      constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys, 0, 0);
+      constexpr uint32_t idesc_s = kFour ? idesc_f16_f32(kRows, kKeys, 0, 0) : idesc_bf16_f32(kRows, kKeys, 0, 0);
       constexpr uint32_t idesc_o = idesc_f16_f32(kRows, kHeadDim, 0, 1);
       const bool s_issuer = warp == 1;
       // Descriptor bases; a K step adds 4096 bytes (S operands) or 256 bytes (V),
@@ -563,7 +663,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
       int g = 0, n = 0;
       bool ok = true;
       for (int idx = blockIdx.x; idx < num_items && ok && !*abort_flag; idx += gridDim.x) {
-        const PItem it = prefill_item(p, idx, table, ws);
+        const PItem it = prefill_item<kFour>(p, idx, table, ws);
         if (!it.ok || it.nkt == 0) continue;  // no MMA work; the softmax writes its zeros
         if (s_issuer) ok = mbar_wait_polled(q_full, n & 1, wctl);
         for (int j = 0; j < it.nkt && ok; ++j, ++g) {
@@ -622,15 +722,21 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
     bool ok = true;
     for (int idx = blockIdx.x; idx < num_items; idx += gridDim.x) {
       if (bar_red_or(kSoftBar, kSoftThreads, !ok || *abort_flag != 0)) break;
-      const PItem it = prefill_item(p, idx, table, ws);
+      const PItem it = prefill_item<kFour>(p, idx, table, ws);
       const int64_t row = it.row0 + r;  // (token, head) row within the sequence
       const bool my_row = row < it.rows;
       const int my_i = (int)(row >> p.log2_heads), my_h = (int)(row & (Hq - 1));
-      float* out_row = p.out + ((it.qrow0 + my_i) * Hq + my_h) * kHeadDim + h * 64;
+      // This row's place in q, out and lse_out.
+      const int64_t my_row_at = kFour ? (it.qrow0 + my_i) * p.q_heads + it.kvh * Hq + my_h : (it.qrow0 + my_i) * Hq + my_h;
+      float* out_row = p.out + my_row_at * kHeadDim + h * 64;  // (not used by the 4-bit cache)
+      uint16_t* out_row16 = p.out16 + my_row_at * kHeadDim + h * 64;
       if (!it.ok) {  // invalid sequence (flagged by the dequant pass): 0 / -inf; beyond the chunk: nothing
         if (my_row) {
-          for (int d = 0; d < 64; d += 4) *reinterpret_cast<float4*>(out_row + d) = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (h == 0 && p.lse_out) p.lse_out[(it.qrow0 + my_i) * Hq + my_h] = -INFINITY;
+          for (int d = 0; d < 64; d += 4) {
+            if constexpr (kFour) *reinterpret_cast<uint2*>(out_row16 + d) = make_uint2(0u, 0u);
+            else *reinterpret_cast<float4*>(out_row + d) = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          if (h == 0 && p.lse_out) p.lse_out[my_row_at] = -INFINITY;
         }
         continue;  // no MMA work for this item
       }
@@ -644,15 +750,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
       }
       // This row's query (bf16), zero beyond the chunk: each half writes 8 of its 16 chunks.
       {
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + (it.qrow0 * Hq + row) * kHeadDim);
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (kFour ? my_row_at : it.qrow0 * Hq + row) * kHeadDim);
 #pragma unroll
-        for (int c = 0; c < 8; ++c)
-          *reinterpret_cast<uint4*>(qs + (h * 8 + c) * 2048 + r * 16) = my_row ? src[h * 8 + c] : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < 8; ++c) {
+          uint4 x = my_row ? src[h * 8 + c] : make_uint4(0, 0, 0, 0);
+          if constexpr (kFour) {
+            uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = pack_f16x2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
+            x = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          *reinterpret_cast<uint4*>(qs + (h * 8 + c) * 2048 + r * 16) = x;
+        }
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
-      const int32_t p0 = p.prefix_len[it.b];
+      const int32_t p0 = p.prefix_len[kFour ? it.b / p.num_kv_heads : it.b];
       const int q_pos = p0 + my_i;
       const int k_lo = p.window > 0 ? max(0, q_pos + 1 - p.window) : 0;
       float m_ref = -INFINITY, l_sum = 0.0f;
@@ -681,8 +795,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
           const uint64_t nm2 = f2(-m_use, -m_use);
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            const float4 a = *reinterpret_cast<const float4*>(kscale + e);
-            const float4 a2 = *reinterpret_cast<const float4*>(kscale + 32 + e);
+            const float sl = p.scale_log2;
+            const float4 a = kFour ? make_float4(sl, sl, sl, sl) : *reinterpret_cast<const float4*>(kscale + e);
+            const float4 a2 = kFour ? a : *reinterpret_cast<const float4*>(kscale + 32 + e);
             if constexpr (!kCompact) {
               f2_split(f2_fma(f2(__uint_as_float(r0[e]), __uint_as_float(r0[e + 1])), f2(a.x, a.y), nm2), z[e],
                        z[e + 1]);
@@ -796,7 +911,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
         tc_fence_after();
         const float inv = Ls > 0.0f ? 1.0f / Ls : 0.0f;
         const float c0 = w0 * inv, c1 = w1 * inv;
-        float* dst = part_row ? part_row : out_row;
+        float* dst = kFour || part_row ? part_row : out_row;
 #pragma unroll
         for (int c = 0; c < 64; c += 32) {
           uint32_t o0[32], o1[32];
@@ -805,18 +920,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
           tmem_wait_ld();
           if (my_row) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<float4*>(dst + c + e) = make_float4(
+            for (int e = 0; e < 32; e += 4) {
+              const float4 x = make_float4(
                   fmaf(c0, __uint_as_float(o0[e]), c1 * __uint_as_float(o1[e])),
                   fmaf(c0, __uint_as_float(o0[e + 1]), c1 * __uint_as_float(o1[e + 1])),
                   fmaf(c0, __uint_as_float(o0[e + 2]), c1 * __uint_as_float(o1[e + 2])),
                   fmaf(c0, __uint_as_float(o0[e + 3]), c1 * __uint_as_float(o1[e + 3])));
+              if (kFour && !part_row)
+                *reinterpret_cast<uint2*>(out_row16 + c + e) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
+              else
+                *reinterpret_cast<float4*>(dst + c + e) = x;
+            }
           }
         }
         if (h == 0 && my_row) {
           const float lse2 = Ls > 0.0f ? M + __log2f(Ls) : -INFINITY;
           if (part_lse) *part_lse = lse2;
-          else if (p.lse_out) p.lse_out[(it.qrow0 + my_i) * Hq + my_h] = lse2 * kLn2;
+          else if (p.lse_out) p.lse_out[my_row_at] = lse2 * kLn2;
         }
         tc_fence_before();
         __syncwarp();
@@ -833,7 +953,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const PrefillParam
 
 // One warp per (split q-tile, row): merge the q-tile's pieces by their log-sum-exp,
 // out = sum_j 2^(lse_j - M) o_j / sum_j 2^(lse_j - M), into the row's output.
-__global__ void __launch_bounds__(256) combine_pieces_kernel(const PrefillParams p) {
+template <bool kFour>
+__global__ void __launch_bounds__(256) combine_pieces_kernel(const __grid_constant__ PrefillParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int64_t w = (blockIdx.x * (int64_t)blockDim.x + threadIdx.x) >> 5;
@@ -845,7 +966,7 @@ __global__ void __launch_bounds__(256) combine_pieces_kernel(const PrefillParams
   const int split_tiles = (ws.num - ws.full) / ws.pieces;
   if (w >= (int64_t)split_tiles * (kQT * kRows)) return;
   const int sp = (int)(w / (kQT * kRows)), r = (int)(w % (kQT * kRows));
-  const PItem it = prefill_item(p, ws.full + sp * ws.pieces, nullptr, ws);
+  const PItem it = prefill_item<kFour>(p, ws.full + sp * ws.pieces, nullptr, ws);
   const int64_t row = it.row0 + r;
   if (!it.ok || row >= it.rows) return;  // invalid sequence (its rows hold zeros) or past the chunk
   const int Hq = p.num_heads;
@@ -869,10 +990,15 @@ __global__ void __launch_bounds__(256) combine_pieces_kernel(const PrefillParams
     acc.w = fmaf(wt, o.w, acc.w);
   }
   const float inv = wsum > 0.0f ? 1.0f / wsum : 0.0f;
-  reinterpret_cast<float4*>(p.out + ((it.qrow0 + my_i) * Hq + my_h) * kHeadDim)[lane] =
-      make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+  const int64_t at = kFour ? (it.qrow0 + my_i) * p.q_heads + it.kvh * Hq + my_h : (it.qrow0 + my_i) * Hq + my_h;
+  if constexpr (kFour)
+    reinterpret_cast<uint2*>(p.out16 + at * kHeadDim)[lane] =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+  else
+    reinterpret_cast<float4*>(p.out + at * kHeadDim)[lane] =
+        make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
   if (p.lse_out && lane == 0)
-    p.lse_out[(it.qrow0 + my_i) * Hq + my_h] = wsum > 0.0f ? (M + __log2f(wsum)) * kLn2 : -INFINITY;
+    p.lse_out[at] = wsum > 0.0f ? (M + __log2f(wsum)) * kLn2 : -INFINITY;
 }
 
 }  // namespace
@@ -905,6 +1031,60 @@ void prefill_piece_region(void* workspace, int32_t batch, int32_t max_pages_per_
   *bytes = (size_t)(((piece_bytes() + 255) / 256) * 256);
 }
 
+namespace {
+
+template <bool kFour>
+cudaError_t launch_kernels(PrefillParams p, cudaStream_t stream) {
+  const int64_t seqs = (int64_t)p.batch * p.num_kv_heads;
+  const int64_t dq_blocks = seqs * (p.kt_rows / kKeys);
+  if (dq_blocks > 0 && p.q_off && p.batch <= kMaxCompactSeqs)
+    dequant_compact_kernel<kFour><<<dim3((unsigned)std::min<int64_t>(dq_blocks, 4 * (int64_t)num_sms())), 256,
+                                    (p.batch + 1) * 4, stream>>>(p);
+  else if (dq_blocks > 0)
+    dequant_kernel<kFour><<<dim3((unsigned)(p.kt_rows / kKeys), (unsigned)p.batch, (unsigned)p.num_kv_heads), 256, 0,
+                            stream>>>(p);
+  cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev < 64 && !attr_set[dev]) {
+    // The register split inside the kernel assumes the launch register count.
+    cudaFuncAttributes fa;
+    for (const void* fn : {(const void*)prefill_kernel<false, kFour>, (const void*)prefill_kernel<true, kFour>}) {
+      e = cudaFuncGetAttributes(&fa, fn);
+      if (e != cudaSuccess) return e;
+      if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidDeviceFunction;
+      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytesMax);
+      if (e != cudaSuccess) return e;
+    }
+    attr_set[dev] = true;
+  }
+  // Work split (work_split) of a chunk call's q-tiles.  A varlen call's q-tiles are
+  // counted on the device (whole, no pieces); the dense count here is the fallback when
+  // they are too many to list.
+  const int64_t qtiles_total = seqs * p.qtiles;
+  const int sms = num_sms();
+  const int grid = (int)(qtiles_total < sms ? qtiles_total : sms);
+  WorkSplit split = work_split(qtiles_total, grid);
+  if (p.compact) split = WorkSplit{(int)qtiles_total, 1, (int)qtiles_total};
+  p.pieces = split.pieces;
+  p.full_items = split.full;
+  p.num_items = split.num;
+  const int smem = p.compact ? kSmemBytesMax : kSmemBytes;
+  if (p.compact)
+    prefill_kernel<true, kFour><<<grid, kThreads, smem, stream>>>(p);
+  else
+    prefill_kernel<false, kFour><<<grid, kThreads, smem, stream>>>(p);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || split.pieces == 1) return e;
+  const int64_t warps_c = (int64_t)(split.num - split.full) / split.pieces * kRows;  // one warp per row
+  return launch_pdl(combine_pieces_kernel<kFour>, dim3((unsigned)((warps_c + 7) / 8)), dim3(256), 0, stream, p);
+}
+
+}  // namespace
+
 cudaError_t launch_prefill(const PrefillLaunch& L, cudaStream_t stream) {
   PrefillParams p;
   p.pages = L.pages;
@@ -928,7 +1108,15 @@ cudaError_t launch_prefill(const PrefillLaunch& L, cudaStream_t stream) {
   p.scale_log2 = L.scale_log2;
   p.wait_ns = wait_limit_ns();
   p.drop_stage = fault_drop_stage();
-  const int64_t rows = (int64_t)L.batch * p.kt_rows;
+  p.num_kv_heads = L.four ? L.num_kv_heads : 1;
+  p.q_heads = L.four ? L.q_heads : L.num_heads;
+  p.out16 = L.out16;
+  for (int j = 0; j < kMaxKvHeads; ++j) {
+    p.pages4[j] = L.four && j < L.num_kv_heads ? L.pages4[j] : nullptr;
+    p.num_pages4[j] = L.four && j < L.num_kv_heads ? L.num_pages4[j] : 0;
+  }
+  const int64_t seqs = (int64_t)L.batch * p.num_kv_heads;  // copies: one per (sequence, K/V head)
+  const int64_t rows = seqs * p.kt_rows;
   const int64_t a = ((rows * kHeadDim * 2 + 255) / 256) * 256;
   uint8_t* ws = static_cast<uint8_t*>(L.workspace);
   p.kb = reinterpret_cast<uint16_t*>(ws);
@@ -940,51 +1128,7 @@ cudaError_t launch_prefill(const PrefillLaunch& L, cudaStream_t stream) {
   p.out = L.out;
   p.lse_out = L.lse_out;
   p.err = L.err;
-
-  const int64_t dq_blocks = (int64_t)L.batch * (p.kt_rows / kKeys);
-  if (dq_blocks > 0 && L.q_off && L.batch <= kMaxCompactSeqs)
-    dequant_compact_kernel<<<dim3((unsigned)std::min<int64_t>(dq_blocks, 4 * (int64_t)num_sms())), 256,
-                             (L.batch + 1) * 4, stream>>>(p);
-  else if (dq_blocks > 0)
-    dequant_kernel<<<dim3((unsigned)(p.kt_rows / kKeys), (unsigned)L.batch), 256, 0, stream>>>(p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-
-  static bool attr_set[64] = {};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 64 && !attr_set[dev]) {
-    // The register split inside the kernel assumes the launch register count.
-    cudaFuncAttributes fa;
-    for (const void* fn : {(const void*)prefill_kernel<false>, (const void*)prefill_kernel<true>}) {
-      e = cudaFuncGetAttributes(&fa, fn);
-      if (e != cudaSuccess) return e;
-      if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidDeviceFunction;
-      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytesMax);
-      if (e != cudaSuccess) return e;
-    }
-    attr_set[dev] = true;
-  }
-  // Work split (work_split) of a chunk call's q-tiles.  A varlen call's q-tiles are
-  // counted on the device (whole, no pieces); the dense count here is the fallback when
-  // they are too many to list.
-  const int64_t qtiles_total = (int64_t)L.batch * p.qtiles;
-  const int sms = num_sms();
-  const int grid = (int)(qtiles_total < sms ? qtiles_total : sms);
-  WorkSplit split = work_split(qtiles_total, grid);
-  if (p.compact) split = WorkSplit{(int)qtiles_total, 1, (int)qtiles_total};
-  p.pieces = split.pieces;
-  p.full_items = split.full;
-  p.num_items = split.num;
-  const int smem = p.compact ? kSmemBytesMax : kSmemBytes;
-  if (p.compact)
-    prefill_kernel<true><<<grid, kThreads, smem, stream>>>(p);
-  else
-    prefill_kernel<false><<<grid, kThreads, smem, stream>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess || split.pieces == 1) return e;
-  const int64_t warps_c = (int64_t)(split.num - split.full) / split.pieces * kRows;  // one warp per row
-  return launch_pdl(combine_pieces_kernel, dim3((unsigned)((warps_c + 7) / 8)), dim3(256), 0, stream, p);
+  return L.four ? launch_kernels<true>(p, stream) : launch_kernels<false>(p, stream);
 }
 
 }  // namespace cai
