@@ -295,7 +295,8 @@ cai_status cai_mqa_prefill_varlen(const cai_kv_pool* pool, const uint16_t* q, in
  * owning rows [b * n_new, (b + 1) * n_new); total_new is not read), or packed as in
  * cai_mqa_prefill_varlen: sequence b owns rows [q_offsets[b], q_offsets[b + 1]) of
  * total_new, at most n_new of them.  A sequence whose offsets are out of order, beyond
- * total_new or longer than n_new sets CAI_DEVERR_LENGTH and none of its rows is touched.
+ * total_new or longer than n_new sets CAI_DEVERR_LENGTH and none of its rows is touched
+ * (the appends may then leave out rows of other sequences, too).
  *
  * The 4-bit cache holds a token's K (and V) as 128 4-bit codes and four scales, one
  * per 32 channels: s = fp16(bf16(max |x| / 7)) (both roundings to nearest even, the

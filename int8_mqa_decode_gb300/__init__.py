@@ -180,7 +180,8 @@ def _check(status: int, where: str) -> None:
 
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # torch.cuda.current_stream().cuda_stream without the Stream object (several microseconds a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -189,11 +190,11 @@ def _ptr(t: Optional[torch.Tensor], name: str, dtype=None, shape=None) -> Option
         return None
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
-    if dtype is not None and t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
+    if dtype is not None and t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:  # (torch.Size is a tuple)
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     return t.data_ptr()
 
@@ -535,92 +536,92 @@ _DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
 def _pools_of(pools, kind):
-    pools = list(pools) if isinstance(pools, (list, tuple)) else [pools]
+    if isinstance(pools, kind):
+        return ctypes.byref(pools.struct), 1
     for p in pools:
         if not isinstance(p, kind):
             raise TypeError(f"pools must be {kind.__name__} objects, got {type(p).__name__}")
+    n = len(pools)
+    if n == 1:
+        return ctypes.byref(pools[0].struct), 1
     struct = cai_kv_pool if kind is KVPool else cai_kv4_pool
-    return (struct * len(pools))(*[p.struct for p in pools]), len(pools)
+    return (struct * n)(*[p.struct for p in pools]), n
 
 
-def _rows_shape(t: torch.Tensor, packed: bool, name: str):
-    """(rows, batch or None, n_new or None, heads) of new-token rows: [rows][heads][128] packed,
-    [batch][n_new][heads][128] otherwise."""
-    if t.dim() != (3 if packed else 4) or t.shape[-1] != HEAD_DIM:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected "
-                         + ("[rows][heads][128] with q_offsets" if packed else "[batch][n_new][heads][128]"))
-    if packed:
-        return t.shape[0], None, None, t.shape[1]
-    return t.shape[0] * t.shape[1], t.shape[0], t.shape[1], t.shape[2]
+def _rows(t: torch.Tensor, name: str, q_offsets, max_new, start_pos: torch.Tensor):
+    """(rows, batch, n_new, heads) of a call whose new-token rows are those of t: [rows][heads][128] packed by
+    q_offsets, [batch][n_new][heads][128] otherwise."""
+    n = t.shape
+    if q_offsets is None:
+        if len(n) != 4 or n[3] != HEAD_DIM:
+            raise ValueError(f"{name} has shape {tuple(n)}, expected [batch][n_new][heads][{HEAD_DIM}]")
+        if max_new is not None:
+            raise ValueError("max_new goes with q_offsets")
+        return n[0] * n[1], n[0], n[1], n[2]
+    if len(n) != 3 or n[2] != HEAD_DIM:
+        raise ValueError(f"{name} has shape {tuple(n)}, expected [rows][heads][{HEAD_DIM}] with q_offsets")
+    if max_new is None:
+        raise ValueError("packed rows (q_offsets) need max_new")
+    batch = start_pos.shape[0]
+    _ptr(q_offsets, "q_offsets", torch.int32, (batch + 1,))
+    return n[0], batch, int(max_new), n[1]
 
 
 def _row_stride(t: torch.Tensor, name: str) -> int:
-    """Elements between rows of [..rows..][heads][128] whose heads are contiguous."""
-    s, n = t.stride(), t.shape
-    if t.numel() == 0:
-        return n[-2] * HEAD_DIM
+    """Elements between the rows of [..rows..][heads][128]: the heads of a row are contiguous, rows equally spaced."""
+    n = t.shape
+    width = n[-2] * HEAD_DIM
+    if t.is_contiguous():
+        return width
+    s = t.stride()
     ok = s[-1] == 1 and (n[-2] == 1 or s[-2] == HEAD_DIM)
-    if t.dim() == 4 and n[0] > 1 and n[1] > 1:
-        ok = ok and s[0] == n[1] * s[1]
+    if len(n) == 3:
+        step = s[0]
+    else:
+        step = s[0] if n[1] == 1 else s[1]
+        ok = ok and (n[0] == 1 or n[1] == 1 or s[0] == n[1] * s[1])
     if not ok:
         raise ValueError(f"{name}: the heads of a row must be contiguous and rows equally spaced")
-    rows = n[0] * n[1] if t.dim() == 4 else n[0]
-    if rows == 1:
-        return n[-2] * HEAD_DIM
-    return s[0] if t.dim() == 3 or n[1] == 1 else s[1]
+    return width if (n[0] if len(n) == 3 else n[0] * n[1]) == 1 else step
 
 
-def _cuda(t: Optional[torch.Tensor], name: str) -> Optional[int]:
-    if t is None:
-        return None
+def _cuda(t: torch.Tensor, name: str) -> int:
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     return t.data_ptr()
 
 
 def _table(block_table: torch.Tensor, batch: int):
-    if block_table.dim() != 2 or block_table.shape[0] != batch:
-        raise ValueError(f"block_table has shape {tuple(block_table.shape)}, expected [{batch}][max_pages]")
-    return _ptr(block_table, "block_table", torch.int32), block_table.shape[1]
-
-
-def _packing(t: torch.Tensor, name: str, q_offsets, max_new, start_pos: torch.Tensor):
-    """(rows, batch, n_new, heads) of a call whose rows are those of t."""
-    rows, batch, n_new, heads = _rows_shape(t, q_offsets is not None, name)
-    if q_offsets is not None:
-        if max_new is None:
-            raise ValueError("packed rows (q_offsets) need max_new")
-        batch, n_new = start_pos.shape[0], int(max_new)
-        _ptr(q_offsets, "q_offsets", torch.int32, (batch + 1,))
-    elif max_new is not None:
-        raise ValueError("max_new goes with q_offsets")
-    return rows, batch, n_new, heads
+    n = block_table.shape
+    if len(n) != 2 or n[0] != batch:
+        raise ValueError(f"block_table has shape {tuple(n)}, expected [{batch}][max_pages]")
+    return _ptr(block_table, "block_table", torch.int32), n[1]
 
 
 def _append_rows(entry: str, kind, pools, k_new, v_new, block_table, start_pos, rope, q, q_out, q_offsets, max_new,
                  err_flag, stream) -> None:
     arr, hkv = _pools_of(pools, kind)
-    rows, batch, n_new, heads = _packing(k_new, "k_new", q_offsets, max_new, start_pos)
+    rows, batch, n_new, heads = _rows(k_new, "k_new", q_offsets, max_new, start_pos)
     if heads != hkv or v_new.shape != k_new.shape:
         raise ValueError(f"k_new and v_new must have one shape with {hkv} heads, got {tuple(k_new.shape)} and "
                          f"{tuple(v_new.shape)}")
-    if k_new.dtype not in _DTYPES or v_new.dtype != k_new.dtype:
+    kv_type = _DTYPES.get(k_new.dtype)
+    if kv_type is None or v_new.dtype != k_new.dtype:
         raise TypeError(f"k_new and v_new must both be fp32 or bf16, got {k_new.dtype} and {v_new.dtype}")
-    if (q is None) != (q_out is None):
-        raise ValueError("q and q_out go together")
-    hq, q_stride = 0, 0
-    if q is not None:
-        q_rows, _, _, hq = _rows_shape(q, q_offsets is not None, "q")
-        if q_rows != rows or q_out.shape != q.shape or q.dtype != torch.bfloat16:
-            raise ValueError("q must be bf16 with the rows of k_new, and q_out of its shape")
-        q_stride = _row_stride(q, "q")
+    hq, q_stride, q_ptr, out_ptr = 0, 0, None, None
+    if q is not None or q_out is not None:
+        if q is None or q_out is None:
+            raise ValueError("q and q_out go together")
+        if q.dim() != k_new.dim() or q.shape[:-2] != k_new.shape[:-2] or q.shape[-1] != HEAD_DIM or q.dtype != torch.bfloat16:
+            raise ValueError("q must be bf16, with the rows of k_new")
+        hq, q_stride, q_ptr = q.shape[-2], _row_stride(q, "q"), _cuda(q, "q")
+        out_ptr = _ptr(q_out, "q_out", torch.bfloat16, q.shape)
     table, width = _table(block_table, batch)
     st = getattr(load(), entry)(
         arr, hkv, ctypes.byref(rope.struct) if rope is not None else None, _cuda(k_new, "k_new"), _cuda(v_new, "v_new"),
-        _DTYPES[k_new.dtype], _row_stride(k_new, "k_new"), _row_stride(v_new, "v_new"), _cuda(q, "q"), q_stride,
-        _ptr(q_out, "q_out", torch.bfloat16), hq, batch, n_new, q_offsets.data_ptr() if q_offsets is not None else None,
-        rows, table, width, _ptr(start_pos, "start_pos", torch.int32, (batch,)),
-        _ptr(err_flag, "err_flag", torch.int32), _stream(stream))
+        kv_type, _row_stride(k_new, "k_new"), _row_stride(v_new, "v_new"), q_ptr, q_stride, out_ptr, hq, batch, n_new,
+        q_offsets.data_ptr() if q_offsets is not None else None, rows, table, width,
+        _ptr(start_pos, "start_pos", torch.int32, (batch,)), _ptr(err_flag, "err_flag", torch.int32), _stream(stream))
     _check(st, entry)
 
 
@@ -650,7 +651,7 @@ def _read_rows(entry: str, kind, pools, k_out, v_out, block_table, start_pos, q_
     one = k_out if k_out is not None else v_out
     if one is None:
         raise ValueError("one of k_out and v_out must be given")
-    rows, batch, n_new, heads = _packing(one, "k_out", q_offsets, max_new, start_pos)
+    rows, batch, n_new, heads = _rows(one, "k_out", q_offsets, max_new, start_pos)
     if heads != hkv or (k_out is not None and v_out is not None and (v_out.shape != k_out.shape or v_out.dtype != k_out.dtype)):
         raise ValueError(f"k_out and v_out must have one shape and dtype, with {hkv} heads")
     if one.dtype not in _DTYPES:
@@ -713,13 +714,13 @@ def cai_kv4_prefill(pools: Sequence[KV4Pool], q: torch.Tensor, block_table: torc
     """Attention of appended new tokens over the 4-bit cache: q bf16 [batch][n_new][Hq][128], or packed
     [rows][Hq][128] with q_offsets and max_new -> out bf16 of the same shape, lse_out without the last dimension."""
     arr, hkv = _pools_of(pools, KV4Pool)
-    rows, batch, n_new, hq = _packing(q, "q", q_offsets, max_new, prefix_len)
+    rows, batch, n_new, hq = _rows(q, "q", q_offsets, max_new, prefix_len)
     table, width = _table(block_table, batch)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     st = load().cai_kv4_prefill(
         arr, hkv, _ptr(q, "q", torch.bfloat16), batch, n_new, q_offsets.data_ptr() if q_offsets is not None else None,
         rows, hq, table, width, _ptr(prefix_len, "prefix_len", torch.int32, (batch,)), window, float(softmax_scale),
-        _ptr(workspace, "workspace"), ws_bytes, _ptr(out, "out", torch.bfloat16, tuple(q.shape)),
-        _ptr(lse_out, "lse_out", torch.float32, tuple(q.shape[:-1])), _ptr(err_flag, "err_flag", torch.int32),
+        _ptr(workspace, "workspace"), ws_bytes, _ptr(out, "out", torch.bfloat16, q.shape),
+        _ptr(lse_out, "lse_out", torch.float32, q.shape[:-1]), _ptr(err_flag, "err_flag", torch.int32),
         _stream(stream))
     _check(st, "cai_kv4_prefill")

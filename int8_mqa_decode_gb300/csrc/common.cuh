@@ -125,6 +125,9 @@ struct AppendRowsParams {
   const float* sin;
   int32_t num_positions, rot, interleaved;  // rot 0: no rotation
   int32_t* err;
+  // Filled by the launch: blocks that write K/V (by `groups` groups of 16 positions per sequence, or by rows
+  // when 0), then blocks that rotate queries; whether the tables are 16-byte aligned.
+  int32_t kv_blocks, groups, q_blocks, wide_tables;
 };
 
 struct ReadRowsParams {
@@ -236,7 +239,7 @@ cai_status cuda_status(cudaError_t e);
 // Kernel launchers (return cudaGetLastError()).
 cudaError_t launch_append(const AppendParams* ps, int n, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeParams& p, int page_size, cudaStream_t stream);
-cudaError_t launch_append_rows(const AppendRowsParams& p, bool four, bool bf16, cudaStream_t stream);
+cudaError_t launch_append_rows(AppendRowsParams p, bool four, bool bf16, cudaStream_t stream);
 cudaError_t launch_read_rows(const ReadRowsParams& p, bool four, bool bf16, cudaStream_t stream);
 cudaError_t launch_decode4(const Decode4Params& p, cudaStream_t stream);
 // Fills the split fields of p (batch, heads, page_size, max_pages and window given; num_splits 0: automatic) and

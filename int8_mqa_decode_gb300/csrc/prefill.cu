@@ -331,9 +331,7 @@ __device__ __forceinline__ void dequant_tile4(const PrefillParams& p, int b, int
     values_f16(w[m], s0[j], s1[j], x);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {  // channels 16 m + 8 (i % 2) .. + 7 of keys 8 (i / 2) .. + 7
-      uint32_t y;
-      asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x[i]));
-      *reinterpret_cast<uint32_t*>(vt + (2 * m + (i & 1)) * 1024 + ((i >> 1) * 8 + g) * 8 + 2 * t) = y;
+      *reinterpret_cast<uint32_t*>(vt + (2 * m + (i & 1)) * 1024 + ((i >> 1) * 8 + g) * 8 + 2 * t) = transpose8x8(x[i]);
     }
   }
 }

@@ -278,6 +278,20 @@ def test_read_gives_back_what_the_cache_stands_for(four, i):
         assert torch.equal(only, v)
 
 
+def test_read_into_outputs_of_odd_alignment():
+    """16-byte aligned outputs, not 32: the same values, and nothing around them."""
+    pools, table, new, start, kr, _ = append_case(True, APPENDS[1], True, seed=3)
+    kw = dict(q_offsets=dev(np.concatenate([[0], np.cumsum(new)]).astype(np.int32)), max_new=int(new.max()))
+    n = kr.shape[0] * kr.shape[1] * 128
+    for dt, pad in ((torch.float32, 4), (torch.bfloat16, 8)):
+        room = torch.full((n + 2 * pad,), 9.0, dtype=dt, device=DEV)
+        k = room[pad:-pad].view(kr.shape)
+        cai.cai_kv4_read(pools, k, None, table, dev(start.astype(np.int32)), **kw)
+        want = kv4.dequantize4(*kv4.quantize4(kr)).astype(np.float32)
+        assert np.array_equal(host(k), want if dt == torch.float32 else kv4.bf16_round(want))
+        assert (room[:pad] == 9).all() and (room[-pad:] == 9).all()
+
+
 @pytest.mark.parametrize("four", [False, True])
 def test_read_bad_rows_are_zero(four):
     cls, bytes_ = (cai.KV4Pool, 2304) if four else (cai.KVPool, 4224)
