@@ -158,9 +158,10 @@ struct Decode4Params {
   float* lse_out;          // natural log, nullable
   // Work split (plan_decode4).  chunk 0: the keys of all sequences and K/V heads, in tiles of 128, are
   // cut into `ranges` equal parts, one per block; piece of block c: slot 2 c + 1 where it holds a
-  // sequence's first tile, 2 c otherwise; meta[b * num_kv_heads + K/V head] = {first block, last block}.
+  // sequence's first tile, 2 c otherwise; meta[c] = {b * num_kv_heads + K/V head, last block} of what starts in
+  // block c and goes on in the next, {-1, -1} if nothing does.  A sequence counts piece_tiles more than it has.
   // chunk > 0: every sequence is cut into `splits` ranges of chunk keys; slot (unit * splits + range).
-  int32_t head_groups, ranges, chunk, splits;
+  int32_t head_groups, ranges, chunk, splits, piece_tiles;
   int2* meta;
   float* ws_o;             // [slot][query heads of a K/V head][128] normalised partial outputs
   float* ws_lse;           // [slot][query heads of a K/V head] log2 units

@@ -119,6 +119,29 @@ __device__ __forceinline__ bool mbar_wait_abortable(uint64_t* bar, uint32_t pari
   }
 }
 
+// The same with fewer instructions per try: a try returns after about 100 cycles, whatever its hint, and
+// where a dozen warps of an SM wait at a time the checks of the limit after every try took a quarter of
+// its issue slots.  Here they come after 64 tries (of at most 2 us each).
+__device__ __forceinline__ bool mbar_wait_lean(uint64_t* bar, uint32_t parity, volatile WaitState* w) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = 0;
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait_suspend(bar, parity, 2000u)) return true;
+    if (w->abort) return false;
+    const uint64_t t = globaltimer_ns();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > w->limit_ns) {
+      w->abort = 1;
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ bool mbar_wait_lean_warp(uint64_t* bar, uint32_t parity, volatile WaitState* w) {
+  return __all_sync(0xffffffffu, mbar_wait_lean(bar, parity, w));
+}
+
 // As mbar_wait_abortable, polling without blocking for a few tries first: a thread
 // suspended by a blocking try resumes a few hundred cycles after the phase completes,
 // which the waits of a ~2.5k-cycle pipeline period cannot afford (measured: 64 tries
