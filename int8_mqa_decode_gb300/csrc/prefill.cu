@@ -63,19 +63,21 @@ constexpr int kOffXch = kOffV + kStagesV * kVSlotBytes;      // softmax exchange
 constexpr int kOffBars = kOffXch + 4 * kRows * 4;
 // k_full, k_empty [kStagesK]; v_full, v_empty [kStagesV]; q_full; s_full, s_read;
 // p_full [2 key halves][kPBuf]; pv_done [kPBuf] (one per P buffer); o_full, o_empty;
-// the MMA issuers' last commits.
-constexpr int kNumBars = 2 * kStagesK + 2 * kStagesV + 1 + 2 + 3 * kPBuf + 2 + 1;
+// the MMA issuers' last commits; item_full, item_empty [kItemSlots].
+constexpr int kItemSlots = 4;
+constexpr int kNumBars = 2 * kStagesK + 2 * kStagesV + 1 + 2 + 3 * kPBuf + 2 + 1 + 2 * kItemSlots;
 constexpr int kOffMisc = kOffBars + 8 * kNumBars;
 // Varlen dequant: sequences whose tiles one block numbers in shared memory.
 constexpr int kMaxCompactSeqs = 8192;
 // A varlen call's item list (see PrefillParams::compact): its count, then the dense
 // q-tile number of each item, in shared memory that only such a launch asks for.
 constexpr int kMaxCompactItems = 4096;
-constexpr int kOffTable = kOffMisc + 32;  // after the tmem slot and the wait state (+8)
+constexpr int kOffItems = (kOffMisc + 32 + 15) & ~15;  // after the tmem slot and the wait state (+8): items, 64 bytes each
+constexpr int kOffTable = kOffItems + kItemSlots * 64;
 constexpr int kSmemBytes = kOffTable + 1024;  // without the list; ... and alignment slack
 constexpr int kSmemBytesMax = kSmemBytes + (kMaxCompactItems + 4) * 4;
 static_assert(kOffXch % 16 == 0 && kOffBars % 8 == 0, "shared-memory layout");
-// Warpgroup 0: K/V producer (warp 0), S issuer (warp 1), PV issuer (warp 2), a spare warp;
+// Warpgroup 0: K/V producer (warp 0), S issuer (warp 1), PV issuer (warp 2), items (warp 3);
 // warpgroups 1 and 2: the softmax, key half 0 and key half 1 of every row.  The block
 // is launched with 168 registers per thread (384 threads; 3 warps x 32 x 168 =
 // 16128 of a sub-partition's 16384), then warpgroup 0 shrinks to 72 and the
@@ -448,6 +450,13 @@ __host__ __device__ inline WorkSplit work_split(int64_t total, int grid) {
   return w;
 }
 
+// (token, head) row `row` of an item's sequence, as a row of q, out and lse_out.
+template <bool kFour>
+__device__ __forceinline__ int64_t q_row(const PrefillParams& p, const PItem& it, int64_t row) {
+  return kFour ? (it.qrow0 + (row >> p.log2_heads)) * p.q_heads + it.kvh * p.num_heads + (row & (p.num_heads - 1))
+               : it.qrow0 * p.num_heads + row;
+}
+
 // list: a varlen call's q-tile numbers (entry i for q-tile i - list_first), or null.
 template <bool kFour>
 __device__ __forceinline__ PItem prefill_item(const PrefillParams& p, int idx, const int32_t* list,
@@ -491,6 +500,27 @@ __device__ __forceinline__ PItem prefill_item(const PrefillParams& p, int idx, c
   return it;
 }
 
+// Rows of 8 units of 16 bytes, one per lane: lane q of 8 leaves with unit q of the 8 rows, so that a store of
+// the 8 lanes covers a whole 128-byte line (32 lines an instruction, a row per lane, took the epilogue
+// 4300 cycles; so they take 1/8).
+__device__ __forceinline__ void transpose_units(uint4 (&x)[8], int q) {
+#pragma unroll
+  for (int m = 4; m >= 1; m >>= 1) {
+    const bool up = (q & m) != 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (i & m) continue;
+      uint4& a = x[i];
+      uint4& b = x[i | m];
+      const uint4 send = up ? a : b;
+      const uint4 r = make_uint4(__shfl_xor_sync(0xffffffffu, send.x, m), __shfl_xor_sync(0xffffffffu, send.y, m),
+                                 __shfl_xor_sync(0xffffffffu, send.z, m), __shfl_xor_sync(0xffffffffu, send.w, m));
+      if (up) a = r;
+      else b = r;
+    }
+  }
+}
+
 // Operand tiles in shared memory: element (r, k) of a 128x128 16-bit tile at
 // (k/8)*2048 + r*16 + (k%8)*2 -- the order in which the dequant pass writes each
 // tile of its copy, so one bulk copy lands it.  As a K-major operand: LBO = 2048
@@ -525,14 +555,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   uint64_t* o_full = pv_done + kPBuf;          // PV issuer commit after an item's last PVs
   uint64_t* o_empty = o_full + 1;              // softmax -> PV issuer after reading O (8 warps)
   uint64_t* mma_drain = o_empty + 1;           // the MMA issuers' last commits, at exit
+  uint64_t* item_full = mma_drain + 1;         // [kItemSlots] warp 3 -> the other roles
+  uint64_t* item_empty = item_full + kItemSlots;  // [kItemSlots] the other roles (11 warps) -> warp 3
+  PItem* items = reinterpret_cast<PItem*>(smem + kOffItems);
   float* xref = reinterpret_cast<float*>(smem + kOffXch);  // [2 halves][128 rows] half-row references
   float* xsum = xref + 2 * kRows;                          // [2 halves][128 rows] half-row sums
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kOffMisc);
   volatile WaitState* const wctl = reinterpret_cast<volatile WaitState*>(smem + kOffMisc + 8);
   volatile int32_t* abort_flag = &wctl->abort;
 
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int Hq = p.num_heads;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   constexpr uint32_t kColP = 128;  // P buffer b at kColP + b * 64 (key half h in its 32 columns at + h * 32); S at 0
   constexpr uint32_t kColO = 256;  // O of key half h at kColO + h * 128
   constexpr uint32_t kSoftBar = 1;
@@ -559,6 +591,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     mbar_init(o_full, 1);
     mbar_init(o_empty, 8);
     mbar_init(mma_drain, 2);
+    for (int k = 0; k < kItemSlots; ++k) {
+      mbar_init(&item_full[k], 1);
+      mbar_init(&item_empty[k], 11);
+    }
     *abort_flag = 0;
     wctl->limit_ns = p.wait_ns;
     fence_barrier_init();
@@ -594,7 +630,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   // A varlen call's decode launch, next in the stream, shares no memory with this grid:
   // it may start now, its CTAs taking the SMs that this grid's CTAs leave.  (Chunk calls
   // do not trigger early: measured 3.6% slower on the append-prefill workload.)
@@ -609,6 +645,23 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   ws.pieces = p.pieces;
   ws.num = n_list >= 0 ? n_list : p.num_items;
   const int num_items = ws.num;
+  // The block's i-th item (chunk calls: item i), for a warp or, `one`, for the producer's one lane; `up` false:
+  // the wait gave up.  The many short items of a varlen call come from warp 3 (7% faster there); chunk calls'
+  // roles work out their few for themselves (5% faster than going through the slots).
+  auto get_item = [&](int i, bool one, bool& up) -> PItem {
+    if constexpr (!kCompact) {
+      up = true;
+      return prefill_item<kFour>(p, i, table, ws);
+    }
+    const int s = i % kItemSlots;
+    PItem it = {};
+    up = one ? mbar_wait_lean(&item_full[s], (i / kItemSlots) & 1, wctl) : mbar_wait_lean_warp(&item_full[s], (i / kItemSlots) & 1, wctl);
+    if (!up) return it;
+    it = items[s];
+    if (!one) __syncwarp();
+    if (one || lane == 0) mbar_arrive(&item_empty[s]);
+    return it;
+  };
 
   if (warp < 4) {
    setmaxnreg_dec<kRegsCtl>();
@@ -616,8 +669,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     // ------------------------------------------------------------ K/V producer
     if (lane == 0) {
       int g = 0, gk = 0, gv = 0;  // tiles; tiles whose K and V loads were issued (or dropped)
-      for (int idx = blockIdx.x; idx < num_items && !*abort_flag; idx += gridDim.x) {
-        const PItem it = prefill_item<kFour>(p, idx, table, ws);
+      bool up = true;
+      for (int idx = blockIdx.x, i = 0; idx < num_items && !*abort_flag; idx += gridDim.x, ++i) {
+        const PItem it = get_item(kCompact ? i : idx, true, up);
+        if (!up) break;
         const int64_t seq_row0 = (int64_t)it.b * p.kt_rows;
         for (int j = 0; j < it.nkt; ++j, ++g) {
           const int sk = g % kStagesK, sv = g % kStagesV;
@@ -644,12 +699,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     }
    } else if (warp == 1 || warp == 2) {
     // ------------------------------------------------------------ MMA issuers
-    // Warp 1 issues S = Q K^T, warp 2 issues O += P V: one thread issues a
-    // 128 x 128 x 16 MMA only about every 115 cycles (measured; the tensor core takes
-    // about 64), so the two streams go out from two threads.  S(g) overwrites S once
-    // the softmax has read S(g - 1) into registers, so it runs during that softmax's
-    // exponentials; P has buffers of its own.
-    if (lane == 0) {
+    // Warp 1 issues S = Q K^T, warp 2 issues O += P V, so neither waits for the other's
+    // operands.  S(g) overwrites S once the softmax has read S(g - 1) into registers, so
+    // it runs during that softmax's exponentials; P has buffers of its own.
+    {
       constexpr uint32_t idesc_s = kFour ? idesc_f16_f32(kRows, kKeys, 0, 0) : idesc_bf16_f32(kRows, kKeys, 0, 0);
       constexpr uint32_t idesc_o = idesc_f16_f32(kRows, kHeadDim, 0, 1);
       const bool s_issuer = warp == 1;
@@ -660,48 +713,76 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const uint64_t dv0 = smem_desc(smem_addr(smem + kOffV), 128, 2048);
       int g = 0, n = 0;
       bool ok = true;
-      for (int idx = blockIdx.x; idx < num_items && ok && !*abort_flag; idx += gridDim.x) {
-        const PItem it = prefill_item<kFour>(p, idx, table, ws);
+      for (int idx = blockIdx.x, i = 0; idx < num_items && ok && !abort_seen_warp(wctl); idx += gridDim.x, ++i) {
+        const PItem it = get_item(kCompact ? i : idx, false, ok);
         if (!it.ok || it.nkt == 0) continue;  // no MMA work; the softmax writes its zeros
-        if (s_issuer) ok = mbar_wait_polled(q_full, n & 1, wctl);
+        if (s_issuer) ok = mbar_wait_lean_warp(q_full, n & 1, wctl);
         for (int j = 0; j < it.nkt && ok; ++j, ++g) {
           const int sk = g % kStagesK, sv = g % kStagesV, b = g % kPBuf;
           if (s_issuer) {
-            ok = mbar_wait_polled(&k_full[sk], (g / kStagesK) & 1, wctl) &&
-                 (g == 0 || mbar_wait_polled(s_read, (g - 1) & 1, wctl));
+            ok = mbar_wait_lean_warp(&k_full[sk], (g / kStagesK) & 1, wctl) &&
+                 (g == 0 || mbar_wait_lean_warp(s_read, (g - 1) & 1, wctl));
             if (!ok) break;
             tc_fence_after();
             const uint64_t dk = dk0 + (uint64_t)(sk * (kTileBytes / 16));
+            if (elect_one()) {
 #pragma unroll
-            for (int ks = 0; ks < kHeadDim / 16; ++ks)
-              mma_f16_ss(tmem, dq + (uint64_t)(ks * 256), dk + (uint64_t)(ks * 256), idesc_s, ks > 0);
-            mma_commit(s_full);
-            mma_commit(&k_empty[sk]);
+              for (int ks = 0; ks < kHeadDim / 16; ++ks)
+                mma_f16_ss(tmem, dq + (uint64_t)(ks * 256), dk + (uint64_t)(ks * 256), idesc_s, ks > 0);
+              mma_commit(s_full);
+              mma_commit(&k_empty[sk]);
+            }
+            __syncwarp();
           } else {
-            ok = (j > 0 || n == 0 || mbar_wait_polled(o_empty, (n - 1) & 1, wctl)) &&
-                 mbar_wait_polled(&v_full[sv], (g / kStagesV) & 1, wctl);
+            ok = (j > 0 || n == 0 || mbar_wait_lean_warp(o_empty, (n - 1) & 1, wctl)) &&
+                 mbar_wait_lean_warp(&v_full[sv], (g / kStagesV) & 1, wctl);
             const uint64_t dv = dv0 + (uint64_t)(sv * (kVSlotBytes / 16));
             // Key half h: O_h += P_h V_h, P_h in its 32 columns of P buffer b.
             for (int hh = 0; hh < 2 && ok; ++hh) {
-              ok = mbar_wait_polled(&p_full[hh * kPBuf + b], (g / kPBuf) & 1, wctl);
+              ok = mbar_wait_lean_warp(&p_full[hh * kPBuf + b], (g / kPBuf) & 1, wctl);
               if (!ok) break;
               tc_fence_after();
+              if (elect_one()) {
 #pragma unroll
-              for (int ks = 0; ks < 4; ++ks)
-                mma_f16_ts(tmem + kColO + hh * 128, tmem + kColP + b * 64 + hh * 32 + ks * 8,
-                           dv + (uint64_t)((hh * 4 + ks) * 16), idesc_o, (j > 0 || ks > 0) ? 1u : 0u);
+                for (int ks = 0; ks < 4; ++ks)
+                  mma_f16_ts(tmem + kColO + hh * 128, tmem + kColP + b * 64 + hh * 32 + ks * 8,
+                             dv + (uint64_t)((hh * 4 + ks) * 16), idesc_o, (j > 0 || ks > 0) ? 1u : 0u);
+                if (hh == 1) {
+                  mma_commit(&pv_done[b]);
+                  mma_commit(&v_empty[sv]);
+                  if (j == it.nkt - 1) mma_commit(o_full);
+                }
+              }
+              __syncwarp();
             }
             if (!ok) break;
-            mma_commit(&pv_done[b]);
-            mma_commit(&v_empty[sv]);
-            if (j == it.nkt - 1) mma_commit(o_full);
           }
         }
         ++n;
       }
       // This issuer's MMAs have completed before tensor memory is freed.
-      mma_commit(mma_drain);
+      if (elect_one()) mma_commit(mma_drain);
+      __syncwarp();
       mbar_wait_drain(mma_drain, 0);
+    }
+   } else {
+    // ------------------------------------------------------------ items
+    // Varlen calls: works out the items ahead of the other roles and brings their queries into L2.
+    for (int idx = blockIdx.x, i = 0; kCompact && idx < num_items && !abort_seen_warp(wctl); idx += gridDim.x, ++i) {
+      const PItem it = prefill_item<kFour>(p, idx, table, ws);
+      const int s = i % kItemSlots;
+      if (i >= kItemSlots && !mbar_wait_asleep_warp(&item_empty[s], (i / kItemSlots - 1) & 1, wctl)) break;
+      if (lane == 0) {
+        items[s] = it;
+        mbar_arrive(&item_full[s]);
+      }
+      if (it.ok && it.nkt > 0) {
+#pragma unroll
+        for (int k = 0; k < 2 * kRows / 32; ++k) {
+          const int64_t row = it.row0 + k * 16 + (lane >> 1);
+          if (row < it.rows) prefetch_l2(p.q + q_row<kFour>(p, it, row) * kHeadDim + (lane & 1) * 64);
+        }
+      }
     }
    }
   } else {
@@ -718,60 +799,96 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     // at its start and to merge the halves; there they stop together if any gave up.
     int g = 0, n = 0;
     bool ok = true;
-    for (int idx = blockIdx.x; idx < num_items; idx += gridDim.x) {
-      if (bar_red_or(kSoftBar, kSoftThreads, !ok || *abort_flag != 0)) break;
-      const PItem it = prefill_item<kFour>(p, idx, table, ws);
-      const int64_t row = it.row0 + r;  // (token, head) row within the sequence
-      const bool my_row = row < it.rows;
-      const int my_i = (int)(row >> p.log2_heads), my_h = (int)(row & (Hq - 1));
-      // This row's place in q, out and lse_out.
-      const int64_t my_row_at = kFour ? (it.qrow0 + my_i) * p.q_heads + it.kvh * Hq + my_h : (it.qrow0 + my_i) * Hq + my_h;
-      float* out_row = p.out + my_row_at * kHeadDim + h * 64;  // (not used by the 4-bit cache)
-      uint16_t* out_row16 = p.out16 + my_row_at * kHeadDim + h * 64;
-      if (!it.ok) {  // invalid sequence (flagged by the dequant pass): 0 / -inf; beyond the chunk: nothing
-        if (my_row) {
-          for (int d = 0; d < 64; d += 4) {
-            if constexpr (kFour) *reinterpret_cast<uint2*>(out_row16 + d) = make_uint2(0u, 0u);
-            else *reinterpret_cast<float4*>(out_row + d) = make_float4(0.f, 0.f, 0.f, 0.f);
-          }
-          if (h == 0 && p.lse_out) p.lse_out[my_row_at] = -INFINITY;
-        }
-        continue;  // no MMA work for this item
-      }
-      // A piece's partial output row (normalised) and log2-sum-exp, for the merge.
-      float* part_row = it.piece >= 0 ? p.piece_o + ((int64_t)it.piece * kRows + r) * kHeadDim + h * 64 : nullptr;
-      float* part_lse = it.piece >= 0 ? p.piece_lse + (int64_t)it.piece * kRows + r : nullptr;
-      if (it.nkt == 0) {  // a piece with no key tiles (no MMA work): weight zero in the merge
-        for (int d = 0; d < 64; d += 4) *reinterpret_cast<float4*>(part_row + d) = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (h == 0) *part_lse = -INFINITY;
-        continue;
-      }
-      // This row's query (bf16), zero beyond the chunk: each half writes 8 of its 16 chunks.
-      {
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + (kFour ? my_row_at : it.qrow0 * Hq + row) * kHeadDim);
+    // This row's query of an item (bf16), zero beyond the chunk: each half takes 8 of its 16 chunks.  With the
+    // 4-bit cache the next item's is loaded and staged while the last products of an item end, so that its S need not
+    // wait (items of 65 tiles: 455 us before, 412 after; the int8 path, whose K scales take the registers, got 5%
+    // slower by it and stages at the item's start).
+    auto load_q = [&](const PItem& it, uint4 (&x)[8]) {
+      const int64_t row = it.row0 + r;
+      const uint4* src = reinterpret_cast<const uint4*>(p.q + q_row<kFour>(p, it, row) * kHeadDim) + h * 8;
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
-          uint4 x = my_row ? src[h * 8 + c] : make_uint4(0, 0, 0, 0);
-          if constexpr (kFour) {
-            uint32_t w[4] = {x.x, x.y, x.z, x.w};
+      for (int c = 0; c < 8; ++c) x[c] = row < it.rows ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+    };
+    auto stage_q = [&](uint4 (&x)[8]) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = pack_f16x2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
-            x = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-          *reinterpret_cast<uint4*>(qs + (h * 8 + c) * 2048 + r * 16) = x;
+      for (int c = 0; c < 8; ++c) {
+        if constexpr (kFour) {
+          uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = pack_f16x2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
+          x[c] = make_uint4(w[0], w[1], w[2], w[3]);
         }
+        *reinterpret_cast<uint4*>(qs + (h * 8 + c) * 2048 + r * 16) = x[c];
       }
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(q_full);
+    };
+    PItem next = {};
+    auto take_next = [&](int idx, int i) -> bool {  // whether the i-th item is there and has MMA work
+      next.ok = false;
+      next.nkt = 0;
+      if (idx < num_items) {
+        bool up;
+        next = get_item(i, false, up);
+        ok = ok && up;
+      }
+      return next.ok && next.nkt > 0;
+    };
+    if (take_next(blockIdx.x, kCompact ? 0 : blockIdx.x) && kFour) {
+      uint4 x[8];
+      load_q(next, x);
+      stage_q(x);
+    }
+    for (int idx = blockIdx.x, i = 0; idx < num_items; idx += gridDim.x, i += kCompact) {
+      if (bar_red_or(kSoftBar, kSoftThreads, !ok || *abort_flag != 0)) break;
+      const PItem it = next;
+      const int64_t row = it.row0 + r;  // (token, head) row within the sequence
+      const bool my_row = row < it.rows;
+      if (!it.ok) {  // invalid sequence (flagged by the dequant pass): 0 / -inf; beyond the chunk: nothing
+        if (my_row) {
+          const int64_t at = q_row<kFour>(p, it, row);
+          for (int d = 0; d < 64; d += 4) {
+            if constexpr (kFour) *reinterpret_cast<uint2*>(p.out16 + at * kHeadDim + h * 64 + d) = make_uint2(0u, 0u);
+            else *reinterpret_cast<float4*>(p.out + at * kHeadDim + h * 64 + d) = make_float4(0.f, 0.f, 0.f, 0.f);
+          }
+          if (h == 0 && p.lse_out) p.lse_out[at] = -INFINITY;
+        }
+        if (take_next(idx + gridDim.x, kCompact ? i + 1 : idx + gridDim.x) && kFour) {  // no MMA work for this item
+          uint4 x[8];
+          load_q(next, x);
+          stage_q(x);
+        }
+        continue;
+      }
+      // A piece's partial output rows (normalised) and log2-sum-exps, for the merge.
+      float* part = it.piece >= 0 ? p.piece_o + (int64_t)it.piece * kRows * kHeadDim : nullptr;
+      float* part_lse = it.piece >= 0 ? p.piece_lse + (int64_t)it.piece * kRows + r : nullptr;
+      if (it.nkt == 0) {  // a piece with no key tiles (no MMA work): weight zero in the merge
+        for (int d = 0; d < 64; d += 4)
+          *reinterpret_cast<float4*>(part + r * kHeadDim + h * 64 + d) = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (h == 0) *part_lse = -INFINITY;
+        if (take_next(idx + gridDim.x, kCompact ? i + 1 : idx + gridDim.x) && kFour) {
+          uint4 x[8];
+          load_q(next, x);
+          stage_q(x);
+        }
+        continue;
+      }
+      if (!kFour) {
+        uint4 x[8];
+        load_q(it, x);
+        stage_q(x);
+      }
       const int32_t p0 = p.prefix_len[kFour ? it.b / p.num_kv_heads : it.b];
-      const int q_pos = p0 + my_i;
+      const int q_pos = p0 + (int)(row >> p.log2_heads);
       const int k_lo = p.window > 0 ? max(0, q_pos + 1 - p.window) : 0;
       float m_ref = -INFINITY, l_sum = 0.0f;
+      bool s_there = false;
       for (int j = 0; j < it.nkt; ++j, ++g) {
         const int sv = g % kStagesV, b = g % kPBuf;
-        ok = mbar_wait_polled_warp(s_full, g & 1, wctl) &&
-             mbar_wait_polled_warp(&v_full[sv], (g / kStagesV) & 1, wctl);
+        ok = ((!kFour && __all_sync(0xffffffffu, s_there)) || mbar_wait_lean_warp(s_full, g & 1, wctl)) &&
+             (kFour || mbar_wait_polled_warp(&v_full[sv], (g / kStagesV) & 1, wctl));  // (for its K scales)
         if (!ok) break;
         tc_fence_after();
         const float* kscale = reinterpret_cast<const float*>(smem + kOffV + sv * kVSlotBytes + kTileBytes) + h * 64;
@@ -858,6 +975,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
           for (int c = 0; c < 64; ++c) z[c] -= mx;
         }
+        const bool p_free = g < kPBuf || mbar_test_wait(&pv_done[b], ((g / kPBuf) - 1) & 1);
         // P = 2^z as fp16 into this half's 32 columns of P buffer b, the A operand of
         // this half's PV, once the PVs of tile g - 2 have read that buffer.
         float l4[4] = {0.f, 0.f, 0.f, 0.f};  // four running sums (chunk calls: as two fp32 pairs)
@@ -883,12 +1001,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           f2_split(l01, l4[0], l4[1]);
           f2_split(l23, l4[2], l4[3]);
         }
-        if (g >= kPBuf) {
+        if (!__all_sync(0xffffffffu, p_free)) {
           ok = mbar_wait_polled_warp(&pv_done[b], ((g / kPBuf) - 1) & 1, wctl);
           if (!ok) break;
         }
         tmem_st_32x32b_x32(tmem + t_lane + kColP + b * 64 + h * 32, pw);
         l_sum += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+        if constexpr (!kFour) s_there = mbar_test_wait(s_full, (g + 1) & 1);  // (1% slower with the 4-bit cache)
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -898,47 +1017,76 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       // with w_h = 2^(m_h - M), M the larger reference; this thread writes its channel half.
       xref[h * kRows + r] = m_ref;
       xsum[h * kRows + r] = l_sum;
+      uint4 qx[8];  // (every S of this item is done: its Q may be overwritten)
+      const bool has_next = take_next(idx + gridDim.x, kCompact ? i + 1 : idx + gridDim.x);
+      if (kFour && has_next) load_q(next, qx);
       if (bar_red_or(kSoftBar, kSoftThreads, !ok)) break;
       const float m0 = xref[r], m1 = xref[kRows + r];
       const float M = fmaxf(m0, m1);
       const float w0 = m0 == -INFINITY ? 0.0f : ex2_approx(m0 - M);
       const float w1 = m1 == -INFINITY ? 0.0f : ex2_approx(m1 - M);
       const float Ls = w0 * xsum[r] + w1 * xsum[kRows + r];
+      if (kFour && has_next) stage_q(qx);
       ok = mbar_wait_polled_warp(o_full, n & 1, wctl);
       if (ok) {
         tc_fence_after();
         const float inv = Ls > 0.0f ? 1.0f / Ls : 0.0f;
         const float c0 = w0 * inv, c1 = w1 * inv;
-        float* dst = kFour || part_row ? part_row : out_row;
+        float o[64];
 #pragma unroll
         for (int c = 0; c < 64; c += 32) {
           uint32_t o0[32], o1[32];
           tmem_ld_32x32b_x32(tmem + t_lane + kColO + h * 64 + c, o0);
           tmem_ld_32x32b_x32(tmem + t_lane + kColO + 128 + h * 64 + c, o1);
           tmem_wait_ld();
-          if (my_row) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 x = make_float4(
-                  fmaf(c0, __uint_as_float(o0[e]), c1 * __uint_as_float(o1[e])),
-                  fmaf(c0, __uint_as_float(o0[e + 1]), c1 * __uint_as_float(o1[e + 1])),
-                  fmaf(c0, __uint_as_float(o0[e + 2]), c1 * __uint_as_float(o1[e + 2])),
-                  fmaf(c0, __uint_as_float(o0[e + 3]), c1 * __uint_as_float(o1[e + 3])));
-              if (kFour && !part_row)
-                *reinterpret_cast<uint2*>(out_row16 + c + e) = make_uint2(pack_bf16x2(x.x, x.y), pack_bf16x2(x.z, x.w));
-              else
-                *reinterpret_cast<float4*>(dst + c + e) = x;
+          for (int e = 0; e < 32; ++e) o[c + e] = fmaf(c0, __uint_as_float(o0[e]), c1 * __uint_as_float(o1[e]));
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(o_empty);
+        if constexpr (kFour) {
+          if (my_row && part) {
+            float* dst = part + r * kHeadDim + h * 64;
+#pragma unroll
+            for (int e = 0; e < 64; e += 4) *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          } else if (my_row) {
+            uint16_t* dst = p.out16 + q_row<kFour>(p, it, row) * kHeadDim + h * 64;
+            uint32_t x[32];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
+            if ((reinterpret_cast<uintptr_t>(p.out16) & 31) == 0) {  // (a tensor's rows; else 16-byte aligned)
+#pragma unroll
+              for (int e = 0; e < 32; e += 8) st_global_v8(dst + 2 * e, &x[e]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4*>(dst + 2 * e) = make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+            }
+          }
+        } else {
+          // Lane q of 8 stores unit q (16 bytes) of the 8 rows from row8 on.
+          const int q = lane & 7, row8 = quarter * 32 + (lane & 24);
+#pragma unroll
+          for (int c = 0; c < 64; c += 32) {
+            uint4 x[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+              x[u] = make_uint4(__float_as_uint(o[c + 4 * u]), __float_as_uint(o[c + 4 * u + 1]),
+                                __float_as_uint(o[c + 4 * u + 2]), __float_as_uint(o[c + 4 * u + 3]));
+            transpose_units(x, q);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const int64_t to = it.row0 + row8 + i;
+              float* dst = part ? part + (row8 + i) * kHeadDim : p.out + q_row<kFour>(p, it, to) * kHeadDim;
+              if (to < it.rows) *reinterpret_cast<uint4*>(dst + h * 64 + c + q * 4) = x[i];
             }
           }
         }
         if (h == 0 && my_row) {
           const float lse2 = Ls > 0.0f ? M + __log2f(Ls) : -INFINITY;
           if (part_lse) *part_lse = lse2;
-          else if (p.lse_out) p.lse_out[my_row_at] = lse2 * kLn2;
+          else if (p.lse_out) p.lse_out[q_row<kFour>(p, it, row)] = lse2 * kLn2;
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(o_empty);
       }
       ++n;
     }

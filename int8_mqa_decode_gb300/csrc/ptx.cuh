@@ -142,6 +142,20 @@ __device__ __forceinline__ bool mbar_wait_lean_warp(uint64_t* bar, uint32_t pari
   return __all_sync(0xffffffffu, mbar_wait_lean(bar, parity, w));
 }
 
+// For a warp that is far ahead of whom it waits for: it sleeps between tries, and so takes no issue slots.
+__device__ __forceinline__ bool mbar_wait_asleep_warp(uint64_t* bar, uint32_t parity, volatile WaitState* w) {
+  const uint64_t t0 = globaltimer_ns();
+  while (!__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) {
+    if (__any_sync(0xffffffffu, w->abort != 0)) return false;
+    if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > w->limit_ns)) {
+      w->abort = 1;
+      return false;
+    }
+    __nanosleep(1000);
+  }
+  return true;
+}
+
 // As mbar_wait_abortable, polling without blocking for a few tries first: a thread
 // suspended by a blocking try resumes a few hundred cycles after the phase completes,
 // which the waits of a ~2.5k-cycle pipeline period cannot afford (measured: 64 tries
@@ -154,6 +168,20 @@ __device__ __forceinline__ bool mbar_wait_polled(uint64_t* bar, uint32_t parity,
 }
 __device__ __forceinline__ bool mbar_wait_polled_warp(uint64_t* bar, uint32_t parity, volatile WaitState* w) {
   return __all_sync(0xffffffffu, mbar_wait_polled(bar, parity, w));
+}
+
+// 32 bytes, 32-byte aligned.
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t* x) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
+               "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
+               : "memory");
+}
+
+// One lane of a whole warp (products issued under it go out every 16 to 64 cycles, under `lane == 0` at best every 46).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}" : "=r"(p));
+  return p != 0;
 }
 
 // The same wait made by all 32 lanes of a warp: true in every lane only if it held in
