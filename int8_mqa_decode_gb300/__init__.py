@@ -535,12 +535,22 @@ class Rope:
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
+def _on_current(*tensors) -> None:
+    """The launch goes to the current device: tensors of another one are refused, not read across."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+
+
 def _pools_of(pools, kind):
     if isinstance(pools, kind):
+        _on_current(pools.pages)
         return ctypes.byref(pools.struct), 1
     for p in pools:
         if not isinstance(p, kind):
             raise TypeError(f"pools must be {kind.__name__} objects, got {type(p).__name__}")
+    _on_current(*[p.pages for p in pools])
     n = len(pools)
     if n == 1:
         return ctypes.byref(pools[0].struct), 1
@@ -617,6 +627,9 @@ def _append_rows(entry: str, kind, pools, k_new, v_new, block_table, start_pos, 
         hq, q_stride, q_ptr = q.shape[-2], _row_stride(q, "q"), _cuda(q, "q")
         out_ptr = _ptr(q_out, "q_out", torch.bfloat16, q.shape)
     table, width = _table(block_table, batch)
+    _on_current(k_new, v_new, q, q_out, block_table, start_pos, q_offsets, err_flag)
+    if rope is not None:
+        _on_current(rope.cos, rope.sin)
     st = getattr(load(), entry)(
         arr, hkv, ctypes.byref(rope.struct) if rope is not None else None, _cuda(k_new, "k_new"), _cuda(v_new, "v_new"),
         kv_type, _row_stride(k_new, "k_new"), _row_stride(v_new, "v_new"), q_ptr, q_stride, out_ptr, hq, batch, n_new,
@@ -657,6 +670,7 @@ def _read_rows(entry: str, kind, pools, k_out, v_out, block_table, start_pos, q_
     if one.dtype not in _DTYPES:
         raise TypeError(f"outputs must be fp32 or bf16, got {one.dtype}")
     table, width = _table(block_table, batch)
+    _on_current(k_out, v_out, block_table, start_pos, q_offsets, err_flag)
     st = getattr(load(), entry)(
         arr, hkv, _ptr(k_out, "k_out"), _ptr(v_out, "v_out"), _DTYPES[one.dtype], batch, n_new,
         q_offsets.data_ptr() if q_offsets is not None else None, rows, table, width,
@@ -694,6 +708,7 @@ def cai_kv4_decode(pools: Sequence[KV4Pool], q: torch.Tensor, block_table: torch
     shape = (batch, hq, HEAD_DIM)
     table, width = _table(block_table, batch)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _on_current(q, block_table, ctx_len, workspace, out, lse_out, err_flag)
     st = load().cai_kv4_decode(
         arr, hkv, _ptr(q, "q", torch.bfloat16, shape), batch, hq, table, width,
         _ptr(ctx_len, "ctx_len", torch.int32, (batch,)), window, float(softmax_scale), num_splits,
@@ -717,6 +732,7 @@ def cai_kv4_prefill(pools: Sequence[KV4Pool], q: torch.Tensor, block_table: torc
     rows, batch, n_new, hq = _rows(q, "q", q_offsets, max_new, prefix_len)
     table, width = _table(block_table, batch)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _on_current(q, block_table, prefix_len, workspace, out, lse_out, err_flag, q_offsets)
     st = load().cai_kv4_prefill(
         arr, hkv, _ptr(q, "q", torch.bfloat16), batch, n_new, q_offsets.data_ptr() if q_offsets is not None else None,
         rows, hq, table, width, _ptr(prefix_len, "prefix_len", torch.int32, (batch,)), window, float(softmax_scale),

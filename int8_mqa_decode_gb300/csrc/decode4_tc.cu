@@ -555,7 +555,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) decode4_tc_kernel(const __grid_
               __syncwarp();
               tc_fence_after();
             }
-            const bool any = fmaxf(fmaxf(wmax[0], wmax[HN]), fmaxf(wmax[2 * HN], wmax[3 * HN])) > -INFINITY;
+            const bool any = okm != 0;  // some key of the tile is attended
 #pragma unroll
             for (int h1 = 0; h1 < HN; h1 += 8) {
               float up = 0.0f, f = 0.0f;  // of head h1 + lane: what its reference rises by, and 2^-up

@@ -400,6 +400,39 @@ def test_decode_many_short_sequences():
         small.check(o[i:i + 1], l[i:i + 1], x[i:i + 1], which[i], int(ctx[i]) - 1, 0, i)
 
 
+@pytest.mark.parametrize("hq", [8, 16, 32, 64])
+@pytest.mark.parametrize("width", [3, 40])
+def test_decode_many_short_sequences_cut_or_whole(hq, width):
+    """The same in both splits: tables of up to 512 tokens (no sequence is cut) and longer ones, and every kernel."""
+    rng = np.random.default_rng(width)
+    small = Cache(rng.integers(0, 45, 30), 1, 16, seed=10, width=width)
+    b = 9000 if hq == 8 and width == 40 else 5200
+    which = rng.integers(0, 30, b)
+    ctx = np.array([small.lengths[w] for w in which], np.int32)
+    q = queries(rng, b, hq)
+    table = small.table[torch.from_numpy(which).to(DEV)].contiguous()
+    ws = torch.empty(max(1, cai.cai_kv4_decode_workspace_size(b, hq, 1, width, 16, 0)), dtype=torch.uint8, device=DEV)
+    out = torch.empty(b, hq, 128, dtype=torch.bfloat16, device=DEV)
+    lse = torch.empty(b, hq, device=DEV)
+    cai.cai_kv4_decode(small.pools, q, table, dev(ctx), 0, SCALE, 0, ws, out, lse)
+    for i in list(range(30)) + list(range(b - 30, b)) + list(rng.integers(0, b, 60)):
+        small.check(host(out[i:i + 1]), host(lse[i:i + 1]), host(q[i:i + 1]), which[i], int(ctx[i]) - 1, 0, i)
+
+
+@pytest.mark.parametrize("hq", [8, 32])
+def test_decode_an_infinite_head_spoils_no_other(hq):
+    """A head whose logits are all infinite or NaN leaves its neighbours alone."""
+    cache = Cache([700], 1, 16, seed=11)
+    q = queries(np.random.default_rng(11), 1, hq)
+    want, wl = decode(cache, q, [700])
+    q2 = q.clone()
+    q2[0, 0] = -float("inf")
+    q2[0, 5] = float("nan")
+    out, lse = decode(cache, q2, [700])
+    rest = [h for h in range(hq) if h not in (0, 5)]
+    assert torch.equal(out[0, rest], want[0, rest]) and torch.equal(lse[0, rest], wl[0, rest])
+
+
 def test_decode_bad_lengths_and_pages():
     cache = Cache([100, 200, 300], 2, 16, seed=2)
     q = queries(np.random.default_rng(2), 3, 16)
@@ -566,6 +599,72 @@ def test_prefill_single_rows_alone_and_decode_agree():
     cache = Cache(lengths, 2, 16, seed=13)
     q = queries(np.random.default_rng(13), 4, 32)
     check_prefill(cache, q, [n - 1 for n in lengths], [1] * 4, max_new=9)
+
+
+def test_prefill_more_items_than_a_block_lists():
+    """Past 4096 q-tiles a packed call numbers them densely."""
+    rng = np.random.default_rng(16)
+    one = Cache([200, 180], 8, 16, seed=16)
+    b, n, hq = 64, 130, 64  # 64 sequences of 9 q-tiles for each of 8 K/V heads, over two stored ones
+    which = [i % 2 for i in range(b)]
+    table = one.table[torch.tensor(which, device=DEV)].contiguous()
+    new = [n] * b
+    new[3], new[7] = 1, 0
+    prefix = [one.lengths[w] - k for w, k in zip(which, new)]
+    off = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    q = queries(rng, int(off[-1]), hq)
+    ws = torch.empty(cai.cai_kv4_prefill_workspace_size(b, hq, 8, table.shape[1], 16), dtype=torch.uint8, device=DEV)
+    out, lse, err = torch.empty_like(q), torch.empty(q.shape[:2], device=DEV), flag()
+    cai.cai_kv4_prefill(one.pools, q, table, dev(np.array(prefix, np.int32)), 0, SCALE, ws, out, lse, err, q_offsets=dev(off), max_new=n)
+    assert err.item() == 0
+    for i in (0, 1, 3, 30, 62, 63):
+        s = slice(off[i], off[i + 1])
+        one.check(host(out[s]), host(lse[s]), host(q[s]), which[i], prefix[i], 0, i)
+
+
+def test_attention_into_outputs_of_odd_alignment():
+    """Outputs that start 16 bytes into a sector; rows behind the last sequence stay as they were."""
+    cache = Cache([300, 33], 1, 16, seed=17)
+    rng = np.random.default_rng(17)
+    prefix, new, rows = [150, 13], [150, 20], 180
+    q = queries(rng, rows, 16)
+    ws = torch.empty(cai.cai_kv4_prefill_workspace_size(2, 16, 1, cache.table.shape[1], 16), dtype=torch.uint8, device=DEV)
+    room = torch.full((rows * 16 * 128 + 16,), 7.0, dtype=torch.bfloat16, device=DEV)
+    lroom = torch.full((rows * 16 + 1,), 7.0, device=DEV)
+    out, lse = room[8:8 + rows * 16 * 128].view(rows, 16, 128), lroom[1:].view(rows, 16)
+    cai.cai_kv4_prefill(cache.pools, q, cache.table, dev(np.array(prefix, np.int32)), 0, SCALE, ws, out, lse,
+                        q_offsets=dev(np.array([0, 150, 170], np.int32)), max_new=150)
+    for b, s in enumerate((slice(0, 150), slice(150, 170))):
+        cache.check(host(out[s]), host(lse[s]), host(q[s]), b, prefix[b], 0, b)
+    assert (room[:8] == 7).all() and (room[8 + 170 * 16 * 128:] == 7).all() and (lroom[1 + 170 * 16:] == 7).all() and lroom[0] == 7
+    for hq in (8, 32):
+        q = queries(rng, 2, hq)
+        room = torch.full((2 * hq * 128 + 16,), 7.0, dtype=torch.bfloat16, device=DEV)
+        out, lse = room[8:8 + 2 * hq * 128].view(2, hq, 128), torch.empty(2, hq, device=DEV)
+        ws = torch.empty(max(1, cai.cai_kv4_decode_workspace_size(2, hq, 1, cache.table.shape[1], 16, 0)), dtype=torch.uint8, device=DEV)
+        cai.cai_kv4_decode(cache.pools, q, cache.table, dev(np.array([300, 33], np.int32)), 0, SCALE, 0, ws, out, lse)
+        for b, n in enumerate((300, 33)):
+            cache.check(host(out[b:b + 1]), host(lse[b:b + 1]), host(q[b:b + 1]), b, n - 1, 0, (hq, b))
+        assert (room[:8] == 7).all() and (room[-8:] == 7).all()
+
+
+def test_tensors_of_another_device_are_refused(monkeypatch):
+    """The launch goes to the current device: with another one current, nothing is launched."""
+    cache = Cache([20], 1, 16, seed=18)
+    q = queries(np.random.default_rng(18), 1, 8)
+    zero = torch.zeros(1, dtype=torch.int32, device=DEV)
+    x = torch.zeros(1, 1, 1, 128, device=DEV)
+    before = cache.pools[0].pages.clone()
+    ws = torch.empty(cai.cai_kv4_prefill_workspace_size(1, 8, 1, cache.table.shape[1], 16), dtype=torch.uint8, device=DEV)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    for call in (lambda: decode(cache, q, [20]), lambda: cai.cai_kv4_append(cache.pools, x, x, cache.table, zero),
+                 lambda: cai.cai_kv4_read(cache.pools, x, None, cache.table, zero),
+                 lambda: cai.cai_kv4_prefill(cache.pools, q[None], cache.table, zero, 0, SCALE, ws, torch.empty_like(q)[None])):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+    monkeypatch.undo()
+    torch.cuda.synchronize()
+    assert torch.equal(cache.pools[0].pages, before)
 
 
 def test_prefill_bad_sequences():
