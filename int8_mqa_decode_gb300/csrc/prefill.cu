@@ -28,26 +28,19 @@
 //     by 2^8), and writes P (fp16) into tensor memory, where it is the A operand
 //     of O_h += P_h V_h (V from shared memory, MN-major).
 //
-// The 4-bit cache runs through the same kernels (kFour): there the copy's K is the fp16 value that a
-// code stands for (exact, so no per-key scale is left), the query is converted to fp16 as it is staged,
-// the copy holds one "sequence" per (sequence, K/V head), whose rows are (token, query head of that K/V
-// head) pairs, and the output is bf16.
+// The 4-bit cache has the same two steps (kFour, and prefill4.cu for the second): there the copy's K is the
+// fp16 value that a code stands for (exact, so no per-key scale is left), and the copy holds one "sequence"
+// per (sequence, K/V head), whose rows are (token, query head of that K/V head) pairs.
 #include <cuda_fp16.h>
 
 #include <algorithm>
 #include <type_traits>
 
-#include "common.cuh"
-#include "kv4.cuh"
-#include "ptx.cuh"
+#include "prefill.cuh"
 
 namespace cai {
 namespace {
 
-constexpr int kRows = 128;                 // query rows per q-tile (MMA M)
-constexpr int kQT = 1;                     // q-tiles per work item
-constexpr int kKeys = 128;                 // keys per tile (MMA N of S, K of PV)
-constexpr int kTileBytes = kKeys * kHeadDim * 2;  // 32 KB of 16-bit values
 constexpr int kStagesK = 2;                // K tile slots
 constexpr int kStagesV = 3;                // V tile slots (with the tile's K scales, which the softmax reads)
 constexpr int kPBuf = 2;                   // P buffers in tensor memory (S has one)
@@ -56,7 +49,7 @@ constexpr int kOffQ = 0;                                     // Q
 // free as soon as S = Q K^T of its tile has run, so the next K tiles load ahead of
 // the softmax; a V slot (and its scales, which the softmax of its tile reads first)
 // is free after its PV, so the V ring is one slot deeper.
-constexpr int kOffK = kOffQ + kQT * kRows * kHeadDim * 2;   // K[kStagesK]
+constexpr int kOffK = kOffQ + kRows * kHeadDim * 2;         // K[kStagesK]
 constexpr int kVSlotBytes = kTileBytes + kKeys * 4;          // V (scaled), K scales
 constexpr int kOffV = kOffK + kStagesK * kTileBytes;         // V[kStagesV]
 constexpr int kOffXch = kOffV + kStagesV * kVSlotBytes;      // softmax exchange: row references, row sums [2][128] each
@@ -64,14 +57,10 @@ constexpr int kOffBars = kOffXch + 4 * kRows * 4;
 // k_full, k_empty [kStagesK]; v_full, v_empty [kStagesV]; q_full; s_full, s_read;
 // p_full [2 key halves][kPBuf]; pv_done [kPBuf] (one per P buffer); o_full, o_empty;
 // the MMA issuers' last commits; item_full, item_empty [kItemSlots].
-constexpr int kItemSlots = 4;
 constexpr int kNumBars = 2 * kStagesK + 2 * kStagesV + 1 + 2 + 3 * kPBuf + 2 + 1 + 2 * kItemSlots;
 constexpr int kOffMisc = kOffBars + 8 * kNumBars;
 // Varlen dequant: sequences whose tiles one block numbers in shared memory.
 constexpr int kMaxCompactSeqs = 8192;
-// A varlen call's item list (see PrefillParams::compact): its count, then the dense
-// q-tile number of each item, in shared memory that only such a launch asks for.
-constexpr int kMaxCompactItems = 4096;
 constexpr int kOffItems = (kOffMisc + 32 + 15) & ~15;  // after the tmem slot and the wait state (+8): items, 64 bytes each
 constexpr int kOffTable = kOffItems + kItemSlots * 64;
 constexpr int kSmemBytes = kOffTable + 1024;  // without the list; ... and alignment slack
@@ -90,70 +79,6 @@ constexpr int kRegsLaunch = 168;
 static_assert(kRegsCtl * 128 + kRegsSoft * 256 <= kRegsLaunch * kThreads, "register split");
 constexpr uint32_t kTmemCols = 512;        // S (128 columns), P[2] (64 each), O[2] (128 each, one per key half)
 constexpr float kRescaleThreshold = 8.0f;
-
-struct PrefillParams {
-  const uint8_t* pages;
-  int32_t num_pages, page_size, max_pages;
-  const int32_t* table;
-  const int32_t* prefix_len;
-  const uint16_t* q;      // bf16 [rows of new tokens][Hq][128], sequence b's rows from q_row0(b)
-  const int32_t* q_off;   // [B + 1] packed new-token offsets, or null: sequence b has n_new rows at b * n_new
-  int32_t batch, n_new, total_new, num_heads, log2_heads, window, kt_rows, qtiles;  // n_new: the most per sequence; qtiles per sequence
-  float scale_log2;
-  // Work items: items [0, full_items) are whole q-tiles; the q-tiles after them (the
-  // last, partial wave of a persistent grid) are cut into `pieces` key ranges each,
-  // item full_items + t being piece t % pieces of q-tile full_items + t / pieces.  A
-  // piece writes its normalised partial output and log2-sum-exp to piece_o / piece_lse
-  // ([t][128 rows][128] and [t][128]); combine_pieces_kernel merges them.
-  int32_t full_items, pieces, num_items;
-  uint64_t wait_ns;  // limit of every bounded wait inside the kernel
-  int32_t drop_stage;  // fault injection: K tile each CTA skips (-1: none)
-  int32_t skip_single;  // see PrefillLaunch
-  // Varlen calls: the items are only the q-tiles that hold rows, sequence by sequence,
-  // through a list of their dense numbers that every CTA builds at its start (the dense
-  // numbering, qtiles slots per sequence for the longest one, would make the grid walk
-  // the empty slots of every short or one-token sequence); past kMaxCompactItems real
-  // q-tiles, the dense numbering.  No pieces then.
-  int32_t compact;
-  float* piece_o;
-  float* piece_lse;
-  uint16_t* kb;  // scratch bf16 [B][KT][128]
-  uint16_t* vh;  // scratch fp16 [B][KT][128]: V codes times the V scale
-  float* ks;     // scratch [B][KT]: K scale * softmax scale * log2(e)
-  float* out;
-  float* lse_out;
-  int32_t* err;
-  // The 4-bit cache; elsewhere one K/V head and q_heads = num_heads.
-  int32_t num_kv_heads, q_heads;
-  const uint8_t* pages4[kMaxKvHeads];
-  int32_t num_pages4[kMaxKvHeads];
-  uint16_t* out16;
-};
-
-// New tokens of sequence b: rows [r0, r0 + n) of q / out, or n = -1 when its offsets
-// are out of order or outside [0, total_new] (nothing of it is read or written).
-struct SeqRows {
-  int64_t r0;
-  int n;
-};
-
-__device__ __forceinline__ SeqRows seq_rows(const PrefillParams& p, int b) {
-  SeqRows s;
-  if (!p.q_off) {
-    s.r0 = (int64_t)b * p.n_new;
-    s.n = p.n_new;
-    return s;
-  }
-  const int32_t a = p.q_off[b], e = p.q_off[b + 1];
-  s.r0 = a;
-  s.n = (a >= 0 && a <= e && e <= p.total_new && e - a <= p.n_new) ? e - a : -1;
-  if (p.skip_single && s.n == 1) s.n = 0;  // decoded by the decode kernel in the same call
-  return s;
-}
-
-__device__ __forceinline__ bool seq_ok(const PrefillParams& p, int32_t p0, int n) {
-  return n >= 0 && p0 >= 0 && (int64_t)p0 + n <= (int64_t)p.max_pages * p.page_size;
-}
 
 // 8 x 8 bytes across the 8 lanes q = lane % 8 of an aligned group: lane q enters with
 // row q (bytes 0..3 in a, 4..7 in b) and leaves with column q (rows 0..3 in a, 4..7 in
@@ -410,96 +335,6 @@ __global__ void __launch_bounds__(256) dequant_compact_kernel(const __grid_const
   }
 }
 
-// One work item: a q-tile (128 consecutive (token, head) rows) of one
-// sequence.  ok = false: no MMA work; the softmax groups then write zeros to the
-// item's rows below `rows` (an invalid sequence) or nothing (rows beyond the chunk).
-struct PItem {
-  int b, row0, kt0, nkt;
-  int kvh;        // K/V head (4-bit cache)
-  int64_t qrow0;  // first packed new-token row of the sequence
-  int rows;       // (token, head) rows of the sequence, 0 if its offsets are invalid
-  bool ok;
-  int piece;      // -1: the whole key range; otherwise the piece's slot in piece_o / piece_lse
-};
-
-// q-tiles holding rows of sequence b (0 when it has no rows in this call); with the 4-bit cache, of
-// (sequence, K/V head) b.
-template <bool kFour>
-__device__ __forceinline__ int seq_qtiles(const PrefillParams& p, int b) {
-  const SeqRows sr = seq_rows(p, kFour ? b / p.num_kv_heads : b);
-  return sr.n > 0 ? (int)(((int64_t)sr.n * p.num_heads + kRows - 1) / kRows) : 0;
-}
-
-// The work split of a persistent grid over `total` q-tiles: items [0, full) are whole
-// q-tiles; the q-tiles of a partial last wave are cut into `pieces` key ranges so that
-// wave ends sooner (with r q-tiles left over, pieces = grid / r, at most 4), item
-// full + t being piece t % pieces of q-tile full + t / pieces; num items in all.  The
-// host applies it to a chunk call's q-tiles.
-struct WorkSplit {
-  int full, pieces, num;
-};
-__host__ __device__ inline WorkSplit work_split(int64_t total, int grid) {
-  const int64_t rem = grid > 0 ? total % grid : 0;
-  int pieces = rem > 0 ? (int)(grid / rem) : 1;
-  if (pieces > 4) pieces = 4;
-  if (pieces < 2) pieces = 1;
-  WorkSplit w;
-  w.pieces = pieces;
-  w.full = (int)(pieces > 1 ? total - rem : total);
-  w.num = (int)(w.full + (pieces > 1 ? rem * pieces : 0));
-  return w;
-}
-
-// (token, head) row `row` of an item's sequence, as a row of q, out and lse_out.
-template <bool kFour>
-__device__ __forceinline__ int64_t q_row(const PrefillParams& p, const PItem& it, int64_t row) {
-  return kFour ? (it.qrow0 + (row >> p.log2_heads)) * p.q_heads + it.kvh * p.num_heads + (row & (p.num_heads - 1))
-               : it.qrow0 * p.num_heads + row;
-}
-
-// list: a varlen call's q-tile numbers (entry i for q-tile i - list_first), or null.
-template <bool kFour>
-__device__ __forceinline__ PItem prefill_item(const PrefillParams& p, int idx, const int32_t* list,
-                                              const WorkSplit& ws, int list_first = 0) {
-  PItem it;
-  int qti = idx, piece = -1;
-  if (idx >= ws.full) {
-    const int t = idx - ws.full;
-    qti = ws.full + t / ws.pieces;
-    piece = t % ws.pieces;
-    it.piece = t;
-  } else {
-    it.piece = -1;
-  }
-  const int qt = list ? list[qti - list_first] : qti;
-  it.b = qt / p.qtiles;
-  it.row0 = (qt - it.b * p.qtiles) * (kQT * kRows);
-  const int seq = kFour ? it.b / p.num_kv_heads : it.b;
-  it.kvh = kFour ? it.b - seq * p.num_kv_heads : 0;
-  const int32_t p0 = p.prefix_len[seq];
-  const SeqRows sr = seq_rows(p, seq);
-  it.qrow0 = sr.r0;
-  it.rows = sr.n > 0 ? sr.n * p.num_heads : 0;
-  it.ok = seq_ok(p, p0, sr.n) && it.row0 < it.rows;
-  if (!it.ok) {
-    it.kt0 = it.nkt = 0;
-    return it;
-  }
-  const int i0 = it.row0 >> p.log2_heads;
-  const int i_last = min((it.row0 + kQT * kRows - 1) >> p.log2_heads, sr.n - 1);
-  const int kv_hi = p0 + i_last + 1;
-  const int kv_lo = p.window > 0 ? max(0, p0 + i0 + 1 - p.window) : 0;
-  it.kt0 = kv_lo / kKeys;
-  it.nkt = (kv_hi - 1) / kKeys - it.kt0 + 1;
-  if (piece >= 0) {  // key tiles [per * piece, per * (piece + 1)) of the q-tile's range
-    const int per = (it.nkt + ws.pieces - 1) / ws.pieces;
-    const int a = min(it.nkt, per * piece), e = min(it.nkt, per * (piece + 1));
-    it.kt0 += a;
-    it.nkt = e - a;
-  }
-  return it;
-}
-
 // Rows of 8 units of 16 bytes, one per lane: lane q of 8 leaves with unit q of the 8 rows, so that a store of
 // the 8 lanes covers a whole 128-byte line (32 lines an instruction, a row per lane, took the epilogue
 // 4300 cycles; so they take 1/8).
@@ -538,7 +373,7 @@ __device__ __forceinline__ void transpose_units(uint4 (&x)[8], int q) {
 // the end of the item (channel half each).
 // kCompact: a varlen call's launch (p.compact): its items go through the item list.
 // Chunk calls compile without that path (its one branch per item cost them 2%).
-template <bool kCompact, bool kFour>
+template <bool kCompact>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ PrefillParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -600,32 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     fence_barrier_init();
   }
   if (kCompact && warp == 3) {
-    // The item list: lane l sums the q-tiles of a run of sequences, a warp scan gives
-    // each run its first item, and each lane writes its run's items; the count is -1
-    // (the dense numbering) when they do not fit.
-    int32_t* hdr = reinterpret_cast<int32_t*>(smem + kOffTable);
-    int32_t* list = hdr + 4;
-    const int nb = kFour ? p.batch * p.num_kv_heads : p.batch;
-    const int per = (nb + 31) / 32;
-    const int b0 = min(nb, lane * per), b1 = min(nb, b0 + per);
-    int sum = 0;
-    for (int b = b0; b < b1; ++b) sum += seq_qtiles<kFour>(p, b);
-    int incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    const int total = __shfl_sync(0xffffffffu, incl, 31);
-    if (total <= kMaxCompactItems) {
-      int run = incl - sum;
-      for (int b = b0; b < b1; ++b) {
-        const int n = seq_qtiles<kFour>(p, b);
-        for (int j = 0; j < n; ++j) list[run + j] = b * p.qtiles + j;
-        run += n;
-      }
-    }
-    if (lane == 0) *hdr = total <= kMaxCompactItems ? total : -1;
+    list_items<false>(p, reinterpret_cast<int32_t*>(smem + kOffTable), lane);
   }
   tc_fence_before();
   __syncthreads();
@@ -651,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   auto get_item = [&](int i, bool one, bool& up) -> PItem {
     if constexpr (!kCompact) {
       up = true;
-      return prefill_item<kFour>(p, i, table, ws);
+      return prefill_item<false>(p, i, table, ws);
     }
     const int s = i % kItemSlots;
     PItem it = {};
@@ -685,9 +495,9 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           gk = g + 1;
           if (g >= kStagesV && !mbar_wait_polled(&v_empty[sv], ((g / kStagesV) - 1) & 1, wctl)) break;
           uint8_t* vs = smem + kOffV + sv * kVSlotBytes;
-          mbar_arrive_expect_tx(&v_full[sv], kFour ? kTileBytes : kVSlotBytes);
+          mbar_arrive_expect_tx(&v_full[sv], kVSlotBytes);
           bulk_g2s(vs, p.vh + row * kHeadDim, kTileBytes, &v_full[sv]);
-          if constexpr (!kFour) bulk_g2s(vs + kTileBytes, p.ks + row, kKeys * 4, &v_full[sv]);
+          bulk_g2s(vs + kTileBytes, p.ks + row, kKeys * 4, &v_full[sv]);
           gv = g + 1;
         }
       }
@@ -703,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     // operands.  S(g) overwrites S once the softmax has read S(g - 1) into registers, so
     // it runs during that softmax's exponentials; P has buffers of its own.
     {
-      constexpr uint32_t idesc_s = kFour ? idesc_f16_f32(kRows, kKeys, 0, 0) : idesc_bf16_f32(kRows, kKeys, 0, 0);
+      constexpr uint32_t idesc_s = idesc_bf16_f32(kRows, kKeys, 0, 0);
       constexpr uint32_t idesc_o = idesc_f16_f32(kRows, kHeadDim, 0, 1);
       const bool s_issuer = warp == 1;
       // Descriptor bases; a K step adds 4096 bytes (S operands) or 256 bytes (V),
@@ -769,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     // ------------------------------------------------------------ items
     // Varlen calls: works out the items ahead of the other roles and brings their queries into L2.
     for (int idx = blockIdx.x, i = 0; kCompact && idx < num_items && !abort_seen_warp(wctl); idx += gridDim.x, ++i) {
-      const PItem it = prefill_item<kFour>(p, idx, table, ws);
+      const PItem it = prefill_item<false>(p, idx, table, ws);
       const int s = i % kItemSlots;
       if (i >= kItemSlots && !mbar_wait_asleep_warp(&item_empty[s], (i / kItemSlots - 1) & 1, wctl)) break;
       if (lane == 0) {
@@ -780,7 +590,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
         for (int k = 0; k < 2 * kRows / 32; ++k) {
           const int64_t row = it.row0 + k * 16 + (lane >> 1);
-          if (row < it.rows) prefetch_l2(p.q + q_row<kFour>(p, it, row) * kHeadDim + (lane & 1) * 64);
+          if (row < it.rows) prefetch_l2(p.q + q_row<false>(p, it, row) * kHeadDim + (lane & 1) * 64);
         }
       }
     }
@@ -799,67 +609,22 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     // at its start and to merge the halves; there they stop together if any gave up.
     int g = 0, n = 0;
     bool ok = true;
-    // This row's query of an item (bf16), zero beyond the chunk: each half takes 8 of its 16 chunks.  With the
-    // 4-bit cache the next item's is loaded and staged while the last products of an item end, so that its S need not
-    // wait (items of 65 tiles: 455 us before, 412 after; the int8 path, whose K scales take the registers, got 5%
-    // slower by it and stages at the item's start).
-    auto load_q = [&](const PItem& it, uint4 (&x)[8]) {
-      const int64_t row = it.row0 + r;
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + q_row<kFour>(p, it, row) * kHeadDim) + h * 8;
-#pragma unroll
-      for (int c = 0; c < 8; ++c) x[c] = row < it.rows ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
-    };
-    auto stage_q = [&](uint4 (&x)[8]) {
-#pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        if constexpr (kFour) {
-          uint32_t w[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) w[e] = pack_f16x2(__uint_as_float(w[e] << 16), __uint_as_float(w[e] & 0xFFFF0000u));
-          x[c] = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        *reinterpret_cast<uint4*>(qs + (h * 8 + c) * 2048 + r * 16) = x[c];
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
-    };
-    PItem next = {};
-    auto take_next = [&](int idx, int i) -> bool {  // whether the i-th item is there and has MMA work
-      next.ok = false;
-      next.nkt = 0;
-      if (idx < num_items) {
-        bool up;
-        next = get_item(i, false, up);
-        ok = ok && up;
-      }
-      return next.ok && next.nkt > 0;
-    };
-    if (take_next(blockIdx.x, kCompact ? 0 : blockIdx.x) && kFour) {
-      uint4 x[8];
-      load_q(next, x);
-      stage_q(x);
-    }
     for (int idx = blockIdx.x, i = 0; idx < num_items; idx += gridDim.x, i += kCompact) {
       if (bar_red_or(kSoftBar, kSoftThreads, !ok || *abort_flag != 0)) break;
-      const PItem it = next;
+      bool up;
+      const PItem it = get_item(kCompact ? i : idx, false, up);
+      ok = ok && up;
       const int64_t row = it.row0 + r;  // (token, head) row within the sequence
       const bool my_row = row < it.rows;
       if (!it.ok) {  // invalid sequence (flagged by the dequant pass): 0 / -inf; beyond the chunk: nothing
         if (my_row) {
-          const int64_t at = q_row<kFour>(p, it, row);
+          const int64_t at = q_row<false>(p, it, row);
           for (int d = 0; d < 64; d += 4) {
-            if constexpr (kFour) *reinterpret_cast<uint2*>(p.out16 + at * kHeadDim + h * 64 + d) = make_uint2(0u, 0u);
-            else *reinterpret_cast<float4*>(p.out + at * kHeadDim + h * 64 + d) = make_float4(0.f, 0.f, 0.f, 0.f);
+            *reinterpret_cast<float4*>(p.out + at * kHeadDim + h * 64 + d) = make_float4(0.f, 0.f, 0.f, 0.f);
           }
           if (h == 0 && p.lse_out) p.lse_out[at] = -INFINITY;
         }
-        if (take_next(idx + gridDim.x, kCompact ? i + 1 : idx + gridDim.x) && kFour) {  // no MMA work for this item
-          uint4 x[8];
-          load_q(next, x);
-          stage_q(x);
-        }
-        continue;
+        continue;  // no MMA work for this item
       }
       // A piece's partial output rows (normalised) and log2-sum-exps, for the merge.
       float* part = it.piece >= 0 ? p.piece_o + (int64_t)it.piece * kRows * kHeadDim : nullptr;
@@ -868,27 +633,30 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         for (int d = 0; d < 64; d += 4)
           *reinterpret_cast<float4*>(part + r * kHeadDim + h * 64 + d) = make_float4(0.f, 0.f, 0.f, 0.f);
         if (h == 0) *part_lse = -INFINITY;
-        if (take_next(idx + gridDim.x, kCompact ? i + 1 : idx + gridDim.x) && kFour) {
-          uint4 x[8];
-          load_q(next, x);
-          stage_q(x);
-        }
         continue;
       }
-      if (!kFour) {
+      // This row's query (bf16), zero beyond the chunk: each half takes 8 of its 16 chunks.  (Staged while the last
+      // item ends, it cost the tile loop registers: 5% slower.)
+      {
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + q_row<false>(p, it, row) * kHeadDim) + h * 8;
         uint4 x[8];
-        load_q(it, x);
-        stage_q(x);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) x[c] = my_row ? __ldg(src + c) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) *reinterpret_cast<uint4*>(qs + (h * 8 + c) * 2048 + r * 16) = x[c];
       }
-      const int32_t p0 = p.prefix_len[kFour ? it.b / p.num_kv_heads : it.b];
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+      const int32_t p0 = p.prefix_len[it.b];
       const int q_pos = p0 + (int)(row >> p.log2_heads);
       const int k_lo = p.window > 0 ? max(0, q_pos + 1 - p.window) : 0;
       float m_ref = -INFINITY, l_sum = 0.0f;
       bool s_there = false;
       for (int j = 0; j < it.nkt; ++j, ++g) {
         const int sv = g % kStagesV, b = g % kPBuf;
-        ok = ((!kFour && __all_sync(0xffffffffu, s_there)) || mbar_wait_lean_warp(s_full, g & 1, wctl)) &&
-             (kFour || mbar_wait_polled_warp(&v_full[sv], (g / kStagesV) & 1, wctl));  // (for its K scales)
+        ok = (__all_sync(0xffffffffu, s_there) || mbar_wait_lean_warp(s_full, g & 1, wctl)) &&
+             mbar_wait_polled_warp(&v_full[sv], (g / kStagesV) & 1, wctl);  // (for its K scales)
         if (!ok) break;
         tc_fence_after();
         const float* kscale = reinterpret_cast<const float*>(smem + kOffV + sv * kVSlotBytes + kTileBytes) + h * 64;
@@ -910,9 +678,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           const uint64_t nm2 = f2(-m_use, -m_use);
 #pragma unroll
           for (int e = 0; e < 32; e += 4) {
-            const float sl = p.scale_log2;
-            const float4 a = kFour ? make_float4(sl, sl, sl, sl) : *reinterpret_cast<const float4*>(kscale + e);
-            const float4 a2 = kFour ? a : *reinterpret_cast<const float4*>(kscale + 32 + e);
+            const float4 a = *reinterpret_cast<const float4*>(kscale + e);
+            const float4 a2 = *reinterpret_cast<const float4*>(kscale + 32 + e);
             if constexpr (!kCompact) {
               f2_split(f2_fma(f2(__uint_as_float(r0[e]), __uint_as_float(r0[e + 1])), f2(a.x, a.y), nm2), z[e],
                        z[e + 1]);
@@ -1007,7 +774,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         }
         tmem_st_32x32b_x32(tmem + t_lane + kColP + b * 64 + h * 32, pw);
         l_sum += (l4[0] + l4[1]) + (l4[2] + l4[3]);
-        if constexpr (!kFour) s_there = mbar_test_wait(s_full, (g + 1) & 1);  // (1% slower with the 4-bit cache)
+        s_there = mbar_test_wait(s_full, (g + 1) & 1);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -1017,16 +784,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       // with w_h = 2^(m_h - M), M the larger reference; this thread writes its channel half.
       xref[h * kRows + r] = m_ref;
       xsum[h * kRows + r] = l_sum;
-      uint4 qx[8];  // (every S of this item is done: its Q may be overwritten)
-      const bool has_next = take_next(idx + gridDim.x, kCompact ? i + 1 : idx + gridDim.x);
-      if (kFour && has_next) load_q(next, qx);
       if (bar_red_or(kSoftBar, kSoftThreads, !ok)) break;
       const float m0 = xref[r], m1 = xref[kRows + r];
       const float M = fmaxf(m0, m1);
       const float w0 = m0 == -INFINITY ? 0.0f : ex2_approx(m0 - M);
       const float w1 = m1 == -INFINITY ? 0.0f : ex2_approx(m1 - M);
       const float Ls = w0 * xsum[r] + w1 * xsum[kRows + r];
-      if (kFour && has_next) stage_q(qx);
       ok = mbar_wait_polled_warp(o_full, n & 1, wctl);
       if (ok) {
         tc_fence_after();
@@ -1045,47 +808,27 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(o_empty);
-        if constexpr (kFour) {
-          if (my_row && part) {
-            float* dst = part + r * kHeadDim + h * 64;
+        // Lane q of 8 stores unit q (16 bytes) of the 8 rows from row8 on.
+        const int q = lane & 7, row8 = quarter * 32 + (lane & 24);
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) *reinterpret_cast<float4*>(dst + e) = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-          } else if (my_row) {
-            uint16_t* dst = p.out16 + q_row<kFour>(p, it, row) * kHeadDim + h * 64;
-            uint32_t x[32];
+        for (int c = 0; c < 64; c += 32) {
+          uint4 x[8];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = pack_bf16x2(o[2 * e], o[2 * e + 1]);
-            if ((reinterpret_cast<uintptr_t>(p.out16) & 31) == 0) {  // (a tensor's rows; else 16-byte aligned)
+          for (int u = 0; u < 8; ++u)
+            x[u] = make_uint4(__float_as_uint(o[c + 4 * u]), __float_as_uint(o[c + 4 * u + 1]),
+                              __float_as_uint(o[c + 4 * u + 2]), __float_as_uint(o[c + 4 * u + 3]));
+          transpose_units(x, q);
 #pragma unroll
-              for (int e = 0; e < 32; e += 8) st_global_v8(dst + 2 * e, &x[e]);
-            } else {
-#pragma unroll
-              for (int e = 0; e < 32; e += 4) *reinterpret_cast<uint4*>(dst + 2 * e) = make_uint4(x[e], x[e + 1], x[e + 2], x[e + 3]);
-            }
-          }
-        } else {
-          // Lane q of 8 stores unit q (16 bytes) of the 8 rows from row8 on.
-          const int q = lane & 7, row8 = quarter * 32 + (lane & 24);
-#pragma unroll
-          for (int c = 0; c < 64; c += 32) {
-            uint4 x[8];
-#pragma unroll
-            for (int u = 0; u < 8; ++u)
-              x[u] = make_uint4(__float_as_uint(o[c + 4 * u]), __float_as_uint(o[c + 4 * u + 1]),
-                                __float_as_uint(o[c + 4 * u + 2]), __float_as_uint(o[c + 4 * u + 3]));
-            transpose_units(x, q);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const int64_t to = it.row0 + row8 + i;
-              float* dst = part ? part + (row8 + i) * kHeadDim : p.out + q_row<kFour>(p, it, to) * kHeadDim;
-              if (to < it.rows) *reinterpret_cast<uint4*>(dst + h * 64 + c + q * 4) = x[i];
-            }
+          for (int i = 0; i < 8; ++i) {
+            const int64_t to = it.row0 + row8 + i;
+            float* dst = part ? part + (row8 + i) * kHeadDim : p.out + q_row<false>(p, it, to) * kHeadDim;
+            if (to < it.rows) *reinterpret_cast<uint4*>(dst + h * 64 + c + q * 4) = x[i];
           }
         }
         if (h == 0 && my_row) {
           const float lse2 = Ls > 0.0f ? M + __log2f(Ls) : -INFINITY;
           if (part_lse) *part_lse = lse2;
-          else if (p.lse_out) p.lse_out[q_row<kFour>(p, it, row)] = lse2 * kLn2;
+          else if (p.lse_out) p.lse_out[q_row<false>(p, it, row)] = lse2 * kLn2;
         }
       }
       ++n;
@@ -1110,15 +853,15 @@ __global__ void __launch_bounds__(256) combine_pieces_kernel(const __grid_consta
   ws.pieces = p.pieces;
   ws.num = p.num_items;
   const int split_tiles = (ws.num - ws.full) / ws.pieces;
-  if (w >= (int64_t)split_tiles * (kQT * kRows)) return;
-  const int sp = (int)(w / (kQT * kRows)), r = (int)(w % (kQT * kRows));
+  if (w >= (int64_t)split_tiles * kRows) return;
+  const int sp = (int)(w / kRows), r = (int)(w % kRows);
   const PItem it = prefill_item<kFour>(p, ws.full + sp * ws.pieces, nullptr, ws);
   const int64_t row = it.row0 + r;
   if (!it.ok || row >= it.rows) return;  // invalid sequence (its rows hold zeros) or past the chunk
   const int Hq = p.num_heads;
   const int my_i = (int)(row >> p.log2_heads), my_h = (int)(row & (Hq - 1));
   const int64_t t0 = (int64_t)sp * ws.pieces;
-  const float lj = lane < ws.pieces ? p.piece_lse[(t0 + lane) * (kQT * kRows) + r] : -INFINITY;
+  const float lj = lane < ws.pieces ? p.piece_lse[(t0 + lane) * kRows + r] : -INFINITY;
   float M = lj;
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
@@ -1129,7 +872,7 @@ __global__ void __launch_bounds__(256) combine_pieces_kernel(const __grid_consta
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int j = 0; j < ws.pieces; ++j) {
     const float wt = __shfl_sync(0xffffffffu, wj, j);
-    const float4 o = reinterpret_cast<const float4*>(p.piece_o + ((t0 + j) * (kQT * kRows) + r) * kHeadDim)[lane];
+    const float4 o = reinterpret_cast<const float4*>(p.piece_o + ((t0 + j) * kRows + r) * kHeadDim)[lane];
     acc.x = fmaf(wt, o.x, acc.x);
     acc.y = fmaf(wt, o.y, acc.y);
     acc.z = fmaf(wt, o.z, acc.z);
@@ -1152,7 +895,7 @@ __global__ void __launch_bounds__(256) combine_pieces_kernel(const __grid_consta
 // Partial outputs of the split last wave: at most one piece per CTA of the grid.  The
 // region is twice that: a varlen call's decode launch keeps its split partials there
 // (fewer splits when they would not fit), and half the room had cost it half its splits.
-static int64_t piece_bytes() { return (int64_t)num_sms() * 2 * (kQT * kRows) * (kHeadDim + 1) * 4; }
+static int64_t piece_bytes() { return (int64_t)num_sms() * 2 * kRows * (kHeadDim + 1) * 4; }
 
 size_t prefill_workspace_bytes(int32_t batch, int32_t max_pages_per_seq, int32_t page_size) {
   const int64_t kt = ((int64_t)max_pages_per_seq * page_size + kKeys - 1) / kKeys * kKeys;
@@ -1179,6 +922,27 @@ void prefill_piece_region(void* workspace, int32_t batch, int32_t max_pages_per_
 
 namespace {
 
+cudaError_t launch_attend8(const PrefillParams& p, int grid, cudaStream_t stream) {
+  static bool attr_set[64] = {};
+  int dev = 0;
+  cudaGetDevice(&dev);
+  if (dev >= 64 || !attr_set[dev]) {
+    // The register split inside the kernel assumes the launch register count.
+    cudaFuncAttributes fa;
+    for (const void* fn : {(const void*)prefill_kernel<false>, (const void*)prefill_kernel<true>}) {
+      cudaError_t e = cudaFuncGetAttributes(&fa, fn);
+      if (e != cudaSuccess) return e;
+      if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidDeviceFunction;
+      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytesMax);
+      if (e != cudaSuccess) return e;
+    }
+    if (dev < 64) attr_set[dev] = true;
+  }
+  if (p.compact) prefill_kernel<true><<<grid, kThreads, kSmemBytesMax, stream>>>(p);
+  else prefill_kernel<false><<<grid, kThreads, kSmemBytes, stream>>>(p);
+  return cudaGetLastError();
+}
+
 template <bool kFour>
 cudaError_t launch_kernels(PrefillParams p, cudaStream_t stream) {
   const int64_t seqs = (int64_t)p.batch * p.num_kv_heads;
@@ -1192,24 +956,9 @@ cudaError_t launch_kernels(PrefillParams p, cudaStream_t stream) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
 
-  static bool attr_set[64] = {};
-  int dev = 0;
-  cudaGetDevice(&dev);
-  if (dev < 64 && !attr_set[dev]) {
-    // The register split inside the kernel assumes the launch register count.
-    cudaFuncAttributes fa;
-    for (const void* fn : {(const void*)prefill_kernel<false, kFour>, (const void*)prefill_kernel<true, kFour>}) {
-      e = cudaFuncGetAttributes(&fa, fn);
-      if (e != cudaSuccess) return e;
-      if (fa.numRegs != kRegsLaunch) return cudaErrorInvalidDeviceFunction;
-      e = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytesMax);
-      if (e != cudaSuccess) return e;
-    }
-    attr_set[dev] = true;
-  }
-  // Work split (work_split) of a chunk call's q-tiles.  A varlen call's q-tiles are
-  // counted on the device (whole, no pieces); the dense count here is the fallback when
-  // they are too many to list.
+  // Work split (work_split) of a chunk call's items.  A varlen call's are counted on the
+  // device (whole, no pieces); the dense count here is the fallback when they are too many
+  // to list.
   const int64_t qtiles_total = seqs * p.qtiles;
   const int sms = num_sms();
   const int grid = (int)(qtiles_total < sms ? qtiles_total : sms);
@@ -1218,12 +967,8 @@ cudaError_t launch_kernels(PrefillParams p, cudaStream_t stream) {
   p.pieces = split.pieces;
   p.full_items = split.full;
   p.num_items = split.num;
-  const int smem = p.compact ? kSmemBytesMax : kSmemBytes;
-  if (p.compact)
-    prefill_kernel<true, kFour><<<grid, kThreads, smem, stream>>>(p);
-  else
-    prefill_kernel<false, kFour><<<grid, kThreads, smem, stream>>>(p);
-  e = cudaGetLastError();
+  if constexpr (kFour) e = launch_attend4(p, grid, stream);
+  else e = launch_attend8(p, grid, stream);
   if (e != cudaSuccess || split.pieces == 1) return e;
   const int64_t warps_c = (int64_t)(split.num - split.full) / split.pieces * kRows;  // one warp per row
   return launch_pdl(combine_pieces_kernel<kFour>, dim3((unsigned)((warps_c + 7) / 8)), dim3(256), 0, stream, p);
@@ -1250,7 +995,7 @@ cudaError_t launch_prefill(const PrefillLaunch& L, cudaStream_t stream) {
   p.log2_heads = 31 - __builtin_clz((unsigned)L.num_heads);
   p.window = L.window;
   p.kt_rows = (int32_t)(((int64_t)L.max_pages * L.page_size + kKeys - 1) / kKeys * kKeys);
-  p.qtiles = (int32_t)(((int64_t)L.n_new * L.num_heads + kQT * kRows - 1) / (kQT * kRows));
+  p.qtiles = (int32_t)(((int64_t)L.n_new * L.num_heads + kRows - 1) / kRows);
   p.scale_log2 = L.scale_log2;
   p.wait_ns = wait_limit_ns();
   p.drop_stage = fault_drop_stage();
@@ -1270,7 +1015,7 @@ cudaError_t launch_prefill(const PrefillLaunch& L, cudaStream_t stream) {
   p.ks = reinterpret_cast<float*>(ws + 2 * a);
   const int64_t sbytes = ((rows * 4 + 255) / 256) * 256;
   p.piece_o = reinterpret_cast<float*>(ws + 2 * a + 2 * sbytes);
-  p.piece_lse = p.piece_o + (int64_t)num_sms() * (kQT * kRows) * kHeadDim;
+  p.piece_lse = p.piece_o + (int64_t)num_sms() * kRows * kHeadDim;
   p.out = L.out;
   p.lse_out = L.lse_out;
   p.err = L.err;
