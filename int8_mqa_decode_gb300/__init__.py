@@ -535,27 +535,46 @@ class Rope:
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
-def _on_current(*tensors) -> None:
-    """The launch goes to the current device: tensors of another one are refused, not read across."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"a tensor is on {t.device}, the current device is cuda:{dev}")
+def _data(t: Optional[torch.Tensor], name: str, dev: int, dtype=None, shape=None) -> Optional[int]:
+    """_ptr for a call on device dev."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be a CUDA tensor of the current device")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if shape is not None and t.shape != shape:  # (torch.Size is a tuple)
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    return t.data_ptr()
 
 
-def _pools_of(pools, kind):
+def _stream_of(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+
+
+def _begin(pools, kind, t: torch.Tensor, name: str):
+    """(device, pool structs, pools) of a call with tensor t.  The launch goes to the current device, so tensors and
+    pools of another one are refused, not read across."""
     if isinstance(pools, kind):
-        _on_current(pools.pages)
-        return ctypes.byref(pools.struct), 1
+        pools = (pools,)
     for p in pools:
         if not isinstance(p, kind):
             raise TypeError(f"pools must be {kind.__name__} objects, got {type(p).__name__}")
-    _on_current(*[p.pages for p in pools])
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    for p in pools:
+        if p.pages.get_device() != dev:
+            raise ValueError(f"a pool is on {p.pages.device}, the current device is cuda:{dev}")
     n = len(pools)
     if n == 1:
-        return ctypes.byref(pools[0].struct), 1
+        return dev, ctypes.byref(pools[0].struct), 1
     struct = cai_kv_pool if kind is KVPool else cai_kv4_pool
-    return (struct * n)(*[p.struct for p in pools]), n
+    return dev, (struct * n)(*[p.struct for p in pools]), n
 
 
 def _rows(t: torch.Tensor, name: str, q_offsets, max_new, start_pos: torch.Tensor):
@@ -572,9 +591,7 @@ def _rows(t: torch.Tensor, name: str, q_offsets, max_new, start_pos: torch.Tenso
         raise ValueError(f"{name} has shape {tuple(n)}, expected [rows][heads][{HEAD_DIM}] with q_offsets")
     if max_new is None:
         raise ValueError("packed rows (q_offsets) need max_new")
-    batch = start_pos.shape[0]
-    _ptr(q_offsets, "q_offsets", torch.int32, (batch + 1,))
-    return n[0], batch, int(max_new), n[1]
+    return n[0], start_pos.shape[0], int(max_new), n[1]
 
 
 def _row_stride(t: torch.Tensor, name: str) -> int:
@@ -595,46 +612,47 @@ def _row_stride(t: torch.Tensor, name: str) -> int:
     return width if (n[0] if len(n) == 3 else n[0] * n[1]) == 1 else step
 
 
-def _cuda(t: torch.Tensor, name: str) -> int:
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    return t.data_ptr()
-
-
-def _table(block_table: torch.Tensor, batch: int):
+def _table(block_table: torch.Tensor, batch: int, dev: int):
     n = block_table.shape
     if len(n) != 2 or n[0] != batch:
         raise ValueError(f"block_table has shape {tuple(n)}, expected [{batch}][max_pages]")
-    return _ptr(block_table, "block_table", torch.int32), n[1]
+    return _data(block_table, "block_table", dev, torch.int32), n[1]
 
 
 def _append_rows(entry: str, kind, pools, k_new, v_new, block_table, start_pos, rope, q, q_out, q_offsets, max_new,
                  err_flag, stream) -> None:
-    arr, hkv = _pools_of(pools, kind)
+    dev, arr, hkv = _begin(pools, kind, k_new, "k_new")
     rows, batch, n_new, heads = _rows(k_new, "k_new", q_offsets, max_new, start_pos)
     if heads != hkv or v_new.shape != k_new.shape:
         raise ValueError(f"k_new and v_new must have one shape with {hkv} heads, got {tuple(k_new.shape)} and "
                          f"{tuple(v_new.shape)}")
-    kv_type = _DTYPES.get(k_new.dtype)
-    if kv_type is None or v_new.dtype != k_new.dtype:
+    dtype = k_new.dtype
+    kv_type = _DTYPES.get(dtype)
+    if kv_type is None or v_new.dtype is not dtype:
         raise TypeError(f"k_new and v_new must both be fp32 or bf16, got {k_new.dtype} and {v_new.dtype}")
+    if v_new.get_device() != dev or (q is not None and q.get_device() != dev):
+        raise ValueError("v_new and q must be CUDA tensors of the current device")
     hq, q_stride, q_ptr, out_ptr = 0, 0, None, None
     if q is not None or q_out is not None:
         if q is None or q_out is None:
             raise ValueError("q and q_out go together")
-        if q.dim() != k_new.dim() or q.shape[:-2] != k_new.shape[:-2] or q.shape[-1] != HEAD_DIM or q.dtype != torch.bfloat16:
+        n = q.shape
+        if len(n) != len(k_new.shape) or n[:-2] != k_new.shape[:-2] or n[-1] != HEAD_DIM or q.dtype is not torch.bfloat16:
             raise ValueError("q must be bf16, with the rows of k_new")
-        hq, q_stride, q_ptr = q.shape[-2], _row_stride(q, "q"), _cuda(q, "q")
-        out_ptr = _ptr(q_out, "q_out", torch.bfloat16, q.shape)
-    table, width = _table(block_table, batch)
-    _on_current(k_new, v_new, q, q_out, block_table, start_pos, q_offsets, err_flag)
+        hq, q_stride, q_ptr = n[-2], _row_stride(q, "q"), q.data_ptr()
+        out_ptr = _data(q_out, "q_out", dev, torch.bfloat16, n)
+    table, width = _table(block_table, batch, dev)
+    cos_sin = None
     if rope is not None:
-        _on_current(rope.cos, rope.sin)
+        if rope.cos.get_device() != dev or rope.sin.get_device() != dev:
+            raise ValueError("the rotation's tables must be on the current device")
+        cos_sin = ctypes.byref(rope.struct)
     st = getattr(load(), entry)(
-        arr, hkv, ctypes.byref(rope.struct) if rope is not None else None, _cuda(k_new, "k_new"), _cuda(v_new, "v_new"),
-        kv_type, _row_stride(k_new, "k_new"), _row_stride(v_new, "v_new"), q_ptr, q_stride, out_ptr, hq, batch, n_new,
-        q_offsets.data_ptr() if q_offsets is not None else None, rows, table, width,
-        _ptr(start_pos, "start_pos", torch.int32, (batch,)), _ptr(err_flag, "err_flag", torch.int32), _stream(stream))
+        arr, hkv, cos_sin, k_new.data_ptr(), v_new.data_ptr(), kv_type, _row_stride(k_new, "k_new"),
+        _row_stride(v_new, "v_new"), q_ptr, q_stride, out_ptr, hq, batch, n_new,
+        _data(q_offsets, "q_offsets", dev, torch.int32, (batch + 1,)), rows, table, width,
+        _data(start_pos, "start_pos", dev, torch.int32, (batch,)), _data(err_flag, "err_flag", dev, torch.int32),
+        _stream_of(stream, dev))
     _check(st, entry)
 
 
@@ -660,21 +678,23 @@ def cai_kv4_append(pools: Sequence[KV4Pool], k_new: torch.Tensor, v_new: torch.T
 
 def _read_rows(entry: str, kind, pools, k_out, v_out, block_table, start_pos, q_offsets, max_new, err_flag,
                stream) -> None:
-    arr, hkv = _pools_of(pools, kind)
     one = k_out if k_out is not None else v_out
     if one is None:
         raise ValueError("one of k_out and v_out must be given")
+    dev, arr, hkv = _begin(pools, kind, one, "k_out")
     rows, batch, n_new, heads = _rows(one, "k_out", q_offsets, max_new, start_pos)
-    if heads != hkv or (k_out is not None and v_out is not None and (v_out.shape != k_out.shape or v_out.dtype != k_out.dtype)):
+    if heads != hkv:
         raise ValueError(f"k_out and v_out must have one shape and dtype, with {hkv} heads")
-    if one.dtype not in _DTYPES:
+    dtype = one.dtype
+    out_type = _DTYPES.get(dtype)
+    if out_type is None:
         raise TypeError(f"outputs must be fp32 or bf16, got {one.dtype}")
-    table, width = _table(block_table, batch)
-    _on_current(k_out, v_out, block_table, start_pos, q_offsets, err_flag)
+    table, width = _table(block_table, batch, dev)
     st = getattr(load(), entry)(
-        arr, hkv, _ptr(k_out, "k_out"), _ptr(v_out, "v_out"), _DTYPES[one.dtype], batch, n_new,
-        q_offsets.data_ptr() if q_offsets is not None else None, rows, table, width,
-        _ptr(start_pos, "start_pos", torch.int32, (batch,)), _ptr(err_flag, "err_flag", torch.int32), _stream(stream))
+        arr, hkv, _data(k_out, "k_out", dev, dtype, one.shape), _data(v_out, "v_out", dev, dtype, one.shape), out_type, batch,
+        n_new, _data(q_offsets, "q_offsets", dev, torch.int32, (batch + 1,)), rows, table, width,
+        _data(start_pos, "start_pos", dev, torch.int32, (batch,)), _data(err_flag, "err_flag", dev, torch.int32),
+        _stream_of(stream, dev))
     _check(st, entry)
 
 
@@ -703,17 +723,17 @@ def cai_kv4_decode(pools: Sequence[KV4Pool], q: torch.Tensor, block_table: torch
                    out: torch.Tensor, lse_out: Optional[torch.Tensor] = None,
                    err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
     """One decode step of one layer over the 4-bit cache: q bf16 [batch][Hq][128] -> out bf16, one pool per K/V head."""
-    arr, hkv = _pools_of(pools, KV4Pool)
+    dev, arr, hkv = _begin(pools, KV4Pool, q, "q")
     batch, hq = q.shape[0], q.shape[1]
     shape = (batch, hq, HEAD_DIM)
-    table, width = _table(block_table, batch)
+    table, width = _table(block_table, batch, dev)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _on_current(q, block_table, ctx_len, workspace, out, lse_out, err_flag)
     st = load().cai_kv4_decode(
-        arr, hkv, _ptr(q, "q", torch.bfloat16, shape), batch, hq, table, width,
-        _ptr(ctx_len, "ctx_len", torch.int32, (batch,)), window, float(softmax_scale), num_splits,
-        _ptr(workspace, "workspace"), ws_bytes, _ptr(out, "out", torch.bfloat16, shape),
-        _ptr(lse_out, "lse_out", torch.float32, (batch, hq)), _ptr(err_flag, "err_flag", torch.int32), _stream(stream))
+        arr, hkv, _data(q, "q", dev, torch.bfloat16, shape), batch, hq, table, width,
+        _data(ctx_len, "ctx_len", dev, torch.int32, (batch,)), window, float(softmax_scale), num_splits,
+        _data(workspace, "workspace", dev), ws_bytes, _data(out, "out", dev, torch.bfloat16, shape),
+        _data(lse_out, "lse_out", dev, torch.float32, (batch, hq)), _data(err_flag, "err_flag", dev, torch.int32),
+        _stream_of(stream, dev))
     _check(st, "cai_kv4_decode")
 
 
@@ -728,15 +748,15 @@ def cai_kv4_prefill(pools: Sequence[KV4Pool], q: torch.Tensor, block_table: torc
                     q_offsets: Optional[torch.Tensor] = None, max_new: Optional[int] = None, stream=None) -> None:
     """Attention of appended new tokens over the 4-bit cache: q bf16 [batch][n_new][Hq][128], or packed
     [rows][Hq][128] with q_offsets and max_new -> out bf16 of the same shape, lse_out without the last dimension."""
-    arr, hkv = _pools_of(pools, KV4Pool)
+    dev, arr, hkv = _begin(pools, KV4Pool, q, "q")
     rows, batch, n_new, hq = _rows(q, "q", q_offsets, max_new, prefix_len)
-    table, width = _table(block_table, batch)
+    table, width = _table(block_table, batch, dev)
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _on_current(q, block_table, prefix_len, workspace, out, lse_out, err_flag, q_offsets)
     st = load().cai_kv4_prefill(
-        arr, hkv, _ptr(q, "q", torch.bfloat16), batch, n_new, q_offsets.data_ptr() if q_offsets is not None else None,
-        rows, hq, table, width, _ptr(prefix_len, "prefix_len", torch.int32, (batch,)), window, float(softmax_scale),
-        _ptr(workspace, "workspace"), ws_bytes, _ptr(out, "out", torch.bfloat16, q.shape),
-        _ptr(lse_out, "lse_out", torch.float32, q.shape[:-1]), _ptr(err_flag, "err_flag", torch.int32),
-        _stream(stream))
+        arr, hkv, _data(q, "q", dev, torch.bfloat16), batch, n_new,
+        _data(q_offsets, "q_offsets", dev, torch.int32, (batch + 1,)), rows, hq, table, width,
+        _data(prefix_len, "prefix_len", dev, torch.int32, (batch,)), window, float(softmax_scale),
+        _data(workspace, "workspace", dev), ws_bytes, _data(out, "out", dev, torch.bfloat16, q.shape),
+        _data(lse_out, "lse_out", dev, torch.float32, q.shape[:-1]), _data(err_flag, "err_flag", dev, torch.int32),
+        _stream_of(stream, dev))
     _check(st, "cai_kv4_prefill")

@@ -12,8 +12,8 @@
 // lane quarter of tensor memory), a producer and an issuer warp, with operands, accumulators and references of its
 // own, so that a role runs ahead of the next as far as the buffers let it, and one set's latencies (a wait
 // on an mbarrier costs 150 cycles and more even when its phase is over) pass under the other's work; a
-// piece ends with the merge of the two.  A converter turns 32 keys of K, then 32 channels of V, into operands; a softmax thread has one
-// key and all heads and writes its weights as 16-byte rows of P^T.
+// piece ends with the merge of the two.  A converter turns 32 keys of K, then 32 channels of V, into operands;
+// a softmax thread has one key and all heads and writes its weights as 16-byte rows of P^T.
 // A head's running maximum is a reference that the set's softmax warps share, raised only when a logit
 // passes it by 2^8: the weights are written on the guess that none does, and one barrier of those four
 // warps says whether the guess held; if not, O^T is rescaled in tensor memory.
@@ -22,7 +22,11 @@
 // conversion that feeds them 353 whatever the number of warps), which at 32 heads leaves the
 // register kernel at 2100 cycles a tile per SM; here the products cost no issue slots (16 instructions
 // of 16 cycles at 32 heads, 32 at 64: elect.sync issues one every 16 cycles, a lane-0 branch one every
-// 46) and the bound is the conversion, about 250 issue slots a sub-partition and 16-key group.
+// 46).  Measured, 64 sequences of 16 to 131 thousand keys on one K/V head: 16 heads 172 us, 32 heads 187, 64 heads
+// 243 (the cache's bytes take 106 at the copy bandwidth); with mma.sync 188, 281 and 536.  A tile takes 1200
+// cycles up to 32 heads, of which the converters' instructions are 500 issue slots a sub-partition and the
+// softmax's and issuers' 300 more: the rest is waits and instruction cache misses.  At 64 heads, 1550 cycles, the
+// softmax is the longest role (64 heads a thread, 160 registers).
 #include <cmath>
 
 #include "decode4.cuh"
@@ -68,7 +72,7 @@ struct ShapeTc {
   static_assert(kSets * kSetCols <= 512, "tensor memory columns");
   // Registers a thread: launched with 96 (five warps on a sub-partition: 15360 of 16384), then the control and
   // converting warpgroups give up what the softmax takes.  The host checks the launch count.
-  static constexpr int kRegsLaunch = 96, kRegsCtl = HN == 64 ? 48 : 56, kRegsConv = HN == 64 ? 64 : 72, kRegsSoft = HN == 64 ? 152 : 136;
+  static constexpr int kRegsLaunch = 96, kRegsCtl = HN == 64 ? 48 : 56, kRegsConv = HN == 64 ? 56 : 72, kRegsSoft = HN == 64 ? 160 : 136;
   static_assert(128 * kRegsCtl + 256 * kRegsConv + 256 * kRegsSoft <= kRegsLaunch * kTcThreads, "register split");
 };
 
