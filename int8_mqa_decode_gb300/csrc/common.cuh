@@ -141,6 +141,7 @@ struct ReadRowsParams {
   void* k_out;                  // fp32 or bf16 [rows][Hkv][128]; either may be null
   void* v_out;
   int32_t* err;
+  int32_t groups;               // filled by the launch: groups of 16 positions that a sequence may have
 };
 
 // One decode launch over the 4-bit cache.  q_off / total_rows: as in DecodeJob.
@@ -241,7 +242,7 @@ cai_status cuda_status(cudaError_t e);
 cudaError_t launch_append(const AppendParams* ps, int n, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeParams& p, int page_size, cudaStream_t stream);
 cudaError_t launch_append_rows(AppendRowsParams p, bool four, bool bf16, cudaStream_t stream);
-cudaError_t launch_read_rows(const ReadRowsParams& p, bool four, bool bf16, cudaStream_t stream);
+cudaError_t launch_read_rows(ReadRowsParams p, bool four, bool bf16, cudaStream_t stream);
 cudaError_t launch_decode4(const Decode4Params& p, cudaStream_t stream);
 // Fills the split fields of p (batch, heads, page_size, max_pages and window given; num_splits 0: automatic) and
 // returns the workspace bytes that they need; place_decode4 then sets the workspace's pointers.

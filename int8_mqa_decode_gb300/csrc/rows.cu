@@ -16,6 +16,8 @@
 // eight heads of a token (a lane eight channels of every other head, 16-byte loads and stores, all
 // of them under way before the position and its part of the tables are known); and one block that
 // checks packed offsets.  Reads go by 16 aligned tokens too.
+#include <algorithm>
+
 #include "common.cuh"
 #include "kv4.cuh"
 #include "ptx.cuh"
@@ -351,6 +353,14 @@ __device__ __forceinline__ void append_row(const AppendRowsParams& p, int64_t ro
     store_row8(p.pages[h] + (int64_t)page * page_bytes(P), P, slot, is_v, lane, x);
 }
 
+// Whether sequence b has rows in the u-th group of 16 aligned positions from its first one on.
+template <class Params>
+__device__ __forceinline__ bool has_group(const Params& p, int b, int64_t u) {
+  const int n = new_rows(p, b).n;
+  const int64_t start = n > 0 ? p.start_pos[b] : 0;
+  return n > 0 && start + n > ((start >> 4) + u) * kBlk;
+}
+
 // The u-th group of 16 aligned positions that sequence b writes, head h's K and V, by a block: warp w takes
 // tokens w and w + 8.  K rows and the rows of a group that is not written whole go out as they come;
 // a whole group's V codes are gathered in shared memory ([token][channel] bytes).
@@ -439,7 +449,10 @@ __device__ __forceinline__ void append_group(const AppendRowsParams& p, int b, i
 
 // (Four blocks an SM at 64 registers, or three at 77: 6353 rows of 32 heads 30.2 or 34.5 us, a decode step of
 // 256 sequences 5.0 or 5.6.)
-template <bool kFour, class T>
+// kMany: there are fewer blocks than groups that every sequence might have; a block looks through its share of these, 32
+// at a time, for those with rows.  (A prompt of 4096 tokens beside 135 single ones, 8 K/V heads: 44 us, a block for each
+// possible group 350.)
+template <bool kFour, class T, bool kMany>
 __global__ void __launch_bounds__(kRowWarps * 32, 4) append_rows_kernel(const __grid_constant__ AppendRowsParams p) {
   __shared__ uint32_t codes[kBlk][kHeadDim / 4];
   grid_dependency_wait();
@@ -449,9 +462,33 @@ __global__ void __launch_bounds__(kRowWarps * 32, 4) append_rows_kernel(const __
   int64_t blk = blockIdx.x;
   if (blk < p.kv_blocks) {
     if (p.groups > 0) {
-      const int64_t i = over(blk, p.num_kv_heads);
-      const int b = (int)over(i, p.groups), h = (int)(blk - i * p.num_kv_heads);
-      append_group<kFour, T>(p, b, i - (int64_t)b * p.groups, h, codes);
+      auto place = [&](int64_t item, int& b, int64_t& u, int& h) {
+        const int64_t i = over(item, p.num_kv_heads);
+        h = (int)(item - i * p.num_kv_heads);
+        b = (int)over(i, p.groups);
+        u = i - (int64_t)b * p.groups;
+      };
+      int b, h;
+      int64_t u;
+      if constexpr (kMany) {
+        const int64_t items = (int64_t)p.batch * p.groups * p.num_kv_heads;
+        for (; blk < items; blk += 32ll * p.kv_blocks) {
+          const int64_t mine = blk + (int64_t)lane * p.kv_blocks;
+          bool rows_there = false;
+          if (mine < items) {
+            place(mine, b, u, h);
+            rows_there = has_group(p, b, u);
+          }
+          for (uint32_t m = __ballot_sync(0xffffffffu, rows_there); m; m &= m - 1) {  // (the same in all warps)
+            place(blk + (int64_t)(__ffs(m) - 1) * p.kv_blocks, b, u, h);
+            append_group<kFour, T>(p, b, u, h, codes);
+            __syncthreads();  // the codes are read
+          }
+        }
+      } else {
+        place(blk, b, u, h);
+        append_group<kFour, T>(p, b, u, h, codes);
+      }
       return;
     }
     const int64_t w = blk * kRowWarps + warp, row = over(w, 2 * p.num_kv_heads);
@@ -508,16 +545,10 @@ __device__ __forceinline__ void widen(const uint4& v, float (&x)[8]) {
 // One warp per (16 aligned tokens, K/V head, K or V).
 constexpr int kVRow = kHeadDim + 8;  // fp16 of a token's row in shared memory (bank spread)
 template <bool kFour, class T>
-__global__ void __launch_bounds__(kRowWarps * 32) read_rows_kernel(const __grid_constant__ ReadRowsParams p) {
-  __shared__ __align__(16) uint16_t stage[kFour ? kRowWarps : 1][kFour ? kBlk * kVRow : 8];
-  grid_dependency_wait();
-  grid_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int64_t w = (int64_t)blockIdx.x * kRowWarps + warp;
+__device__ __forceinline__ void read_group(const ReadRowsParams& p, int64_t w, int b, int lane, uint16_t* st) {
   const int units = 2 * p.num_kv_heads;
   const int64_t u = over(w, units);  // group of 16 positions, counted from start_pos's
   const int unit = (int)(w - u * units), h = unit >> 1;
-  const int b = blockIdx.y;
   const NewRows nr = new_rows(p, b);
   if (nr.n < 0 && w == 0 && lane == 0 && p.err) atomicOr(p.err, CAI_DEVERR_LENGTH);
   if (nr.n <= 0) return;
@@ -574,7 +605,6 @@ __global__ void __launch_bounds__(kRowWarps * 32) read_rows_kernel(const __grid_
     }
     if (vo) {
       // V comes a channel per lane: transposed 8 x 8 in registers, gathered to rows in shared memory.
-      uint16_t* st = stage[warp];
       const uint4 s0 = *reinterpret_cast<const uint4*>(blk + kBlkVs + t * 32);
       const uint4 s1 = *reinterpret_cast<const uint4*>(blk + kBlkVs + t * 32 + 16);
       const uint32_t sa[4] = {s0.x, s0.y, s0.z, s0.w}, sb[4] = {s1.x, s1.y, s1.z, s1.w};
@@ -641,38 +671,95 @@ __global__ void __launch_bounds__(kRowWarps * 32) read_rows_kernel(const __grid_
   }
 }
 
+// kMany: as in append_rows_kernel, a warp looking through the (sequence, group, unit) triples.
+template <bool kFour, class T, bool kMany>
+__global__ void __launch_bounds__(kRowWarps * 32) read_rows_kernel(const __grid_constant__ ReadRowsParams p) {
+  __shared__ __align__(16) uint16_t stage[kFour ? kRowWarps : 1][kFour ? kBlk * kVRow : 8];
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint16_t* st = stage[kFour ? warp : 0];
+  int64_t w = (int64_t)blockIdx.x * kRowWarps + warp;
+  if constexpr (kMany) {
+    const int units = 2 * p.num_kv_heads, groups = p.groups;
+    const int64_t items = (int64_t)p.batch * groups * units, step = (int64_t)gridDim.x * kRowWarps;
+    for (; w < items; w += 32 * step) {
+      const int64_t mine = w + lane * step;
+      bool rows_there = false;
+      if (mine < items) {
+        const int64_t i = over(mine, units);
+        const int b = (int)over(i, groups);
+        rows_there = has_group(p, b, i - (int64_t)b * groups);
+        if (mine == (int64_t)b * groups * units && new_rows(p, b).n < 0 && p.err) atomicOr(p.err, CAI_DEVERR_LENGTH);
+      }
+      for (uint32_t m = __ballot_sync(0xffffffffu, rows_there); m; m &= m - 1) {
+        const int64_t item = w + (__ffs(m) - 1) * step;
+        const int b = (int)over(over(item, units), groups);
+        read_group<kFour, T>(p, item - (int64_t)b * groups * units, b, lane, st);
+        __syncwarp();  // the staged rows are read
+      }
+    }
+  } else {
+    read_group<kFour, T>(p, w, blockIdx.y, lane, st);
+  }
+}
+
+}  // namespace
+
+namespace {
+
+// Groups of 16 positions that a sequence's new tokens touch at most, from any position.
+template <class Params>
+int32_t most_groups(const Params& p) {
+  return (int32_t)(((int64_t)(p.q_off ? std::min(p.n_new, p.total_new) : p.n_new) + 2 * kBlk - 2) / kBlk);
+}
+
+template <bool kFour, class T>
+cudaError_t launch_append_many(const AppendRowsParams& p, unsigned grid, bool many, cudaStream_t stream) {
+  return many ? launch_pdl(append_rows_kernel<kFour, T, true>, dim3(grid), dim3(kRowWarps * 32), 0, stream, p)
+              : launch_pdl(append_rows_kernel<kFour, T, false>, dim3(grid), dim3(kRowWarps * 32), 0, stream, p);
+}
+template <bool kFour, class T>
+cudaError_t launch_read_many(const ReadRowsParams& p, dim3 grid, bool many, cudaStream_t stream) {
+  return many ? launch_pdl(read_rows_kernel<kFour, T, true>, grid, dim3(kRowWarps * 32), 0, stream, p)
+              : launch_pdl(read_rows_kernel<kFour, T, false>, grid, dim3(kRowWarps * 32), 0, stream, p);
+}
+
 }  // namespace
 
 cudaError_t launch_append_rows(AppendRowsParams p, bool four, bool bf16, cudaStream_t stream) {
   const int64_t rows = p.q_off ? p.total_new : (int64_t)p.batch * p.n_new;
   const auto blocks = [](int64_t warps) { return (warps + kRowWarps - 1) / kRowWarps; };
   const int64_t q_blocks = blocks(rows * ((p.num_q_heads + kQHeads - 1) / kQHeads));
-  // Chunks by groups of 16 positions (n_new tokens from any position touch at most this many).
-  p.groups = p.n_new >= kBlk ? (p.n_new + 2 * kBlk - 2) / kBlk : 0;
-  const int64_t kv_blocks =
-      p.groups ? (int64_t)p.batch * p.groups * p.num_kv_heads : blocks(rows * 2 * p.num_kv_heads);
+  // Chunks by groups of 16 positions.
+  p.groups = p.n_new >= kBlk ? most_groups(p) : 0;
+  const int64_t seqs = (int64_t)p.batch * p.num_kv_heads;
+  // (Ragged batches: one wave of blocks that look for their groups.  6353 rows of 48 sequences 28.8 us, with a block
+  // for each possible group 30.1.)
+  const int64_t wave = (int64_t)num_sms() * 4;
+  const bool many = p.q_off && p.groups * seqs > wave;
+  const int64_t kv_blocks = many ? wave : p.groups ? seqs * p.groups : blocks(rows * 2 * p.num_kv_heads);
   const int64_t grid = q_blocks + kv_blocks + (p.q_off ? 1 : 0);
   if (grid > 2147483647ll) return cudaErrorInvalidValue;
   p.q_blocks = (int32_t)q_blocks;
   p.kv_blocks = (int32_t)kv_blocks;
   p.wide_tables = ((reinterpret_cast<uintptr_t>(p.cos) | reinterpret_cast<uintptr_t>(p.sin)) & 15) == 0;
-  const dim3 g((unsigned)grid), block(kRowWarps * 32);
-  if (four)
-    return bf16 ? launch_pdl(append_rows_kernel<true, uint16_t>, g, block, 0, stream, p)
-                : launch_pdl(append_rows_kernel<true, float>, g, block, 0, stream, p);
-  return bf16 ? launch_pdl(append_rows_kernel<false, uint16_t>, g, block, 0, stream, p)
-              : launch_pdl(append_rows_kernel<false, float>, g, block, 0, stream, p);
+  const unsigned g = (unsigned)grid;
+  if (four) return bf16 ? launch_append_many<true, uint16_t>(p, g, many, stream) : launch_append_many<true, float>(p, g, many, stream);
+  return bf16 ? launch_append_many<false, uint16_t>(p, g, many, stream) : launch_append_many<false, float>(p, g, many, stream);
 }
 
-cudaError_t launch_read_rows(const ReadRowsParams& p, bool four, bool bf16, cudaStream_t stream) {
-  // n_new tokens from any position touch at most this many groups of 16.
-  const int64_t warps = (((int64_t)p.n_new + 2 * kBlk - 2) / kBlk) * 2 * p.num_kv_heads;
-  const dim3 grid((unsigned)((warps + kRowWarps - 1) / kRowWarps), (unsigned)p.batch), block(kRowWarps * 32);
-  if (four)
-    return bf16 ? launch_pdl(read_rows_kernel<true, uint16_t>, grid, block, 0, stream, p)
-                : launch_pdl(read_rows_kernel<true, float>, grid, block, 0, stream, p);
-  return bf16 ? launch_pdl(read_rows_kernel<false, uint16_t>, grid, block, 0, stream, p)
-              : launch_pdl(read_rows_kernel<false, float>, grid, block, 0, stream, p);
+cudaError_t launch_read_rows(ReadRowsParams p, bool four, bool bf16, cudaStream_t stream) {
+  p.groups = most_groups(p);
+  const int64_t warps = (int64_t)p.groups * 2 * p.num_kv_heads;
+  const int64_t per = (warps + kRowWarps - 1) / kRowWarps;
+  // (Here looking for the groups pays only where most have no rows: 64 sequences of up to 1024 tokens, of four K/V
+  // heads, take 14 us with a warp for each possible group and 22 so; the prompt beside 135 tokens 75 and 12.)
+  const int64_t wave = (int64_t)num_sms() * 8;
+  const bool many = p.q_off && per * p.batch > 4 * wave;
+  const dim3 grid((unsigned)(many ? wave : per), (unsigned)(many ? 1 : p.batch));
+  if (four) return bf16 ? launch_read_many<true, uint16_t>(p, grid, many, stream) : launch_read_many<true, float>(p, grid, many, stream);
+  return bf16 ? launch_read_many<false, uint16_t>(p, grid, many, stream) : launch_read_many<false, float>(p, grid, many, stream);
 }
 
 }  // namespace cai

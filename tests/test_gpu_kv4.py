@@ -184,6 +184,26 @@ def test_append_packed(four, i):
     append_case(four, APPENDS[i], True, seed=i, slices=i % 2 == 0)
 
 
+MANY = (5, 2, 16, 128, False, True, [1 if i % 40 else 230 for i in range(300)] + [0, 17], [(i * 7) % 70 for i in range(302)])
+
+
+@pytest.mark.parametrize("four", [False, True])
+def test_append_and_read_of_long_beside_many_single_tokens(four):
+    """A batch whose longest sequence would give every other one blocks without rows."""
+    pools, table, new, start, kr, vr = append_case(four, MANY, True, seed=30)
+    kw = dict(q_offsets=dev(np.concatenate([[0], np.cumsum(new)]).astype(np.int32)), max_new=int(new.max()))
+    k, v = (torch.full(kr.shape, float("nan"), device=DEV) for _ in range(2))
+    (cai.cai_kv4_read if four else cai.cai_kv_read)(pools, k, v, table, dev(start.astype(np.int32)), **kw)
+
+    def want(x):
+        if four:
+            return kv4.dequantize4(*kv4.quantize4(x)).astype(np.float32)
+        c, s = oracle.quantize_rows(x.reshape(-1, 128))
+        return (c.astype(np.float32) * s[:, None]).reshape(x.shape)
+
+    assert np.array_equal(host(k), want(kr)) and np.array_equal(host(v), want(vr))
+
+
 @pytest.mark.parametrize("four", [False, True])
 @pytest.mark.parametrize("n", [1, 19])
 def test_append_equal_counts(four, n):
