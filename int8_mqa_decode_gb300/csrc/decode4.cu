@@ -17,6 +17,10 @@
 // to the B operand by an 8 x 8 transpose in registers, and O^T += V^T P^T accumulates channels x heads
 // in registers.  At the end of a piece the warps' parts are merged through the ring's shared memory.
 //
+// Roundings, here and in decode4_tc.cu: the query to fp16 (exact within fp16's range), a weight to fp16 for its
+// product with V (2^-11 of it; the sums take it unrounded, in fp32), the output to bf16 once; partial outputs stay
+// fp32.
+//
 // Why this tensor path: at up to 8 heads a 16-key group's 32 m16n8k16 and the conversion of its codes take
 // a sub-partition about as long as its bytes take the SM at the copy bandwidth (long contexts of 8 heads:
 // 142 us for 4.97 M keys, of 106 at the copy bandwidth).  The tensor memory kernel's products are padded

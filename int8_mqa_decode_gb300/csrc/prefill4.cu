@@ -13,6 +13,9 @@
 // S after PV in the same columns: 1740 a q-tile and tile, half of it the way from P to the next S.)
 // The softmax is that of prefill.cu: a reference per row, raised when a logit passes it by 2^8.
 //
+// Roundings: the query to fp16 (exact within fp16's range), a weight to fp16 for its product with V (2^-11 of it; the sums
+// take it unrounded, in fp32), the output to bf16 once; a piece's partial output stays fp32.
+//
 // Bound: 16 products of 64 cycles a tile, and the exponentials, 512 cycles a sub-partition.
 #include "prefill.cuh"
 
