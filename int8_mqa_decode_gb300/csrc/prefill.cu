@@ -59,6 +59,9 @@ constexpr int kOffBars = kOffXch + 4 * kRows * 4;
 // the MMA issuers' last commits; item_full, item_empty [kItemSlots].
 constexpr int kNumBars = 2 * kStagesK + 2 * kStagesV + 1 + 2 + 3 * kPBuf + 2 + 1 + 2 * kItemSlots;
 constexpr int kOffMisc = kOffBars + 8 * kNumBars;
+// A varlen call's item list (see PrefillParams::compact): its count, then the dense
+// number of each item, in shared memory that only such a launch asks for.
+constexpr int kMaxCompactItems = 4096;
 // Varlen dequant: sequences whose tiles one block numbers in shared memory.
 constexpr int kMaxCompactSeqs = 8192;
 constexpr int kOffItems = (kOffMisc + 32 + 15) & ~15;  // after the tmem slot and the wait state (+8): items, 64 bytes each
@@ -335,6 +338,34 @@ __global__ void __launch_bounds__(256) dequant_compact_kernel(const __grid_const
   }
 }
 
+// The list of a varlen call's items (by one warp): lane l sums the items of a run of sequences, a warp scan gives
+// each run its first item, and each lane writes its run's items.  hdr: the count, -1 (the dense numbering) when they
+// do not fit.
+__device__ __forceinline__ void list_items(const PrefillParams& p, int32_t* hdr, int lane) {
+  int32_t* list = hdr + 4;
+  const int nb = p.batch;
+  const int per = (nb + 31) / 32;
+  const int b0 = min(nb, lane * per), b1 = min(nb, b0 + per);
+  int sum = 0;
+  for (int b = b0; b < b1; ++b) sum += seq_qtiles(p, b);
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  const int total = __shfl_sync(0xffffffffu, incl, 31);
+  if (total <= kMaxCompactItems) {
+    int run = incl - sum;
+    for (int b = b0; b < b1; ++b) {
+      const int n = seq_qtiles(p, b);
+      for (int j = 0; j < n; ++j) list[run + j] = b * p.qtiles + j;
+      run += n;
+    }
+  }
+  if (lane == 0) *hdr = total <= kMaxCompactItems ? total : -1;
+}
+
 // Rows of 8 units of 16 bytes, one per lane: lane q of 8 leaves with unit q of the 8 rows, so that a store of
 // the 8 lanes covers a whole 128-byte line (32 lines an instruction, a row per lane, took the epilogue
 // 4300 cycles; so they take 1/8).
@@ -435,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     fence_barrier_init();
   }
   if (kCompact && warp == 3) {
-    list_items<false>(p, reinterpret_cast<int32_t*>(smem + kOffTable), lane);
+    list_items(p, reinterpret_cast<int32_t*>(smem + kOffTable), lane);
   }
   tc_fence_before();
   __syncthreads();

@@ -9,9 +9,6 @@ namespace cai {
 constexpr int kRows = 128;                 // query rows per q-tile (MMA M)
 constexpr int kKeys = 128;                 // keys per tile (MMA N of S, K of PV)
 constexpr int kTileBytes = kKeys * kHeadDim * 2;  // 32 KB of 16-bit values
-// A varlen call's item list (see PrefillParams::compact): its count, then the dense
-// number of each item, in shared memory that only such a launch asks for.
-constexpr int kMaxCompactItems = 4096;
 constexpr int kItemSlots = 4;              // items handed from one warp to the other roles
 
 struct PrefillParams {
@@ -36,7 +33,7 @@ struct PrefillParams {
   // through a list of their dense numbers that every CTA builds at its start (the dense
   // numbering, qtiles slots per sequence for the longest one, would make the grid walk
   // the empty slots of every short or one-token sequence); past kMaxCompactItems real
-  // q-tiles, the dense numbering.  No pieces then.
+  // q-tiles, the dense numbering.  No pieces then.  (With the 4-bit cache one warp walks the sequences instead.)
   int32_t compact;
   float* piece_o;
   float* piece_lse;
@@ -91,11 +88,9 @@ struct PItem {
   int piece;      // -1: the whole key range; otherwise the piece's slot in piece_o / piece_lse
 };
 
-// q-tiles holding rows of sequence b (0 when it has no rows in this call); with the 4-bit cache, of
-// (sequence, K/V head) b.
-template <bool kFour>
+// q-tiles holding rows of sequence b (0 when it has no rows in this call), for each of its K/V heads.
 __device__ __forceinline__ int seq_qtiles(const PrefillParams& p, int b) {
-  const SeqRows sr = seq_rows(p, kFour ? b / p.num_kv_heads : b);
+  const SeqRows sr = seq_rows(p, b);
   return sr.n > 0 ? (int)(((int64_t)sr.n * p.num_heads + kRows - 1) / kRows) : 0;
 }
 
@@ -168,35 +163,6 @@ __device__ __forceinline__ PItem prefill_item(const PrefillParams& p, int idx, c
     it.nkt = e - a;
   }
   return it;
-}
-
-// The list of a varlen call's items (by one warp): lane l sums the items of a run of sequences, a warp scan gives
-// each run its first item, and each lane writes its run's items.  hdr: the count, -1 (the dense numbering) when they
-// do not fit.
-template <bool kFour>
-__device__ __forceinline__ void list_items(const PrefillParams& p, int32_t* hdr, int lane) {
-  int32_t* list = hdr + 4;
-  const int nb = kFour ? p.batch * p.num_kv_heads : p.batch;
-  const int per = (nb + 31) / 32;
-  const int b0 = min(nb, lane * per), b1 = min(nb, b0 + per);
-  int sum = 0;
-  for (int b = b0; b < b1; ++b) sum += seq_qtiles<kFour>(p, b);
-  int incl = sum;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  const int total = __shfl_sync(0xffffffffu, incl, 31);
-  if (total <= kMaxCompactItems) {
-    int run = incl - sum;
-    for (int b = b0; b < b1; ++b) {
-      const int n = seq_qtiles<kFour>(p, b);
-      for (int j = 0; j < n; ++j) list[run + j] = b * p.qtiles + j;
-      run += n;
-    }
-  }
-  if (lane == 0) *hdr = total <= kMaxCompactItems ? total : -1;
 }
 
 // Attention over the copy of a 4-bit cache (prefill4.cu).

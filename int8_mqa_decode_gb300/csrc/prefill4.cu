@@ -31,8 +31,7 @@ constexpr int kOffBars4 = kOffXch4 + 4 * kRows * 4;
 constexpr int kNumBars4 = 2 * kStagesK4 + 2 * kStagesV4 + 1 + 2 + 4 + 2 + 1 + 1 + 2 * kItemSlots;
 constexpr int kOffMisc4 = kOffBars4 + 8 * kNumBars4;             // tensor memory slot, wait state
 constexpr int kOffItems4 = (kOffMisc4 + 32 + 15) & ~15;          // items, 64 bytes each
-constexpr int kOffTable4 = kOffItems4 + kItemSlots * 64;
-constexpr int kSmem4 = kOffTable4 + (kMaxCompactItems + 4) * 4;
+constexpr int kSmem4 = kOffItems4 + kItemSlots * 64;
 static_assert(sizeof(PItem) <= 64 && kSmem4 <= 227 * 1024, "shared memory");
 // Warpgroup 0: producer, the issuers of S and of PV, items; warpgroups 1 and 2: softmax of key half 0 and 1.
 constexpr int kThreads4 = 384;
@@ -93,26 +92,17 @@ __global__ void __launch_bounds__(kThreads4, 1) attend4_kernel(const __grid_cons
     wctl->limit_ns = p.wait_ns;
     fence_barrier_init();
   }
-  int32_t* hdr = reinterpret_cast<int32_t*>(smem + kOffTable4);
-  if (kCompact && warp == 3) list_items<true>(p, hdr, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
   if (kCompact) grid_launch_dependents();  // (as in prefill.cu)
-  const int n_list = kCompact ? *hdr : -1;
-  const int32_t* table = n_list >= 0 ? hdr + 4 : nullptr;
-  WorkSplit ws;
-  ws.full = p.full_items;
-  ws.pieces = p.pieces;
-  ws.num = n_list >= 0 ? n_list : p.num_items;
-  // This block's items: blockIdx.x, + gridDim.x, ...
-  const int mine = (int)blockIdx.x < ws.num ? (ws.num - 1 - (int)blockIdx.x) / (int)gridDim.x + 1 : 0;
   bool ok = true;  // no wait of this warp gave up
-  // The block's i-th item; the slot is free again on return.
+  // The block's i-th item, nkt < 0 past its last; the slot is free again on return.
   auto get_item = [&](int i) -> PItem {
     const int s = i % kItemSlots;
     PItem it = {};
+    it.nkt = -1;
     ok = mbar_wait_lean_warp(&item_full[s], (i / kItemSlots) & 1, wctl);
     if (!ok) return it;
     it = items[s];
@@ -126,8 +116,9 @@ __global__ void __launch_bounds__(kThreads4, 1) attend4_kernel(const __grid_cons
     if (warp == 0) {
       // ------------------------------------------------------------ K/V producer
       int g = 0, gk = 0, gv = 0;  // tiles; tiles whose K and V loads were issued (or dropped)
-      for (int i = 0; i < mine && ok; ++i) {
+      for (int i = 0;; ++i) {
         const PItem it = get_item(i);
+        if (!ok || it.nkt < 0) break;
         const uint16_t* kb = p.kb + ((int64_t)it.b * p.kt_rows + (int64_t)it.kt0 * kKeys) * kHeadDim;
         const uint16_t* vh = p.vh + ((int64_t)it.b * p.kt_rows + (int64_t)it.kt0 * kKeys) * kHeadDim;
         for (int j = 0; j < it.nkt && ok; ++j, ++g) {
@@ -160,8 +151,9 @@ __global__ void __launch_bounds__(kThreads4, 1) attend4_kernel(const __grid_cons
       const uint64_t dk0 = smem_desc(smem_addr(smem + kOffK4), 2048, 128);
       const uint64_t dv0 = smem_desc(smem_addr(smem + kOffV4), 128, 2048);
       int g = 0, n = 0;  // tiles, items
-      for (int i = 0; i < mine && ok; ++i) {
+      for (int i = 0; ok; ++i) {
         const PItem it = get_item(i);
+        if (it.nkt < 0) break;
         if (!it.ok || it.nkt == 0) continue;  // no products; the softmax writes its zeros
         if (warp == 1) {
           ok = mbar_wait_lean_warp(q_full, n & 1, wctl);
@@ -213,15 +205,49 @@ __global__ void __launch_bounds__(kThreads4, 1) attend4_kernel(const __grid_cons
       mbar_wait_drain(drain, 0);
     } else {
       // ------------------------------------------------------------ items
-      // Works out the items ahead of the other roles and brings their queries into L2.
-      for (int i = 0; i < mine && !abort_seen_warp(wctl); ++i) {
-        const PItem it = prefill_item<true>(p, blockIdx.x + i * gridDim.x, table, ws);
+      // Works out the items ahead of the other roles and brings their queries into L2.  A varlen call's are numbered
+      // without the empty q-tiles that the longest sequence gives the others: lane l has the q-tiles of one sequence of
+      // a window of 32, and the window moves on.
+      WorkSplit ws;
+      ws.full = p.full_items;
+      ws.pieces = p.pieces;
+      ws.num = p.num_items;
+      int w0 = -32, n = 0, incl = 0, window = 0;  // first sequence; this lane's q-tiles, items up to it; the window's items
+      int64_t before = 0;                         // items before the window
+      for (int i = 0; !abort_seen_warp(wctl); ++i) {
+        const int64_t at = blockIdx.x + (int64_t)i * gridDim.x;
+        PItem it = {};
+        it.nkt = -1;
+        if constexpr (kCompact) {
+          while (w0 < p.batch && at >= before + window) {
+            before += window;
+            w0 += 32;
+            n = w0 + lane < p.batch ? seq_qtiles(p, w0 + lane) : 0;
+            incl = n * p.num_kv_heads;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+              const int v = __shfl_up_sync(0xffffffffu, incl, o);
+              if (lane >= o) incl += v;
+            }
+            window = __shfl_sync(0xffffffffu, incl, 31);
+          }
+          if (w0 < p.batch) {
+            const int rel = (int)(at - before), l = __ffs(__ballot_sync(0xffffffffu, incl > rel)) - 1;
+            const int nl = __shfl_sync(0xffffffffu, n, l);
+            const int e = rel - (__shfl_sync(0xffffffffu, incl, l) - nl * p.num_kv_heads), h = e / nl;
+            it = prefill_item<true>(p, ((w0 + l) * p.num_kv_heads + h) * p.qtiles + (e - h * nl), nullptr, ws);
+          }
+        } else if (at < ws.num) {
+          it = prefill_item<true>(p, (int)at, nullptr, ws);
+        }
         const int s = i % kItemSlots;
         if (i >= kItemSlots && !mbar_wait_asleep_warp(&item_empty[s], (i / kItemSlots - 1) & 1, wctl)) break;
         if (lane == 0) {
           items[s] = it;
           mbar_arrive(&item_full[s]);
         }
+        __syncwarp();
+        if (it.nkt < 0) break;
         if (it.ok && it.nkt > 0) {
           for (int k = 0; k < kRows / 16; ++k) {
             const int64_t row = it.row0 + k * 16 + (lane >> 1);
@@ -259,17 +285,16 @@ __global__ void __launch_bounds__(kThreads4, 1) attend4_kernel(const __grid_cons
       if (lane == 0) mbar_arrive(q_full);
     };
     int g = 0;  // tiles
-    PItem next = {};
-    if (mine > 0) next = get_item(0);
+    PItem next = get_item(0);
     if (ok && has_products(next)) {
       uint4 x[8];
       load_q(next, x);
       stage_q(x);
     }
     const uint64_t sl2 = f2(p.scale_log2, p.scale_log2);
-    for (int i = 0; i < mine; ++i) {
+    for (int i = 0;; ++i) {
       // The eight warps meet at an item's start (the exchange is read) and merge; there they stop together.
-      if (bar_red_or(kBarSoft4, 256, !ok)) break;
+      if (bar_red_or(kBarSoft4, 256, !ok) || next.nkt < 0) break;
       const PItem it = next;
       const int64_t row = it.row0 + r;  // (token, head) row within the sequence
       const bool my_row = row < it.rows;
@@ -286,13 +311,11 @@ __global__ void __launch_bounds__(kThreads4, 1) attend4_kernel(const __grid_cons
           for (int d = 0; d < 64; d += 4) *reinterpret_cast<float4*>(part + d) = make_float4(0.f, 0.f, 0.f, 0.f);
           if (h == 0) *part_lse = -INFINITY;
         }
-        if (i + 1 < mine) {
-          next = get_item(i + 1);
-          if (ok && has_products(next)) {
-            uint4 x[8];
-            load_q(next, x);
-            stage_q(x);
-          }
+        next = get_item(i + 1);
+        if (ok && has_products(next)) {
+          uint4 x[8];
+          load_q(next, x);
+          stage_q(x);
         }
         continue;
       }
@@ -387,7 +410,7 @@ __global__ void __launch_bounds__(kThreads4, 1) attend4_kernel(const __grid_cons
       xsum[h * kRows + r] = l_sum;
       bool staged = false;
       uint4 qx[8];
-      if (ok && i + 1 < mine) {
+      if (ok) {
         next = get_item(i + 1);
         staged = ok && has_products(next);
         if (staged) load_q(next, qx);
