@@ -152,6 +152,7 @@ struct Decode4Params {
   int32_t page_size, max_pages, window;
   const int32_t* table;    // [B][max_pages]
   const int32_t* ctx_len;  // [B]
+  int32_t before_new;      // ctx_len does not count the new token (prefill calls)
   const int32_t* q_off;    // nullable
   int32_t total_rows;
   const uint16_t* q;       // bf16 bits

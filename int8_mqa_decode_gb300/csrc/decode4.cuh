@@ -34,8 +34,8 @@ __device__ __forceinline__ bool seq_keys(const Decode4Params& p, int b, int32_t&
     const int32_t a = p.q_off[b], e = p.q_off[b + 1];
     if (!(a >= 0 && e == a + 1 && e <= p.total_rows)) return false;  // a chunk: the prefill kernel's
     row = a;
-    L = L < 0 || L >= p.max_pages * p.page_size ? -1 : L + 1;        // the length before the new token was given
   }
+  if (p.before_new) L = L < 0 || L >= p.max_pages * p.page_size ? -1 : L + 1;
   sp = seq_splits(L, p.window, p.max_pages * p.page_size, p.chunk > 0 ? p.chunk : 1);
   return true;
 }

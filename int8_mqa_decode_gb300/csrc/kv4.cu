@@ -314,8 +314,13 @@ cai_status cai_kv4_prefill(const cai_kv4_pool* kv_pools, int32_t num_kv_heads, c
   // behind the prefill without waiting for it (disjoint output rows, and a part of the workspace of its own).
   L.skip_single = q_offsets != nullptr;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = launch_prefill(L, s);
-  if (e != cudaSuccess || !L.skip_single) return cuda_status(e);
+  // One new token for every sequence: decode alone (64 sequences of 4000, 8 K/V heads: 71 us, through the copy
+  // 380).
+  const bool all_single = !q_offsets && n_new == 1;
+  if (!all_single) {
+    const cudaError_t e = launch_prefill(L, s);
+    if (e != cudaSuccess || !L.skip_single) return cuda_status(e);
+  }
   Decode4Params d = {};
   fill_pools(kv_pools, num_kv_heads, d);
   d.num_heads = num_q_heads;
@@ -324,6 +329,7 @@ cai_status cai_kv4_prefill(const cai_kv4_pool* kv_pools, int32_t num_kv_heads, c
   d.window = window;
   d.table = block_table;
   d.ctx_len = prefix_len;
+  d.before_new = 1;
   d.q_off = q_offsets;
   d.total_rows = (int32_t)rows;
   d.q = q;
@@ -335,7 +341,7 @@ cai_status cai_kv4_prefill(const cai_kv4_pool* kv_pools, int32_t num_kv_heads, c
   d.err = err_flag;
   d.wait_ns = wait_limit_ns();
   d.drop_stage = fault_drop_stage();
-  d.overlap_prev = 1;
+  d.overlap_prev = !all_single;
   return cuda_status(launch_decode4(d, s));
 }
 

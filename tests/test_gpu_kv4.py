@@ -621,6 +621,31 @@ def test_prefill_single_rows_alone_and_decode_agree():
     check_prefill(cache, q, [n - 1 for n in lengths], [1] * 4, max_new=9)
 
 
+def test_prefill_of_one_token_each_is_a_decode_step():
+    """Without offsets, too: the same rows, flags and edges as through the decode call."""
+    lengths = [77, 500, 1, 2000]
+    cache = Cache(lengths, 2, 16, seed=19)
+    q = queries(np.random.default_rng(19), 4, 32)
+    want = decode(cache, q, lengths)
+    ws = torch.full((cai.cai_kv4_prefill_workspace_size(4, 32, 2, cache.table.shape[1], 16),), 0xFF, dtype=torch.uint8, device=DEV)
+
+    def run(prefix):
+        out = torch.full((4, 1, 32, 128), 5.0, dtype=torch.bfloat16, device=DEV)
+        lse = torch.full((4, 1, 32), 5.0, device=DEV)
+        err = flag()
+        cai.cai_kv4_prefill(cache.pools, q[:, None], cache.table, dev(np.array(prefix, np.int32)), 0, SCALE, ws, out, lse, err)
+        return out[:, 0], lse[:, 0], int(err.item())
+
+    out, lse, err = run([n - 1 for n in lengths])
+    assert err == 0 and torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    out, lse, err = run([76, -1, 0, cache.table.shape[1] * 16])
+    assert err == cai.CAI_DEVERR_LENGTH
+    for b in (1, 3):
+        assert (out[b] == 0).all() and (lse[b] == -float("inf")).all()
+    for b in (0, 2):
+        assert torch.equal(out[b], want[0][b]) and torch.equal(lse[b], want[1][b])
+
+
 def test_prefill_more_items_than_a_block_lists():
     """Past 4096 q-tiles a packed call numbers them densely."""
     rng = np.random.default_rng(16)
