@@ -142,12 +142,15 @@ __device__ __forceinline__ bool mbar_wait_lean_warp(uint64_t* bar, uint32_t pari
   return __all_sync(0xffffffffu, mbar_wait_lean(bar, parity, w));
 }
 
-// For a warp that is far ahead of whom it waits for: it sleeps between tries, and so takes no issue slots.
+// For a warp that is far ahead of whom it waits for: it sleeps between tries, and so takes no issue slots.  What it
+// waits for may rightly take longer than the others' waits (a whole work item), so a limit below two seconds does
+// not count here; it ends when another wait has given up.
 __device__ __forceinline__ bool mbar_wait_asleep_warp(uint64_t* bar, uint32_t parity, volatile WaitState* w) {
   const uint64_t t0 = globaltimer_ns();
   while (!__all_sync(0xffffffffu, mbar_test_wait(bar, parity))) {
     if (__any_sync(0xffffffffu, w->abort != 0)) return false;
-    if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > w->limit_ns)) {
+    const uint64_t limit = w->limit_ns > 2000000000ull ? w->limit_ns : 2000000000ull;
+    if (__any_sync(0xffffffffu, globaltimer_ns() - t0 > limit)) {
       w->abort = 1;
       return false;
     }

@@ -738,6 +738,32 @@ def test_prefill_bad_sequences():
     cache.check(o[:4], l[:4], host(q)[:4], 0, 10, 0, "0")
 
 
+def test_prefill_items_longer_than_the_wait_limit():
+    """The limit is one of waits for a step, not for a work item: 900 items of 260 thousand keys under 0.3 ms."""
+    n, prefix = 900, 260000
+    pages = -(-(prefix + n) // 64)
+    pool = cai.KV4Pool(pages, 64)
+    table = torch.randperm(pages, device=DEV).to(torch.int32)[None].contiguous()
+    zero = torch.zeros(1, dtype=torch.int32, device=DEV)
+    x = torch.randn(1, prefix + n, 1, 128, device=DEV, generator=torch.Generator(DEV).manual_seed(1))
+    cai.cai_kv4_append([pool], x, x.flip(1), table, zero)
+    q = torch.randn(1, n, 128, 128, device=DEV, generator=torch.Generator(DEV).manual_seed(2)).to(torch.bfloat16)
+    ws = torch.empty(cai.cai_kv4_prefill_workspace_size(1, 128, 1, pages, 64), dtype=torch.uint8, device=DEV)
+    at = zero + prefix
+    outs = []
+    for limit in (0, 300_000):
+        cai.cai_set_wait_limit_ns(limit)
+        try:
+            err, out = flag(), torch.empty_like(q)
+            cai.cai_kv4_prefill([pool], q, table, at, 0, SCALE, ws, out, None, err)
+            torch.cuda.synchronize()
+            assert err.item() == 0
+            outs.append(out)
+        finally:
+            cai.cai_set_wait_limit_ns(0)
+    assert torch.equal(outs[0], outs[1])
+
+
 def test_prefill_gives_up_then_recovers():
     prefix, new = [900, 1500, 2000], [64, 1, 100]
     cache = Cache([a + n for a, n in zip(prefix, new)], 1, 16, seed=15)
