@@ -731,7 +731,8 @@ cudaError_t launch_append_rows(AppendRowsParams p, bool four, bool bf16, cudaStr
   const int64_t rows = p.q_off ? p.total_new : (int64_t)p.batch * p.n_new;
   const auto blocks = [](int64_t warps) { return (warps + kRowWarps - 1) / kRowWarps; };
   const int64_t q_blocks = blocks(rows * ((p.num_q_heads + kQHeads - 1) / kQHeads));
-  // Chunks by groups of 16 positions.
+  // Chunks by groups of 16 positions, fewer new tokens by rows (64 sequences, 8 K/V heads, int8: 8 tokens 9.2 us by groups
+  // and 8.3 by rows, 16 tokens 13.7 and 13.4, 64 tokens 22.5 and 43.4; 4-bit 5.8 and 5.2, 8.3 and 8.8, 19.4 and 28.5).
   p.groups = p.n_new >= kBlk ? most_groups(p) : 0;
   const int64_t seqs = (int64_t)p.batch * p.num_kv_heads;
   // (Ragged batches: one wave of blocks that look for their groups.  6353 rows of 48 sequences 28.8 us, with a block
