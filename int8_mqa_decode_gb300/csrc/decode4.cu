@@ -232,7 +232,12 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks4) decode4_kernel(const __
             }
           }
 
-        // ---- logits minus reference, in log2 units
+        // ---- logits minus reference, in log2 units; masked after the scale, which may be 0 or negative
+        const uint64_t sl2 = f2(p.scale_log2, p.scale_log2);
+#pragma unroll
+        for (int h = 0; h < kStepBlks; ++h)
+#pragma unroll
+          for (int e = 0; e < 4; e += 2) f2_split(f2_fma(f2(sc[h][e], sc[h][e + 1]), sl2, mref), sc[h][e], sc[h][e + 1]);
         if (edge) {
 #pragma unroll
           for (int h = 0; h < kStepBlks; ++h)
@@ -243,14 +248,10 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks4) decode4_kernel(const __
             }
         }
         float mx = -INFINITY;
-        const uint64_t sl2 = f2(p.scale_log2, p.scale_log2);
 #pragma unroll
         for (int h = 0; h < kStepBlks; ++h)
 #pragma unroll
-          for (int e = 0; e < 4; e += 2) {
-            f2_split(f2_fma(f2(sc[h][e], sc[h][e + 1]), sl2, mref), sc[h][e], sc[h][e + 1]);
-            mx = fmax3(mx, sc[h][e], sc[h][e + 1]);
-          }
+          for (int e = 0; e < 4; e += 2) mx = fmax3(mx, sc[h][e], sc[h][e + 1]);
         if (__any_sync(0xffffffffu, have_ref ? mx > kRaise4 : mx > -INFINITY)) {
           // Raise the references that a logit passes by 2^8 (all of them at the first key).
           float up[2], f[2];
