@@ -13,13 +13,13 @@
 // bulk copies, so no warp waits for another before a piece ends.  Scores are computed transposed,
 // S^T = K Q^T with mma.m16n8k16 (16 keys x 8 heads): the codes become the A operand in registers, query
 // heads fill the N side.  A column of S^T is one head: the running maximum is a reference per head,
-// raised only when a logit passes it by 2^8, so the common step has no reduction across lanes.  P^T goes
+// raised only when a logit passes it by 2^15, so the common step has no reduction across lanes.  P^T goes
 // to the B operand by an 8 x 8 transpose in registers, and O^T += V^T P^T accumulates channels x heads
 // in registers.  At the end of a piece the warps' parts are merged through the ring's shared memory.
 //
-// Roundings, here and in decode4_tc.cu: the query to fp16 (exact within fp16's range), a weight to fp16 for its
-// product with V (2^-11 of it; the sums take it unrounded, in fp32), the output to bf16 once; partial outputs stay
-// fp32.
+// Roundings, here and in decode4_tc.cu: the query to fp16 (exact for magnitudes from 2^-17 to 65504, below that off by
+// 2^-25 at most), a weight to fp16 for its product with V (2^-11 of it, or 2^-32 of the sum of all where that is more, see
+// kWeightLift; the sums take it unrounded, in fp32), the output to bf16 once; partial outputs stay fp32.
 //
 // Why this tensor path: at up to 8 heads a 16-key group's 32 m16n8k16 and the conversion of its codes take
 // a sub-partition about as long as its bytes take the SM at the copy bandwidth (long contexts of 8 heads:
@@ -39,7 +39,7 @@ constexpr int kStep = kStepBlks * kBlk;               // its keys
 constexpr int kStepBytes = kStepBlks * kBlkBytes;     // 4608
 constexpr int kIdSteps = 32 / kStepBlks;              // steps whose page ids a warp holds, one per lane
 constexpr int kORow = kHeadDim + 4;                   // floats of a head's row in the merge buffer (bank spread)
-constexpr float kRaise4 = 8.0f;                       // log2 units a logit may exceed its reference by
+constexpr float kRaise4 = kWeightLift + 8.0f;         // log2 units a logit may exceed its reference by
 
 constexpr int kHeads4 = 8;
 constexpr int kBlocks4 = 4, kStages4 = 3;             // blocks per SM, stages of a warp's ring: 221 KB in flight on an SM
@@ -253,14 +253,14 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks4) decode4_kernel(const __
 #pragma unroll
           for (int e = 0; e < 4; e += 2) mx = fmax3(mx, sc[h][e], sc[h][e + 1]);
         if (__any_sync(0xffffffffu, have_ref ? mx > kRaise4 : mx > -INFINITY)) {
-          // Raise the references that a logit passes by 2^8 (all of them at the first key).
+          // Raise the references that a logit passes by 2^15 (all of them at the first key).
           float up[2], f[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float v = fmaxf(fmaxf(sc[0][e], sc[0][2 + e]), fmaxf(sc[1][e], sc[1][2 + e]));
 #pragma unroll
             for (int x = 4; x < 32; x <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, x));
-            up[e] = !have_ref || v > kRaise4 ? v : 0.0f;
+            up[e] = !have_ref || v > kRaise4 ? v - kWeightLift : 0.0f;
             f[e] = have_ref ? ex2_approx(-up[e]) : 0.0f;
 #pragma unroll
             for (int m = 0; m < 8; ++m) {

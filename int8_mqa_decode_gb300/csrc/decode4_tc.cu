@@ -15,7 +15,7 @@
 // piece ends with the merge of the two.  A converter turns 32 keys of K, then 32 channels of V, into operands;
 // a softmax thread has one key and all heads and writes its weights as 16-byte rows of P^T.
 // A head's running maximum is a reference that the set's softmax warps share, raised only when a logit
-// passes it by 2^8: the weights are written on the guess that none does, and one barrier of those four
+// passes it by 2^15: the weights are written on the guess that none does, and one barrier of those four
 // warps says whether the guess held; if not, O^T is rescaled in tensor memory.
 //
 // Why: mma.sync takes a sub-partition's issue slots (measured: 32 m16n8k16 alone 262 cycles, with the
@@ -43,7 +43,7 @@ constexpr int kT = kDecodeTile;                      // 128 keys
 constexpr int kTileBlks = kT / kBlk;                 // 8
 constexpr int kTileBytes = kTileBlks * kBlkBytes;    // 18432
 constexpr int kInfo = 16;                            // ring of tiles' key ranges, longer than any lag
-constexpr float kRaiseTc = 8.0f;                     // log2 units a logit may exceed its reference by
+constexpr float kRaiseTc = kWeightLift + 8.0f;       // log2 units a logit may exceed its reference by
 constexpr uint32_t kBarPiece = 1 + kSets;            // named barriers: 1 + set (its softmax), all softmax warps
 
 template <int HN>
@@ -537,7 +537,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) decode4_tc_kernel(const __grid_
             const float mx = logits();
             const bool raised = raise;
             if (raise) {
-            // Raise the references that a logit passes by 2^8 (all of them at the first tile with a key).
+            // Raise the references that a logit passes by 2^15 (all of them at the first tile with a key).
 #pragma unroll
             for (int h1 = 0; h1 < HN; h1 += 16) {  // 16 heads at a time
               float mine = -INFINITY;
@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) decode4_tc_kernel(const __grid_
               if (lane < 8) {
                 const float* w = wmax + h1 + lane;
                 const float v = fmaxf(fmaxf(w[0], w[HN]), fmaxf(w[2 * HN], w[3 * HN]));
-                up = any && (!have_ref || v > kRaiseTc) ? v : 0.0f;
+                up = any && (!have_ref || v > kRaiseTc) ? v - kWeightLift : 0.0f;
                 f = ex2_approx(-up);
                 nref[h1 + lane] -= up;
               }

@@ -25,6 +25,12 @@ constexpr int kBlkBytes = 2304;
 constexpr int kBlkV = 1024, kBlkKs = 2048, kBlkVs = 2176;
 constexpr float kMaxScale4 = 9344.0f;  // 7 * 9344 = 65408 is finite in fp16
 
+// Where a softmax reference is set or raised it lies this far (log2 units) below the largest logit: that has a weight of
+// 2^7, and a logit may pass it by 2^8 before the next raise, so weights stay within 2^15 and finite in fp16.
+// A weight below 2^-14 is a subnormal of fp16, off by up to 2^-25: 2^-32 of the sum at most, which is 2^7 and more.  (With the
+// largest at 2^0 a flat rest of 131072 keys 2^25.5 below one key, 0.3% of the sum, was lost from the product.)
+constexpr float kWeightLift = 7.0f;
+
 __host__ __device__ constexpr int page_bytes4(int P) { return P / kBlk * kBlkBytes; }
 
 __device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {

@@ -11,10 +11,12 @@
 // the other has the other pipes.  (With one S buffer and P beside it both halves waited for the same S and came to
 // their exponentials together: 1500 cycles a tile, now 1430.  Two q-tiles a block with all 128 keys a thread,
 // S after PV in the same columns: 1740 a q-tile and tile, half of it the way from P to the next S.)
-// The softmax is that of prefill.cu: a reference per row, raised when a logit passes it by 2^8.
+// The softmax is that of prefill.cu, a reference per row, with larger weights (kWeightLift): raised when a logit passes it
+// by 2^15.
 //
-// Roundings: the query to fp16 (exact within fp16's range), a weight to fp16 for its product with V (2^-11 of it; the sums
-// take it unrounded, in fp32), the output to bf16 once; a piece's partial output stays fp32.
+// Roundings: the query to fp16 (exact for magnitudes from 2^-17 to 65504, below that off by 2^-25 at most), a weight to
+// fp16 for its product with V (2^-11 of it, or 2^-32 of the sum of all where that is more; the sums take it unrounded, in
+// fp32), the output to bf16 once; a piece's partial output stays fp32.
 //
 // Bound: 16 products of 64 cycles a tile, and the exponentials, 512 cycles a sub-partition.
 #include "prefill.cuh"
@@ -39,7 +41,7 @@ constexpr int kRegsLaunch4 = 168, kRegsCtl4 = 72, kRegsSoft4 = 216;
 static_assert(kRegsCtl4 * 128 + kRegsSoft4 * 256 <= kRegsLaunch4 * kThreads4, "register split");
 constexpr uint32_t kColO4 = 256;  // S buffer b at b * 128 (P of half h over its first 32 columns of half h); O_h at kColO4 + h * 128
 constexpr uint32_t kBarSoft4 = 1;
-constexpr float kRaisePrefill4 = 8.0f;
+constexpr float kRaisePrefill4 = kWeightLift + 8.0f;  // log2 units a logit may exceed its reference by
 constexpr int kItemUsers = 1 + 2 + 8;  // warps that read an item
 
 template <bool kCompact>
@@ -357,10 +359,11 @@ __global__ void __launch_bounds__(kThreads4, 1) attend4_kernel(const __grid_cons
           for (int e = 0; e < 4; ++e) mx4[e] = fmax3(mx4[e], z[c + 2 * e], z[c + 2 * e + 1]);
         }
         const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-        // Raise the reference when the half row has none yet, or a logit exceeds it by 2^8.
+        // Raise the reference when the half row has none yet, or a logit exceeds it by 2^15.
         const bool raise = m_ref == -INFINITY ? mx > -INFINITY : mx > kRaisePrefill4;
         if (__any_sync(0xffffffffu, raise)) {
-          const float alpha = raise ? ex2_approx(m_ref - (m_use + mx)) : 1.0f;  // 0 when there was no reference
+          const float up = mx - kWeightLift;
+          const float alpha = raise ? ex2_approx(m_ref - (m_use + up)) : 1.0f;  // 0 when there was no reference
           if (j > 0) {  // O_h holds earlier tiles: wait for their PVs, then rescale this row of it
             ok = mbar_wait_lean_warp(&pv_done[b ^ 1], ((g - 1) >> 1) & 1, wctl);
             if (!ok) break;
@@ -377,9 +380,9 @@ __global__ void __launch_bounds__(kThreads4, 1) attend4_kernel(const __grid_cons
           }
           if (raise) {
             l_sum *= alpha;
-            m_ref = m_use + mx;
+            m_ref = m_use + up;
 #pragma unroll
-            for (int c = 0; c < 64; ++c) z[c] -= mx;
+            for (int c = 0; c < 64; ++c) z[c] -= up;
           }
         }
         // P = 2^z as fp16, over the S that it came from: the A operand of this half's PV.

@@ -105,3 +105,65 @@ def test_prefill_scales(scale, hkv, hq, window):
         for i, b in enumerate(some):
             s = slice(i * n, (i + 1) * n)
             check_rows(cache, out[s], lse[s], host(qn[s]), b, first[b], window, scale, (n, b))
+
+
+# ------------------------------------------------------------ a heavy key beside a long flat rest
+
+# The largest logit has a weight of 2^7 and more, which is part of the sum that divides, so a weight among the
+# subnormals of fp16 is off by 2^-25 / 2^7 of the sum at most: n 2^-32 max|v| where the bound above has n 2^-25.  Long
+# sums: a thread adds n / 128 weights (and 16 of a tile) in fp32, n 2^-30 of their sum at most; the products add
+# n / 16 times, a bit of fp32 cut off each time, n 2^-27 of sum p|v|.
+SINK_KEYS = 131072
+
+
+@pytest.fixture(scope="module")
+def sink():
+    """One K/V head: position 0 has the only key that is not 0 and the only value that is."""
+    rng = np.random.default_rng(77)
+    k, v = np.zeros((SINK_KEYS, 128), np.float32), rng.normal(size=(SINK_KEYS, 128)).astype(np.float32) + 1
+    k[0, 0], v[0] = 7.0, 0.0  # (its group's scale is 1: the cache has 7)
+    pages = SINK_KEYS // 64
+    pool = cai.KV4Pool(pages, 64)
+    table = dev(rng.permutation(pages).astype(np.int32)[None])
+    cai.cai_kv4_append([pool], dev(k)[None, :, None], dev(v)[None, :, None], table, torch.zeros(1, dtype=torch.int32, device=DEV))
+    return pool, table, kv4.dequantize4(*kv4.quantize4(v))
+
+
+def check_sink(sink, out, lse, q, n, where):
+    """out, lse, q [hq][128] of a row that attends positions 0 .. n - 1."""
+    v = sink[2][:n]
+    z = q[:, 0].astype(np.float64) * 7.0 * SCALE
+    total = np.exp(z) + (n - 1)
+    ref = v.sum(0)[None] / total[:, None]
+    each = 2.0 ** -11 + 2.0 ** -12 + n * (2.0 ** -27 + 2.0 ** -30)
+    soft = each * np.abs(v).sum(0)[None] / total[:, None] + n * 2.0 ** -32 * np.abs(v).max()
+    bound = 2.0 ** -8 * np.abs(ref) + (1 + 2.0 ** -8) * soft
+    err = np.abs(out.astype(np.float64) - ref)
+    assert (err <= bound).all(), (where, err.max(), np.abs(ref).max())
+    assert (np.abs(lse - np.log(total)) <= 2.0 ** -20 * (z + 1 + np.log(total)) + n * 2.0 ** -30).all(), where
+
+
+def sink_queries(rows, hq):
+    """Logits of the heavy key between 14 and 19 (20 to 27 in powers of two): the rest has up to a sixth of the weight."""
+    q = np.random.default_rng(hq).normal(size=(rows, hq, 128)).astype(np.float32)
+    q[..., 0] = np.linspace(14, 19, rows * hq).reshape(rows, hq) / (7 * SCALE)
+    return dev(q, torch.bfloat16)
+
+
+@pytest.mark.parametrize("splits", [0, 1, 7])
+@pytest.mark.parametrize("hq", [8, 16, 32, 64])
+def test_decode_counts_small_weights(sink, hq, splits):
+    q = sink_queries(2, hq)
+    ctx = [SINK_KEYS, 70001]
+    out, lse = decode([sink[0]], q, sink[1].repeat(2, 1), ctx, splits=splits, page=64)
+    for b, n in enumerate(ctx):
+        check_sink(sink, out[b], lse[b], host(q[b]), n, (b, splits))
+
+
+@pytest.mark.parametrize("packed", [False, True])
+def test_prefill_counts_small_weights(sink, packed):
+    prefix, n, hq = SINK_KEYS - 9, 9, 32
+    q = sink_queries(n, hq)
+    out, lse = prefill([sink[0]], q, sink[1], [prefix], [n], page=64, packed=packed)
+    for i in range(n):
+        check_sink(sink, out[i], lse[i], host(q[i]), prefix + i + 1, i)
