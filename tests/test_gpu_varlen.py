@@ -157,3 +157,23 @@ def test_varlen_only_decode_rows():
     w, cache, off, out, lse, err = mixed_case(prefix, n_new, seed=83)
     assert err == 0
     check_all_rows(w, off, out, lse, prefix, n_new)
+
+
+def test_varlen_more_q_tiles_than_the_list_holds():
+    """Past 4096 q-tiles with rows the items are numbered densely, empty ones included: empty and one-token sequences
+    beside the long ones."""
+    n_new = [1040, 1, 0, 1040, 1040, 7, 1040, 1040, 0, 1040, 1, 1040, 1040, 300]
+    prefix = [0, 50, 20, 3, 100, 0, 17, 64, 0, 1, 900, 40, 0, 128]
+    assert sum(-(-n * 64 // 128) for n in n_new if n > 1) > 4096
+    w, cache, off, out, lse, err = mixed_case(prefix, n_new, Hq=64, seed=83)
+    assert err == 0 and np.isfinite(out).all() and np.isfinite(lse).all()
+    for b, (p0, n) in enumerate(zip(prefix, n_new)):
+        if n == 0:
+            continue
+        kc, ks, vc, vs = oracle.seq_kv(w.seed, 0, b, p0 + n)
+        q = synth.q_rows(w.seed, synth.STREAM_Q_PREFILL, b, n * 64).reshape(n, 64, 128)
+        some = sorted({0, n // 2, n - 1})
+        o_ref, l_ref = oracle.prefill_seq(q, kc, ks, vc, vs, p0, 0, w.softmax_scale, some)
+        rows = [off[b] + i for i in some]
+        assert np.abs(out[rows] - o_ref).max() <= ATOL, b
+        assert np.abs(lse[rows] - l_ref).max() <= ATOL, b
