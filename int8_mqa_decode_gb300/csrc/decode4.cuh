@@ -72,6 +72,7 @@ __device__ __forceinline__ void start_list(const Decode4Params& p, int c, List4&
     __syncthreads();
     return;
   }
+  // (Blocks of the same range but different head groups each store this, and later the same final value.)
   if (tid == 0) p.meta[c] = make_int2(-1, -1);
   const int per = (p.batch + kThreads - 1) / (kThreads);
   const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);

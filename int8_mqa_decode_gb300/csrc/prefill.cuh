@@ -121,10 +121,10 @@ __device__ __forceinline__ int64_t q_row(const PrefillParams& p, const PItem& it
                : it.qrow0 * p.num_heads + row;
 }
 
-// list: a varlen call's q-tile numbers (entry i for q-tile i - list_first), or null.
+// list: a varlen call's q-tile numbers, or null.
 template <bool kFour>
 __device__ __forceinline__ PItem prefill_item(const PrefillParams& p, int idx, const int32_t* list,
-                                              const WorkSplit& ws, int list_first = 0) {
+                                              const WorkSplit& ws) {
   PItem it;
   int qti = idx, piece = -1;
   if (idx >= ws.full) {
@@ -135,7 +135,7 @@ __device__ __forceinline__ PItem prefill_item(const PrefillParams& p, int idx, c
   } else {
     it.piece = -1;
   }
-  const int qt = list ? list[qti - list_first] : qti;
+  const int qt = list ? list[qti] : qti;
   it.b = qt / p.qtiles;
   it.row0 = (qt - it.b * p.qtiles) * kRows;
   const int seq = kFour ? it.b / p.num_kv_heads : it.b;

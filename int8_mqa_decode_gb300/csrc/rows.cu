@@ -53,8 +53,7 @@ __device__ __forceinline__ uint2 to_bf16x4(const float (&x)[4]) {
   return make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
 }
 
-// Channels c0 .. c0 + N - 1 of row `src`, rotated by c, s (one value per pair and channel) where they lie
-// below rot.  N is 4 or 8, c0 a multiple of N.
+// A position's coefficients for channels c0 .. c0 + N - 1 (N is 4 or 8, c0 a multiple of N), where these lie below rot.
 template <int N>
 struct Turn {
   float c[N], s[N];  // per channel; half-split: s is negated for the first channel of a pair
@@ -135,7 +134,8 @@ __device__ __forceinline__ void bf16x8(const uint4& w, float (&v)[8]) {
 __device__ __forceinline__ float load1(const float* x) { return *x; }
 __device__ __forceinline__ float load1(const uint16_t* x) { return __uint_as_float((uint32_t)*x << 16); }
 
-// x (channels c0 .. c0 + N - 1, y those at t.partner beside them where there is one) turned in place.
+// x (channels c0 .. c0 + N - 1 of row src) turned in place; y: their partner channels where these are a whole vector
+// (partner_of), otherwise they are read one by one.
 // a c - b s and b c + a s: a product with -s and a sum round as the product with s and the difference do.
 template <int N, class T>
 __device__ __forceinline__ void turn_row(const AppendRowsParams& p, const Turn<N>& t, const T* src, int c0, float (&x)[N], const float (&y)[N]) {
