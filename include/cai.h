@@ -296,7 +296,9 @@ cai_status cai_mqa_prefill_varlen(const cai_kv_pool* pool, const uint16_t* q, in
  * cai_mqa_prefill_varlen: sequence b owns rows [q_offsets[b], q_offsets[b + 1]) of
  * total_new, at most n_new of them.  A sequence whose offsets are out of order, beyond
  * total_new or longer than n_new sets CAI_DEVERR_LENGTH and none of its rows is touched
- * (the appends may then leave out rows of other sequences, too).
+ * (the appends may then leave out rows of other sequences, too).  With packed rows n_new
+ * is a bound; appends and reads look through batch * num_kv_heads * n_new / 16 groups of
+ * positions for those with rows, so a bound far above every count costs time.
  *
  * The 4-bit cache holds a token's K (and V) as 128 4-bit codes and four scales, one
  * per 32 channels: s = fp16(bf16(max |x| / 7)) (both roundings to nearest even, the
@@ -389,12 +391,16 @@ cai_status cai_kv4_read(const cai_kv4_pool* kv_pools, int32_t num_kv_heads, void
 /* One decode step of one layer over the 4-bit cache: cai_gqa_decode's attention, reading
  * 144 bytes a token and K/V head.
  *   num_q_heads   a multiple of num_kv_heads; up to 128 query heads per K/V head
+ *   q             multiplied as fp16: exact for magnitudes from 2^-17 to 65504, below that
+ *                 off by 2^-25 at most
+ *   softmax_scale finite; 0 and negative ones included
  *   out           bf16 bits [batch][num_q_heads][128], 16-byte aligned (fp32 sums, rounded
- *                 once)
+ *                 once; a weight enters its product with V as fp16, off by 2^-11 of itself or
+ *                 2^-32 of the sum of the weights)
  *   workspace     cai_kv4_decode_workspace_size() bytes, 256-byte aligned; may be null when
  *                 that is 0.  It needs no preparation; calls that share it must not overlap
  *                 on the GPU.
- *   q, block_table, ctx_len, window, softmax_scale, num_splits, lse_out as cai_gqa_decode
+ *   q, block_table, ctx_len, window, num_splits, lse_out otherwise as cai_gqa_decode
  * A sequence with nothing to attend, or of an invalid length (flagged), gets out = 0 and
  * lse = -inf.  Slots past a sequence's length are not looked at, whatever they hold. */
 size_t cai_kv4_decode_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
@@ -412,8 +418,10 @@ cai_status cai_kv4_decode(const cai_kv4_pool* kv_pools, int32_t num_kv_heads, co
  *   num_q_heads   num_kv_heads times a power of two from 1 to 128
  *   q             bf16 bits [rows][num_q_heads][128]; prefix_len int32 [batch]
  *   out           bf16 bits [rows][num_q_heads][128]; lse_out fp32 [rows][num_q_heads], nullable
- *   workspace     cai_kv4_prefill_workspace_size() bytes, 256-byte aligned (no preparation)
- * Other arguments and errors as for the int8 calls. */
+ *   workspace     cai_kv4_prefill_workspace_size() bytes, 256-byte aligned (no preparation).
+ *                 It holds an fp16 copy of the keys and values: 520 bytes for every token
+ *                 that the tables have room for and K/V head, whatever the lengths and the window
+ * Roundings as cai_kv4_decode's; other arguments and errors as for the int8 calls. */
 size_t cai_kv4_prefill_workspace_size(int32_t batch, int32_t num_q_heads, int32_t num_kv_heads,
                                       int32_t max_pages_per_seq, int32_t page_size);
 cai_status cai_kv4_prefill(const cai_kv4_pool* kv_pools, int32_t num_kv_heads, const uint16_t* q, int32_t batch,
@@ -504,14 +512,18 @@ cai_status cai_ring_table_row(int32_t* row, int32_t max_pages_per_seq, const int
  * clock after each suspension of up to 1 ms, so shorter limits act as about 1 ms).  A
  * CTA whose wait runs out sets CAI_DEVERR_TIMEOUT, stops its work, waits for its own
  * copies and tensor-core operations in flight, frees its tensor memory and returns;
- * that launch's outputs are unspecified.  A short limit is for failure-detection
- * tests; a serving process leaves the default. */
+ * that launch's outputs are unspecified.  One wait has a limit of 2 s at least: that of
+ * the warp that works out items ahead in packed prefill calls and in the 4-bit prefill,
+ * which waits for whole items and ends as soon as another wait has given up.  A short
+ * limit is for failure-detection tests; a serving process leaves the default. */
 void cai_set_wait_limit_ns(uint64_t ns);
 
 /* Fault injection for failure-detection tests (process-wide, read at each launch;
  * -1, the default, turns it off).  With stage = n >= 0, every CTA of the following
- * decode launches skips the load of its n-th K/V stage (64 tokens), and every CTA of
- * the following prefill launches skips the load of its n-th K tile (128 keys); the
+ * decode launches skips the load of its n-th K/V stage (64 tokens; over the 4-bit cache
+ * its n-th tile of 128 keys, or, up to 8 heads per K/V head, each warp its n-th step of 32),
+ * and every CTA of the following prefill launches skips the load of its n-th K tile (128
+ * keys); the
  * waits for them run out after the wait limit and the launch reports
  * CAI_DEVERR_TIMEOUT.  Nothing faults: the load is simply never issued.  A CTA with
  * fewer stages than n + 1 is not affected. */
