@@ -1,0 +1,689 @@
+"""Cases of the operators for long contexts: appends rotated by several position axes, page summaries,
+the selection of pages for each query, and attention over lists of pages.
+
+`run` computes a case in plain torch (`own = False`) or through the library (`own = True`).
+A page's summary holds, for each of the 128 key channels, the smallest and the largest cached value of the
+page's tokens, as 8-bit codes under one scale, rounded away from each other.  A query's score for a page is
+the largest logit that the summary allows any head of the group, in whole numbers and single products, so
+that it is the same number however it is computed.
+"""
+import math
+
+import numpy as np
+import torch
+
+own = False
+
+D = 128            # head_dim
+BLOCK = 2304       # bytes of 16 tokens in the 4-bit cache
+DEV = "cuda"
+SCALE = 1.0 / math.sqrt(D)
+
+
+# ------------------------------------------------------------------------------------ cases
+
+def listed():
+    return [
+        # A decode step of a small server of image dialogues: four sequences, MQA.
+        dict(name="axes8_step", op="axes8", batch=4, n=1, ragged=False, hq=8, hkv=1, page=16, lo=64, hi=512, rot=128,
+             axes=3, inter=False, bf16=True),
+        # Frames of a video appended to long dialogues, q, k and v slices of one fused projection.
+        dict(name="axes8_frames", op="axes8", batch=16, n=256, ragged=False, hq=32, hkv=1, page=16, lo=8192, hi=8192,
+             rot=128, axes=3, inter=False, bf16=True),
+        # Continuous batching with grouped heads, the axes taking turns over the channels, fp32 inputs.
+        dict(name="axes4_ragged", op="axes4", batch=48, n=400, ragged=True, hq=32, hkv=2, page=64, lo=1, hi=9000,
+             rot=128, axes=3, inter=True, bf16=False),
+        # After each decode step the page that the new token lies in.
+        dict(name="sum8_step", op="sum8", batch=64, n=1, ragged=False, hkv=8, page=16, lo=256, hi=8192),
+        # Restored dialogues get their summaries.
+        dict(name="sum4_dialogues", op="sum4", batch=64, n=8192, ragged=True, hkv=4, page=32, lo=0, hi=0),
+        # The smallest selection, where latency counts.
+        dict(name="select_small", op="select", batch=4, n=1, ragged=False, hq=8, hkv=1, page=16, lo=1000, hi=4000,
+             keep=32, first=1, last=2),
+        # Long contexts, 64 heads on one K/V head: 4096 of up to 131072 tokens.
+        dict(name="select_long", op="select", batch=64, n=1, ragged=False, hq=64, hkv=1, page=64, lo=16384, hi=131072,
+             keep=64, first=1, last=2),
+        # A chunk on a reused prefix, every row its own pages.
+        dict(name="select_chunk", op="select", batch=16, n=256, ragged=False, hq=32, hkv=1, page=16, lo=8192, hi=8192,
+             keep=128, first=1, last=4),
+        # The smallest attention over lists.
+        dict(name="attend8_small", op="attend8", rows=4, per=1, hq=8, hkv=1, page=16, lo=1000, hi=4000, keep=32),
+        # A decode step over what select_long leaves.
+        dict(name="attend8_long", op="attend8", rows=64, per=1, hq=64, hkv=1, page=64, lo=16384, hi=131072, keep=64),
+        # Grouped heads, a list for each K/V head.
+        dict(name="attend4_grouped", op="attend4", rows=96, per=1, hq=64, hkv=8, page=32, lo=256, hi=16384, keep=64),
+        # A chunk's rows over what select_chunk leaves, 4-bit.
+        dict(name="attend4_chunk", op="attend4", rows=4096, per=256, hq=32, hkv=1, page=16, lo=8192, hi=8192, keep=128),
+    ]
+
+
+def _log(rng, lo, hi):
+    return int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))
+
+
+def draw(rng):
+    op = rng.choice(["axes8", "axes4", "sum8", "sum4", "select", "select", "attend8", "attend8", "attend4", "attend4"])
+    page = rng.choice([16, 32, 64])
+    if op.startswith("attend"):
+        hkv = rng.choice([1, 1, 2, 4, 8])
+        g = rng.choice([1, 3, 4, 5, 8, 12, 16, 24, 32, 40, 64])
+        hi = _log(rng, 20, 131072)
+        keep = _log(rng, 2, 4096 // page)
+        most = 4096 * 2048 * 32  # the largest listed case's (row, key, head) triples
+        per = rng.choice([1, 1, _log(rng, 2, 256)])
+        rows = _log(rng, 1, max(1, min(4096, most // (min(hi, keep * page) * g * hkv), 4_000_000 * per // (hi * hkv),
+                                       1_800_000 * per // (min(hi, keep * page) * hkv), 65536 // (g * hkv))))
+        return dict(op=op, rows=rows, per=min(per, rows), hq=g * hkv, hkv=hkv, page=page, lo=rng.randint(1, hi), hi=hi,
+                    keep=keep)
+    if op == "select":
+        hkv = rng.choice([1, 1, 2, 4, 8])
+        g = rng.choice([1, 3, 4, 5, 8, 12, 16, 32, 64, 128])
+        hi = _log(rng, 20, 131072)
+        n = rng.choice([1, 1, _log(rng, 2, 500)])
+        most = 16 * 256 * 32 * (8192 + 256) // 16  # the largest listed case's (row, head, block) triples
+        n = max(1, min(n, most // (g * hkv * (hi // page + n // page + 1)), 65536 // (g * hkv)))
+        batch = max(1, min(_log(rng, 1, 256), most // (n * g * hkv * (hi // page + n // page + 1)), 65536 // (n * g * hkv),
+                           400_000 // (hkv * (hi // page + n // page + 1))))
+        first, last = rng.choice([0, 1, 2]), rng.choice([1, 2, 4])
+        return dict(op=op, batch=batch, n=n, ragged=n > 1 and rng.random() < 0.5, hq=g * hkv, hkv=hkv, page=page,
+                    lo=rng.randint(0, hi), hi=hi, keep=first + last + rng.choice([0, _log(rng, 1, 256)]), first=first,
+                    last=last)
+    hkv = rng.choice([1, 2, 4, 8])
+    if op.startswith("sum"):
+        n = rng.choice([1, 1, _log(rng, 2, 8192)])
+        hi = _log(rng, 1, 8192)
+        batch = max(1, min(_log(rng, 1, 256), 300_000 // ((n + hi) * hkv)))
+        return dict(op=op, batch=batch, n=n, ragged=n > 1 and rng.random() < 0.5, hkv=hkv, page=page,
+                    lo=rng.randint(0, hi), hi=hi)
+    n = rng.choice([1, 1, _log(rng, 2, 1000)])
+    hi = _log(rng, 1, 30000)
+    batch = max(1, min(_log(rng, 1, 256), 16384 // (n * hkv)))
+    return dict(op=op, batch=batch, n=n, ragged=n > 1 and rng.random() < 0.5, hq=hkv * rng.choice([1, 4, 8]), hkv=hkv,
+                page=page, lo=rng.randint(0, hi), hi=hi, rot=rng.choice([128, 128, 64, 32, 98, 2]),
+                axes=rng.choice([1, 2, 3, 3, 4]), inter=rng.random() < 0.5, bf16=rng.random() < 0.5)
+
+
+# ----------------------------------------------------------------------------------- inputs
+
+def _lengths(case, count):
+    """Context (or prefix) lengths: the case alone gives them, a seed their order."""
+    return np.random.default_rng(7).integers(case["lo"], case["hi"] + 1, count).astype(np.int64)
+
+
+def _new(case):
+    """New tokens of every sequence, likewise."""
+    b, n = case["batch"], case["n"]
+    if not case["ragged"]:
+        return np.full(b, n, dtype=np.int64)
+    rng = np.random.default_rng(8)
+    new = rng.integers(0, n + 1, b)
+    new[rng.random(b) < 0.3] = 1  # decode rows beside the chunks
+    new[0] = n
+    return new.astype(np.int64)
+
+
+def _tables(lengths, page, rng):
+    """A block table [batch][max pages] over a shuffled pool with some pages to spare; unused entries are -1."""
+    pages = -(-lengths // page)
+    total, most = int(pages.sum()) + 200, max(1, int(pages.max()))
+    perm, table, at = rng.permutation(total).astype(np.int32), np.full((len(lengths), most), -1, np.int32), 0
+    for b, k in enumerate(pages):
+        table[b, :k] = perm[at:at + k]
+        at += int(k)
+    return torch.from_numpy(table).to(DEV), total
+
+
+def _cache4(hkv, num_pages, page, gen):
+    """Filled 4-bit pools [hkv][bytes]: near-normal codes, scales of unit-size keys and values with some larger groups."""
+    blocks = hkv * num_pages * (page // 16)
+    pool = torch.empty(blocks, BLOCK, dtype=torch.uint8, device=DEV)
+    step = 1 << 16
+    for a in range(0, blocks, step):
+        n = min(step, blocks - a)
+        x = torch.randn(n, 2048, 2, device=DEV, generator=gen).mul_(2.6).round_().clamp_(-7, 7).add_(8).to(torch.uint8)
+        pool[a:a + n, :2048] = x[..., 0] | (x[..., 1] << 4)
+        s = torch.randn(n, 128, device=DEV, generator=gen).mul_(0.35).exp_().mul_(0.3)
+        pool[a:a + n, 2048:] = s.to(torch.bfloat16).to(torch.float16).view(torch.uint8)
+    return pool.view(hkv, -1)
+
+
+def _cache8(hkv, num_pages, page, gen):
+    """Filled int8 pools [hkv][bytes]."""
+    total = hkv * num_pages
+    pool = torch.empty(total, page * 264, dtype=torch.uint8, device=DEV)
+    step = 1 << 14
+    for a in range(0, total, step):
+        n = min(step, total - a)
+        x = torch.randn(n, page * 256, device=DEV, generator=gen).mul_(40).round_().clamp_(-127, 127)
+        pool[a:a + n, :page * 256] = x.to(torch.int8).view(torch.uint8)
+        s = torch.randn(n, page * 2, device=DEV, generator=gen).mul_(0.2).exp_().mul_(0.025)
+        pool[a:a + n, page * 256:] = s.view(torch.uint8)
+    return pool.view(hkv, -1)
+
+
+def prepare(case, seed):
+    rng = np.random.default_rng(seed)
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(seed)
+    op, page, hkv = case["op"], case["page"], case["hkv"]
+    cache = _cache8 if op.endswith("8") else _cache4
+    st = dict(case=case)
+    if op.startswith("attend"):
+        rows, per, keep = case["rows"], case["per"], case["keep"]
+        seqs = -(-rows // per)
+        st["ctx"] = ctx = rng.permutation(_lengths(case, seqs))  # of a sequence's last row
+        table, pages = _tables(ctx, page, rng)
+        st["arena"] = cache(hkv, pages, page, gen)
+        st["q"] = (torch.randn(rows, case["hq"], D, device=DEV, generator=gen) * 1.5).to(torch.bfloat16)
+        # Rows of a sequence follow one another; row r sees the tokens up to its own.  Its list: the first
+        # page, the last one and others at random, in ascending order.
+        r = torch.arange(rows, device=DEV)
+        seen = torch.from_numpy(ctx).to(DEV)[r // per] - (per - 1) + r % per
+        seen = seen.clamp(min=1)
+        have = (seen + page - 1) // page
+        score = torch.rand(rows, hkv, max(keep, table.shape[1]), device=DEV, generator=gen)
+        i = torch.arange(score.shape[2], device=DEV)
+        score[(i == 0).expand_as(score)] = 2.0
+        score = torch.where((i == have[:, None, None] - 1), torch.full_like(score, 3.0), score)
+        score = torch.where(i < have[:, None, None], score, torch.full_like(score, -1.0))
+        top = score.topk(keep, -1)
+        blocks = torch.where(top.values >= 0, top.indices, torch.full_like(top.indices, 1 << 30)).sort(-1).values
+        ids = table.long()[r // per]
+        ids = ids[r[:, None, None], blocks.clamp(max=table.shape[1] - 1)]
+        st["pages"] = torch.where(blocks < 1 << 30, ids, torch.full_like(ids, -1)).to(torch.int32).contiguous()
+        st["len"] = torch.where(have <= keep, seen, (keep - 1) * page + (seen - 1) % page + 1).to(torch.int32)
+        return st
+    b = case["batch"]
+    order = rng.permutation(b)
+    before, new = _lengths(case, b)[order], _new(case)[order]
+    st["before"], st["new"], st["rows"] = before, new, int(new.sum())
+    st["table"], pages = _tables(before + new, page, rng)
+    st["start"] = torch.from_numpy(before.astype(np.int32)).to(DEV)
+    st["offsets"] = torch.from_numpy(np.concatenate([[0], np.cumsum(new)]).astype(np.int32)).to(DEV)
+    if op == "select":
+        # Summaries of unit-size keys, some channels larger, as page records of 256 codes and one scale.
+        size = torch.where(torch.rand(D, device=DEV, generator=gen) < 0.05, 4.0, 1.0)
+        mid = torch.randn(hkv, pages, D, device=DEV, generator=gen) * size * 9
+        out = (torch.randn(hkv, pages, D, device=DEV, generator=gen).abs() * 6 + 12) * size
+        codes = torch.cat(((mid + out).ceil(), (mid - out).floor()), -1).clamp_(-127, 127).to(torch.int8)
+        scale = torch.randn(hkv, pages, device=DEV, generator=gen).mul_(0.2).exp_().mul_(0.03)
+        st["data"] = torch.cat((codes.view(torch.uint8).flatten(1), scale.view(torch.uint8).flatten(1)), 1)
+        st["q"] = (torch.randn(st["rows"], case["hq"], D, device=DEV, generator=gen) * 1.5).to(torch.bfloat16)
+        return st
+    st["arena"] = cache(hkv, pages, page, gen)
+    if op.startswith("sum"):
+        # Buffers of the summaries, and which pages the call brings up to date.
+        st["data"] = torch.zeros(hkv, pages * 260, dtype=torch.uint8, device=DEV)
+        table = st["table"].cpu().numpy()
+        live = [np.arange(p // page, -(-(p + n) // page)) if n else np.arange(0) for p, n in zip(before, new)]
+        st["touched"] = torch.from_numpy(np.concatenate([table[i, x] for i, x in enumerate(live)]).astype(np.int64)).to(DEV)
+        st["filled"] = torch.from_numpy(np.concatenate(
+            [np.minimum(p + n - x * page, page) for x, p, n in zip(live, before, new)])).to(DEV)
+        return st
+    hq, half = case["hq"], case["rot"] // 2
+    # One fused projection [rows][hq + 2 hkv][128]: q, k and v are its slices; some channels are large.
+    qkv = torch.randn(st["rows"], hq + 2 * hkv, D, device=DEV, generator=gen)
+    qkv[:, hq:hq + hkv] *= torch.where(torch.rand(D, device=DEV, generator=gen) < 0.05, 6.0, 1.0)
+    st["qkv"] = qkv.to(torch.bfloat16 if case["bf16"] else torch.float32)
+    st["q"] = st["qkv"][:, :hq] if case["bf16"] else qkv[:, :hq].to(torch.bfloat16).contiguous()
+    st["k"], st["v"] = st["qkv"][:, hq:hq + hkv], st["qkv"][:, hq + hkv:]
+    # Axes: sections of the pairs, or turn by turn.  Positions: time runs on, the others within an image.
+    axes = case["axes"]
+    st["axis"] = [i % axes if case["inter"] else i * axes // half for i in range(half)]
+    count = int((before + new).max()) + 1
+    inv = 10000.0 ** (-torch.arange(half, device=DEV, dtype=torch.float64) / half)
+    ang = torch.arange(count, device=DEV, dtype=torch.float64)[:, None] * inv
+    st["cos"], st["sin"] = ang.cos().float(), ang.sin().float()
+    seq, at = _rows(st)
+    side = min(24, count)
+    st["positions"] = torch.stack([at] + [at * (a + 1) // side ** (a - 1) % side for a in range(1, axes)], 1).to(torch.int32)
+    st["axis_of"] = torch.tensor(st["axis"], device=DEV)
+    return st
+
+
+# -------------------------------------------------------------------------------- plain form
+
+def _rows(st):
+    """Sequence and position of every new row, on the device."""
+    off = st["offsets"].long()
+    i = torch.arange(st["rows"], device=DEV)
+    seq = torch.searchsorted(off, i, right=True) - 1
+    return seq, st["start"].long()[seq] + i - off[seq]
+
+
+def _rotate(x, st):
+    """Rotation of channels [0, rot) in fp32, a pair by its axis's position, every product and the sum rounded on its own."""
+    rot, half = st["case"]["rot"], st["case"]["rot"] // 2
+    pos = st["positions"].long()[:, st["axis_of"]]  # [rows][half]
+    i = torch.arange(half, device=DEV)
+    c, s = st["cos"][pos, i][:, None], st["sin"][pos, i][:, None]
+    y = x.float().clone()
+    a, b = (y[..., 0:rot:2], y[..., 1:rot:2]) if st["case"]["inter"] else (y[..., :half], y[..., half:rot])
+    lo, hi = a * c - b * s, b * c + a * s
+    if st["case"]["inter"]:
+        y[..., 0:rot:2], y[..., 1:rot:2] = lo, hi
+    else:
+        y[..., :half], y[..., half:rot] = lo, hi
+    return y
+
+
+def _codes4(x):
+    """fp32 [..., 128] -> codes (float), scales fp16 [..., 4]."""
+    g = x.unflatten(-1, (4, 32))
+    amax = g.abs().amax(-1)
+    s = (amax / torch.full_like(amax, 7.0)).to(torch.bfloat16).clamp(max=9344.0).to(torch.float16)
+    sf = s.float()[..., None]
+    c = torch.where(sf > 0, (g / torch.where(sf > 0, sf, torch.ones_like(sf))).round().clamp(-7, 7), torch.zeros_like(g))
+    return c.flatten(-2), s
+
+
+def _codes8(x):
+    amax = x.abs().amax(-1, keepdim=True)
+    s = amax / torch.full_like(amax, 127.0)
+    c = torch.where(s > 0, (x / torch.where(s > 0, s, torch.ones_like(s))).round().clamp(-127, 127), torch.zeros_like(x))
+    return c, s
+
+
+def _write4(pools, page_id, slot, page, k, v):
+    """Writes rows k, v fp32 [rows][heads][128] into their slots and returns the values they stand for."""
+    heads = torch.arange(len(pools), device=DEV)
+    blk, r = (page_id * (page // 16) + slot // 16)[:, None], (slot % 16)[:, None]
+    t, hb, e = (r % 8) // 2, r // 8, r % 2
+    kc, ks = _codes4(k)
+    vc, vs = _codes4(v)
+    p = pools.view(len(pools), -1, BLOCK)
+    # K: word (t, j) of a token's 64 bytes holds channels 32 j + 8 t + 2 i + e at bits 4 i + 16 e.
+    c = (kc + 8).to(torch.uint8).unflatten(-1, (4, 4, 4, 2)).permute(0, 1, 3, 2, 5, 4)  # [row, head, t, j, e, i]
+    b = c[..., 0::2] | (c[..., 1::2] << 4)                                              # bytes [..., t, j, e, i / 2]
+    p[..., :1024].unflatten(2, (16, 64))[heads, blk, r] = b.flatten(2)
+    # V: a token's byte of word (h, g, t, w) holds channels 16 (4 h + w) + g and + 8.
+    c = (vc + 8).to(torch.uint8).unflatten(-1, (2, 4, 2, 8))                            # [..., h, w, half, g]
+    b = (c[..., 0, :] | (c[..., 1, :] << 4)).transpose(-1, -2)                          # [..., h, g, w]
+    p[..., 1024:2048].unflatten(2, (2, 8, 4, 4, 4)).permute(0, 1, 4, 6, 2, 3, 5)[heads, blk, t, hb + 2 * e] = b
+    sc = p[..., 2048:].view(torch.float16)
+    sc[..., :64].unflatten(2, (16, 4))[heads, blk, r] = ks
+    sc[..., 64:].unflatten(2, (4, 2, 4, 2)).permute(0, 1, 2, 3, 5, 4)[heads, blk, t, hb, e] = vs
+    up = lambda c, s: (c.unflatten(-1, (4, 32)) * s.float()[..., None]).flatten(-2)  # noqa: E731
+    return up(kc, ks), up(vc, vs)
+
+
+def _write8(pools, page_id, slot, page, k, v):
+    heads = torch.arange(len(pools), device=DEV)
+    page_id, slot = page_id[:, None], slot[:, None]
+    kc, ks = _codes8(k)
+    vc, vs = _codes8(v)
+    p = pools.view(len(pools), -1, page * 264)
+    p[..., :page * D].unflatten(2, (page, D))[heads, page_id, slot] = kc.to(torch.int8).view(torch.uint8)
+    p[..., page * D:page * 256].unflatten(2, (D, page)).transpose(2, 3)[heads, page_id, slot] = vc.to(torch.int8).view(torch.uint8)
+    sc = p[..., page * 256:].view(torch.float32)
+    sc[heads, page_id, slot] = ks[..., 0]
+    sc[heads, page_id, page + slot] = vs[..., 0]
+    return kc * ks, vc * vs
+
+
+def _values4(blocks):
+    """4-bit blocks uint8 [..., 2304] -> the K and V values fp32 [..., 16, 128] that they stand for."""
+    shape, blocks = blocks.shape[:-1], blocks.reshape(-1, BLOCK)
+    n = blocks.shape[0]
+    sc = blocks[:, 2048:].contiguous().view(torch.float16).float()
+    kb = blocks[:, :1024].reshape(n, 16, 4, 4, 2, 2)                   # [row, t, j, e, i / 2]
+    k = torch.stack((kb & 15, kb >> 4), -1).float() - 8                # [..., e, i / 2, i % 2]
+    k = k.flatten(5).permute(0, 1, 3, 2, 5, 4).reshape(n, 16, 4, 32)   # [row, j, t, i, e]
+    k = k * sc[:, :64].view(n, 16, 4, 1)
+    vb = blocks[:, 1024:2048].reshape(n, 2, 8, 4, 4, 2, 2)             # [h, g, t, w, e, hb]
+    v = torch.stack((vb & 15, vb >> 4), -1).float() - 8                # [..., half]
+    v = v.permute(0, 6, 3, 5, 1, 4, 7, 2).reshape(n, 2, 4, 2, 4, 32)   # [hb, t, e, h w half g]: group = channel / 32
+    v = v * sc[:, 64:].view(n, 4, 2, 4, 2).permute(0, 2, 1, 4, 3)[..., None]
+    return k.reshape(*shape, 16, D), v.reshape(*shape, 16, D)
+
+
+def _values(st, pages):
+    """K and V fp32 [..., page, 128] of pages [...][heads] of the cache."""
+    page, arena = st["case"]["page"], st["arena"]
+    heads = torch.arange(len(arena), device=DEV)
+    if st["case"]["op"].endswith("4"):
+        k, v = _values4(arena.view(len(arena), -1, page // 16, BLOCK)[heads, pages])
+        return k.flatten(-3, -2), v.flatten(-3, -2)
+    p = arena.view(len(arena), -1, page * 264)[heads, pages]
+    sc = p[..., page * 256:].contiguous().view(torch.float32)
+    k = p[..., :page * D].contiguous().view(torch.int8).unflatten(-1, (page, D)).float()
+    v = p[..., page * D:page * 256].contiguous().view(torch.int8).unflatten(-1, (D, page)).transpose(-1, -2).float()
+    return k * sc[..., :page, None], v * sc[..., page:, None]
+
+
+def _summaries(st):
+    """Views of the summaries: codes int8 [heads][pages][256] (largest, smallest), scales fp32 [heads][pages]."""
+    data = st["data"]
+    pages = data.shape[1] // 260
+    return data[:, :pages * 256].view(torch.int8).unflatten(1, (pages, 256)), data[:, pages * 256:].view(torch.float32)
+
+
+def _summary_values(st):
+    codes, scale = _summaries(st)
+    return torch.mul(codes[:, st["touched"]], scale[:, st["touched"]][..., None])
+
+
+def _plain_summarize(st):
+    page = st["case"]["page"]
+    heads = torch.arange(st["case"]["hkv"], device=DEV)
+    k = _values(st, st["touched"][:, None].expand(-1, len(heads)))[0]  # [pages][heads][page][128]
+    there = (torch.arange(page, device=DEV) < st["filled"][:, None])[:, None, :, None]
+    lo = torch.where(there, k, torch.full_like(k, math.inf)).amin(2)
+    hi = torch.where(there, k, torch.full_like(k, -math.inf)).amax(2)
+    amax = torch.maximum(lo.abs(), hi.abs()).amax(-1, keepdim=True)
+    s = amax / torch.full_like(amax, 127.0)
+    safe = torch.where(s > 0, s, torch.ones_like(s))
+    code = torch.cat(((hi / safe).ceil().clamp(max=127), (lo / safe).floor().clamp(min=-127)), -1)
+    code = torch.where(s > 0, code, torch.zeros_like(code))
+    codes, scale = _summaries(st)
+    codes[heads, st["touched"][:, None]] = code.to(torch.int8)
+    scale[heads, st["touched"][:, None]] = s[..., 0]
+    return {"bounds": _summary_values(st)}
+
+
+def _plain_select(st):
+    c = st["case"]
+    b, n, hq, hkv, page, keep = c["batch"], int(st["new"].max()), c["hq"], c["hkv"], c["page"], c["keep"]
+    seq, at = _rows(st)
+    row = at - st["start"].long()[seq]
+    q = torch.zeros(b, n, hq, D, device=DEV)
+    q[seq, row] = st["q"].float()
+    code, t = _codes8(q)
+    both = torch.cat((code.clamp(min=0), code.clamp(max=0)), -1).view(b, n, hkv, hq // hkv, 256).transpose(1, 2)
+    codes, scale = _summaries(st)
+    table = st["table"].long()
+    most = table.shape[1]
+    heads = torch.arange(hkv, device=DEV)[:, None]
+    pages = table.clamp(min=0)[:, None]
+    # Whole numbers below 2^21: the product in fp32 is exact.
+    d = both.flatten(2, 3) @ codes[heads, pages].float().transpose(2, 3)      # [b][hkv][n G][blocks]
+    d = d.unflatten(2, (n, hq // hkv)) * t.view(b, n, hkv, hq // hkv, 1).transpose(1, 2)
+    score = (d.amax(3) * scale[heads, pages][:, :, None]).transpose(1, 2)[seq, row]  # [rows][hkv][blocks]
+    have = (at // page + 1)[:, None, None]
+    i = torch.arange(most, device=DEV)
+    inf = torch.full_like(score, math.inf)
+    score = torch.where((i < c["first"]) | (i >= have - c["last"]), inf, score)
+    score = torch.where(i < have, score, -inf)
+    top = score.sort(dim=-1, descending=True, stable=True).indices[..., :keep]
+    blocks = torch.where(top < have, top, torch.full_like(top, 1 << 30)).sort(-1).values
+    ids = table[seq[:, None, None], blocks.clamp(max=most - 1)]
+    ids = torch.where(blocks < 1 << 30, ids, torch.full_like(ids, -1)).to(torch.int32)
+    ids = torch.cat((ids, ids.new_full((*ids.shape[:2], keep - ids.shape[2]), -1)), -1)
+    length = torch.where(have[:, 0, 0] <= keep, at + 1, (keep - 1) * page + at % page + 1)
+    return {"pages": ids, "len": length.to(torch.int32)}
+
+
+def _plain_attend(st):
+    c = st["case"]
+    rows, hkv, hq = st["q"].shape[0], c["hkv"], c["hq"]
+    k, v = _values(st, st["pages"].long().clamp(min=0).transpose(1, 2))  # [rows][keep][hkv][page][128]
+    k, v = (x.transpose(1, 2).flatten(2, 3) for x in (k, v))
+    there = torch.arange(k.shape[2], device=DEV) < st["len"].long()[:, None, None, None]
+    z = (st["q"].float().view(rows, hkv, hq // hkv, D) @ k.transpose(2, 3)).mul_(SCALE)
+    z = torch.where(there, z, torch.full_like(z, -math.inf))
+    m = z.amax(-1, keepdim=True)
+    z = (z - m).exp()
+    s = z.sum(-1, keepdim=True)
+    return {"out": ((z @ v) / s).view(rows, hq, D).to(torch.bfloat16), "lse": (m + s.log()).view(rows, hq)}
+
+
+def _plain(st):
+    op, page = st["case"]["op"], st["case"]["page"]
+    if op.startswith("attend"):
+        return _plain_attend(st)
+    if op == "select":
+        return _plain_select(st)
+    if op.startswith("sum"):
+        return _plain_summarize(st)
+    seq, at = _rows(st)
+    page_id, slot = st["table"].long()[seq, at // page], at % page
+    write = _write4 if op == "axes4" else _write8
+    k, v = write(st["arena"], page_id, slot, page, _rotate(st["k"], st), st["v"].float())
+    return {"q": _rotate(st["q"], st).to(torch.bfloat16), "k": k, "v": v}
+
+
+# --------------------------------------------------------------------------- the library's calls
+
+def _own(st):
+    import int8_mqa_decode_gb300 as cai
+    c = st["case"]
+    op, page, hkv = c["op"], c["page"], c["hkv"]
+    eight = op.endswith("8")
+    if "handles" not in st:  # what a program keeps: pool handles, the rotation's tables, a workspace
+        if "arena" in st:
+            pool = cai.KVPool if eight else cai.KV4Pool
+            bytes_ = cai.cai_page_bytes(page) if eight else cai.cai_kv4_page_bytes(page)
+            st["handles"] = [pool(p.numel() // bytes_, page, pages=p) for p in st["arena"]]
+        if "data" in st:
+            st["summaries"] = [cai.KVSummary(x.numel() // 260, page, data=x) for x in st["data"]]
+            st.setdefault("handles", None)
+        if op.startswith("axes"):
+            st["rope"] = cai.RopeAxes(st["cos"], st["sin"], st["axis"], interleaved=c["inter"])
+        elif op.startswith("attend"):
+            size = cai.cai_kv_attend_pages_workspace_size if eight else cai.cai_kv4_attend_pages_workspace_size
+            st["ws"] = torch.zeros(size(c["rows"], c["hq"], hkv, c["keep"], page), dtype=torch.uint8, device=DEV)
+        elif op == "select":
+            st["ws"] = torch.empty(cai.cai_kv_select_workspace_size(c["batch"], st["rows"], c["hq"], hkv, st["table"].shape[1]),
+                                   dtype=torch.uint8, device=DEV)
+    if op.startswith("attend"):
+        out = torch.empty(c["rows"], c["hq"], D, dtype=torch.bfloat16, device=DEV)
+        lse = torch.empty(c["rows"], c["hq"], dtype=torch.float32, device=DEV)
+        attend = cai.cai_kv_attend_pages if eight else cai.cai_kv4_attend_pages
+        attend(st["handles"], st["q"], st["pages"], st["len"], SCALE, 0, st["ws"], out, lse)
+        return {"out": out, "lse": lse}
+    n = st["rows"]
+    if c["ragged"]:
+        packed = dict(q_offsets=st["offsets"], max_new=c["n"])
+        shape = lambda x: x  # noqa: E731
+    else:
+        packed = {}
+        shape = lambda x: x.unflatten(0, (c["batch"], c["n"]))  # noqa: E731
+    if op == "select":
+        pages = torch.empty(n, hkv, c["keep"], dtype=torch.int32, device=DEV)
+        length = torch.empty(n, dtype=torch.int32, device=DEV)
+        cai.cai_kv_select(st["summaries"], shape(st["q"]), st["table"], st["start"], c["first"], c["last"], st["ws"],
+                          shape(pages), shape(length), **packed)
+        return {"pages": pages, "len": length}
+    if op.startswith("sum"):
+        summarize = cai.cai_kv_summarize if eight else cai.cai_kv4_summarize
+        summarize(st["handles"], st["summaries"], st["table"], st["start"], c["n"],
+                  q_offsets=st["offsets"] if c["ragged"] else None)
+        return {"bounds": _summary_values(st)}
+    k = torch.empty(n, hkv, D, dtype=torch.float32, device=DEV)
+    v = torch.empty_like(k)
+    q = torch.empty(n, c["hq"], D, dtype=torch.bfloat16, device=DEV)
+    append, read = (cai.cai_kv_append_rope_axes, cai.cai_kv_read) if eight else (cai.cai_kv4_append_axes, cai.cai_kv4_read)
+    append(st["handles"], shape(st["k"]), shape(st["v"]), st["table"], st["start"], st["rope"], shape(st["positions"]),
+           q=shape(st["q"]), q_out=shape(q), **packed)
+    read(st["handles"], shape(k), shape(v), st["table"], st["start"], **packed)  # what the cache now stands for
+    return {"q": q, "k": k, "v": v}
+
+
+def run(state):
+    return _own(state) if own else _plain(state)
+
+
+# ------------------------------------------------------------------------------------- work
+
+def work(case):
+    """Bytes and operations of one pass: cached tokens, summaries, inputs and table entries read once, outputs written once."""
+    c, op, page, hkv = case, case["op"], case["page"], case["hkv"]
+    if op.startswith("attend"):
+        rows, per, hq, keep = c["rows"], c["per"], c["hq"], c["keep"]
+        ctx = _lengths(c, -(-rows // per))
+        tokens = unique = 0.0
+        for i, x in enumerate(ctx):
+            seen = np.maximum(1, x - (per - 1) + np.arange(min(per, rows - i * per)))
+            mine = np.where(-(-seen // page) <= keep, seen, (keep - 1) * page + (seen - 1) % page + 1).astype(np.float64)
+            tokens += mine.sum()
+            unique += min(mine.sum(), float(x))
+        token = 264 if op == "attend8" else 144
+        io = rows * hq * (2 * D + 2 * D + 4) + 4.0 * tokens / page * hkv
+        return {"bytes": unique * hkv * token + io, "flops": 4 * D * tokens * hq}
+    before, new = _lengths(c, c["batch"]), _new(c)
+    rows = float(new.sum())
+    if op == "select":
+        blocks = [(p + np.arange(n)) // page + 1 for p, n in zip(before, new)]
+        triples = float(sum(x.sum() for x in blocks))
+        unique = float(sum(x[-1] for x in blocks if len(x)))
+        io = rows * (c["hq"] * 2 * D + hkv * 4 * c["keep"] + 4) + 4 * unique
+        return {"bytes": unique * hkv * 260 + io, "flops": 4 * D * triples * c["hq"]}
+    if op.startswith("sum"):
+        token = 132 if op == "sum8" else 72
+        pages = float(sum(-(-(p + n) // page) - p // page for p, n in zip(before, new) if n))
+        tokens = float(sum(p + n - p // page * page for p, n in zip(before, new) if n))
+        return {"bytes": hkv * (tokens * token + pages * (260 + 1024)) + 4 * pages, "flops": tokens * hkv * 4 * D}
+    wide, token, hq = 2 if c["bf16"] else 4, 264 if op == "axes8" else 144, c["hq"]
+    # k, v in; cache bytes and the values they stand for out; q in and out; a row of each table, positions.
+    bytes_ = rows * (hkv * (2 * D * wide + token + 2 * D * 4) + hq * D * 4 + c["rot"] * 4 + 4 * c["axes"])
+    return {"bytes": bytes_, "flops": rows * (hkv * 8 * D + hq * 3 * D)}
+
+
+# ------------------------------------------------------------------------------------ exact
+
+def _exact_rotation(x, pos, cos, sin, axis, inter, rounded):
+    """x float64 [rows][heads][128]; `rounded`: every product and sum to fp32, as the operator is defined."""
+    f = (lambda a: a.astype(np.float32).astype(np.float64)) if rounded else (lambda a: a)
+    y = x.copy()
+    half = cos.shape[1]
+    for i in range(half):
+        a, b = (2 * i, 2 * i + 1) if inter else (i, i + half)
+        c, s = cos[pos[:, axis[i]], i][:, None], sin[pos[:, axis[i]], i][:, None]
+        y[:, :, a] = f(f(x[:, :, a] * c) - f(x[:, :, b] * s))
+        y[:, :, b] = f(f(x[:, :, b] * c) + f(x[:, :, a] * s))
+    return y
+
+
+def _exact_values(x, bits):
+    """What the cache stands for after an append of x float64 [rows][heads][128]."""
+    f32 = lambda a: a.astype(np.float32)  # noqa: E731
+    top, size = (7, 32) if bits == 4 else (127, D)
+    out = np.zeros_like(x)
+    for a in range(0, D, size):
+        g = x[..., a:a + size]
+        s = f32(np.abs(g).max(-1) / top)
+        if bits == 4:
+            s = torch.from_numpy(np.ascontiguousarray(s)).bfloat16().float().numpy()
+            s = np.minimum(s, 9344.0).astype(np.float16)
+        s = s.astype(np.float64)[..., None]
+        code = np.clip(np.rint(f32(np.divide(g, s, out=np.zeros_like(g), where=s > 0))), -top, top)
+        out[..., a:a + size] = code * s
+    return out
+
+
+def _exact_cached(pool, page, page_id, slot, bits):
+    """K, V float64 [...][128] of single tokens, by the byte that each code stands in."""
+    ch = torch.arange(D, device=DEV)
+    base = page_id.long()[..., None] * (page * (264 if bits == 8 else 144))
+    slot = slot[..., None]
+    if bits == 8:
+        k, v = pool[base + slot * D + ch].view(torch.int8), pool[base + page * D + ch * page + slot].view(torch.int8)
+        words = pool.view(torch.float32)
+        at = base // 4 + page * 64 + slot
+        return k.double() * words[at].double(), v.double() * words[at + page].double()
+    base = base + (slot // 16) * BLOCK
+    r = slot % 16
+    bit = 4 * (ch % 8 // 2) + 16 * (ch % 2)
+    k = (pool[base + r * 64 + (ch % 32 // 8) * 16 + (ch // 32) * 4 + bit // 8] >> (bit % 8)) & 15
+    m, g, up = ch // 16, ch % 8, ch % 16 // 8
+    t, hb, e = r % 8 // 2, r // 8, r % 2
+    v = (pool[base + 1024 + (((m // 4) * 32 + g * 4 + t) * 4 + m % 4) * 4 + hb + 2 * e] >> (4 * up)) & 15
+    half = pool.view(torch.float16)
+    ks = half[(base + 2048) // 2 + r * 4 + ch // 32]
+    vs = half[(base + 2176) // 2 + t * 16 + hb * 8 + (ch // 32) * 2 + e]
+    return (k.double() - 8) * ks.double(), (v.double() - 8) * vs.double()
+
+
+def _exact_attend(st):
+    c, page = st["case"], st["case"]["page"]
+    rows, hkv, g = c["rows"], c["hkv"], c["hq"] // c["hkv"]
+    out = torch.zeros(rows, c["hq"], D, dtype=torch.float64, device=DEV)
+    lse = torch.zeros(rows, c["hq"], dtype=torch.float64, device=DEV)
+    longest = int(st["len"].max())
+    at = torch.arange(longest, device=DEV)
+    step = max(1, 400_000 // longest)
+    for a in range(0, rows, step):
+        r = slice(a, min(rows, a + step))
+        for j in range(hkv):
+            ids = st["pages"][r, j][:, at // page].clamp(min=0)
+            k, v = _exact_cached(st["arena"][j], page, ids, (at % page).expand(ids.shape), 8 if c["op"] == "attend8" else 4)
+            h = slice(j * g, (j + 1) * g)
+            z = torch.einsum("rhd,rtd->rht", st["q"][r, h].double(), k) * SCALE
+            z = z.masked_fill((at >= st["len"][r, None])[:, None], -math.inf)
+            lse[r, h] = torch.logsumexp(z, -1)
+            out[r, h] = torch.einsum("rht,rtd->rhd", torch.softmax(z, -1), v)
+    return {"out": out, "lse": lse}
+
+
+def _exact_select(st):
+    c, page, keep, hkv, g = st["case"], st["case"]["page"], st["case"]["keep"], st["case"]["hkv"], st["case"]["hq"] // st["case"]["hkv"]
+    codes, scale = _summaries(st)
+    table = st["table"].cpu().numpy()
+    pages = np.full((st["rows"], hkv, keep), -1, np.int32)
+    length = np.zeros(st["rows"], np.int32)
+    row = 0
+    for b in range(c["batch"]):
+        n, p0 = int(st["new"][b]), int(st["before"][b])
+        if n == 0:
+            continue
+        at = p0 + np.arange(n)
+        have = at // page + 1
+        ids = st["table"][b, :int(have[-1])].long()
+        for j in range(hkv):
+            hi, lo = codes[j, ids, :D].short(), codes[j, ids, D:].short()
+            q = st["q"][row:row + n, j * g:(j + 1) * g].double().cpu().numpy()
+            t = (np.abs(q).max(-1) / 127).astype(np.float32)
+            t64 = t.astype(np.float64)[..., None]
+            qc = np.clip(np.rint(np.divide(q, t64, out=np.zeros_like(q), where=t64 > 0).astype(np.float32)), -127, 127)
+            qc = torch.from_numpy(qc).to(DEV).short()
+            best = torch.full((n, len(ids)), -math.inf, dtype=torch.float64, device=DEV)
+            step = max(1, 400_000_000 // (len(ids) * D))
+            for h in range(g):
+                for a in range(0, n, step):
+                    x = qc[a:a + step, h, None]
+                    dot = torch.maximum(x * hi, x * lo).sum(-1, dtype=torch.int32)
+                    weighed = dot.double() * torch.from_numpy(t[a:a + step, h]).to(DEV).double()[:, None]
+                    best[a:a + step] = torch.maximum(best[a:a + step], weighed.float().double())
+            score = (best * scale[j, ids].double()).float().cpu().numpy()
+            for i in range(n):
+                m = int(have[i])
+                s = score[i, :m].copy()
+                s[:c["first"]] = s[max(0, m - c["last"]):] = np.inf
+                kept = np.sort(np.lexsort((np.arange(m), -s))[:keep])
+                pages[row + i, j, :len(kept)] = table[b, kept]
+        length[row:row + n] = np.where(have <= keep, at + 1, (keep - 1) * page + at % page + 1)
+        row += n
+    return {"pages": pages, "len": length}
+
+
+def exact(case, seed):
+    st = prepare(case, seed)
+    c, op, page, hkv = case, case["op"], case["page"], case["hkv"]
+    bits = 8 if op.endswith("8") else 4
+    if op.startswith("attend"):
+        return _exact_attend(st)
+    if op == "select":
+        return _exact_select(st)
+    if op.startswith("sum"):
+        bounds = []
+        slot = torch.arange(page, device=DEV)
+        for pool in st["arena"]:
+            parts = []
+            for ids, filled in zip(st["touched"].split(4096), st["filled"].split(4096)):
+                k = _exact_cached(pool, page, ids[:, None].expand(-1, page), slot.expand(len(ids), -1), bits)[0]
+                k = k.float().double()  # a cached value is an fp32 number
+                out = slot >= filled[:, None]
+                hi = k.masked_fill(out[..., None], -math.inf).amax(1).cpu().numpy()
+                lo = k.masked_fill(out[..., None], math.inf).amin(1).cpu().numpy()
+                s = (np.maximum(np.abs(hi), np.abs(lo)).max(-1) / 127).astype(np.float32).astype(np.float64)[:, None]
+                div = lambda x: np.divide(x, s, out=np.zeros_like(x), where=s > 0).astype(np.float32)  # noqa: E731
+                code = np.concatenate((np.minimum(np.ceil(div(hi)), 127), np.maximum(np.floor(div(lo)), -127)), 1)
+                parts.append(code * s)
+            bounds.append(np.concatenate(parts) if parts else np.zeros((0, 256)))
+        return {"bounds": np.stack(bounds)}
+    cos, sin = (st[x].cpu().numpy().astype(np.float64) for x in ("cos", "sin"))
+    wide = lambda x: x.float().cpu().numpy().astype(np.float64)  # noqa: E731
+    pos = st["positions"].cpu().numpy()
+    return {"q": _exact_rotation(wide(st["q"]), pos, cos, sin, st["axis"], c["inter"], False),
+            "k": _exact_values(_exact_rotation(wide(st["k"]), pos, cos, sin, st["axis"], c["inter"], True), bits),
+            "v": _exact_values(wide(st["v"]), bits)}
