@@ -374,6 +374,33 @@ cai_status cai_kv4_append(const cai_kv4_pool* kv_pools, int32_t num_kv_heads, co
                           int32_t total_new, const int32_t* block_table, int32_t max_pages_per_seq,
                           const int32_t* start_pos, int32_t* err_flag, void* stream);
 
+/* cai_kv_append_rope and cai_kv4_append for tokens that have a position on several axes, as
+ * those of images and video do (time, height, width): pair i of row r turns by row
+ * positions[r][axis[i]] of the tables.  The slot that a row is written to is start_pos[b] + i
+ * as ever.  With equal positions on all axes it is the rotation by that position.
+ *   rope          must be given; num_positions is the tables' rows, for every axis
+ *   axis          host uint8 [rot_dim / 2]: the axis of each pair, below num_axes (sections one
+ *                 behind the other, in turn, or any other way)
+ *   num_axes      1..4
+ *   positions     int32 [rows][num_axes], 4-byte aligned, row by row as k_new (text: the same
+ *                 number on all axes)
+ * A row with a position outside [0, num_positions) on any axis, used by a pair or not, sets
+ * CAI_DEVERR_LENGTH and is left out; other arguments and errors as cai_kv_append_rope. */
+cai_status cai_kv_append_rope_axes(const cai_kv_pool* kv_pools, int32_t num_kv_heads, const cai_rope* rope,
+                                   const uint8_t* axis, int32_t num_axes, const int32_t* positions,
+                                   const void* k_new, const void* v_new, cai_dtype kv_type, int64_t k_stride,
+                                   int64_t v_stride, const uint16_t* q, int64_t q_stride, uint16_t* q_out,
+                                   int32_t num_q_heads, int32_t batch, int32_t n_new, const int32_t* q_offsets,
+                                   int32_t total_new, const int32_t* block_table, int32_t max_pages_per_seq,
+                                   const int32_t* start_pos, int32_t* err_flag, void* stream);
+cai_status cai_kv4_append_axes(const cai_kv4_pool* kv_pools, int32_t num_kv_heads, const cai_rope* rope,
+                               const uint8_t* axis, int32_t num_axes, const int32_t* positions, const void* k_new,
+                               const void* v_new, cai_dtype kv_type, int64_t k_stride, int64_t v_stride,
+                               const uint16_t* q, int64_t q_stride, uint16_t* q_out, int32_t num_q_heads,
+                               int32_t batch, int32_t n_new, const int32_t* q_offsets, int32_t total_new,
+                               const int32_t* block_table, int32_t max_pages_per_seq, const int32_t* start_pos,
+                               int32_t* err_flag, void* stream);
+
 /* Read cached tokens back as the values they stand for (code * scale in fp32; bf16 rounds
  * that once more): for an attention that the library does not have, or to move a dialogue
  * from one cache to the other.  Row i of sequence b comes from position start_pos[b] + i.

@@ -26,6 +26,7 @@ __all__ = [
     "cai_host_cache_destroy", "cai_host_cache_match", "cai_host_cache_restore", "cai_host_cache_store",
     "cai_host_cache_stats", "cai_host_cache_restore_batch", "cai_set_wait_limit_ns", "cai_set_fault_injection", "cai_ring_pages", "cai_ring_table_row",
     "KV4Pool", "Rope", "cai_kv4_page_bytes", "cai_kv_append_rope", "cai_kv4_append", "cai_kv_read", "cai_kv4_read",
+    "RopeAxes", "cai_kv_append_rope_axes", "cai_kv4_append_axes",
     "cai_kv4_decode_workspace_size", "cai_kv4_decode", "cai_kv4_prefill_workspace_size", "cai_kv4_prefill",
 ]
 
@@ -127,6 +128,11 @@ def load():
         f = getattr(lib, name)
         f.argtypes = [pp, i32, rope_p, vp, vp, ctypes.c_int, i64, i64, vp, i64, vp, i32, i32, i32, vp, i32, vp, i32, vp,
                       vp, vp]
+        f.restype = ctypes.c_int
+    for name, pp in (("cai_kv_append_rope_axes", pool_p), ("cai_kv4_append_axes", pool4_p)):
+        f = getattr(lib, name)
+        f.argtypes = [pp, i32, rope_p, vp, i32, vp, vp, vp, ctypes.c_int, i64, i64, vp, i64, vp, i32, i32, i32, vp, i32, vp,
+                      i32, vp, vp, vp]
         f.restype = ctypes.c_int
     for name, pp in (("cai_kv_read", pool_p), ("cai_kv4_read", pool4_p)):
         f = getattr(lib, name)
@@ -532,6 +538,19 @@ class Rope:
                                2 * cos.shape[1], int(interleaved))
 
 
+class RopeAxes(Rope):
+    """Rotation by positions on several axes (1 to 4): ``axis[i]`` is the axis of channel pair i, one entry for each of
+    the rot_dim / 2 pairs."""
+
+    def __init__(self, cos: torch.Tensor, sin: torch.Tensor, axis: Sequence[int], interleaved: bool = False):
+        super().__init__(cos, sin, interleaved)
+        axis = [int(a) for a in axis]
+        if len(axis) != cos.shape[1] or not all(0 <= a < 4 for a in axis):
+            raise ValueError(f"axis must hold an axis (0 to 3) for each of the {cos.shape[1]} pairs")
+        self.axis = (ctypes.c_uint8 * len(axis))(*axis)
+        self.least_axes = max(axis, default=0) + 1
+
+
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1}
 
 
@@ -620,7 +639,7 @@ def _table(block_table: torch.Tensor, batch: int, dev: int):
 
 
 def _append_rows(entry: str, kind, pools, k_new, v_new, block_table, start_pos, rope, q, q_out, q_offsets, max_new,
-                 err_flag, stream) -> None:
+                 err_flag, stream, positions=None) -> None:
     dev, arr, hkv = _begin(pools, kind, k_new, "k_new")
     rows, batch, n_new, heads = _rows(k_new, "k_new", q_offsets, max_new, start_pos)
     if heads != hkv or v_new.shape != k_new.shape:
@@ -647,8 +666,18 @@ def _append_rows(entry: str, kind, pools, k_new, v_new, block_table, start_pos, 
         if rope.cos.get_device() != dev or rope.sin.get_device() != dev:
             raise ValueError("the rotation's tables must be on the current device")
         cos_sin = ctypes.byref(rope.struct)
+    axes = ()
+    if positions is not None:
+        if not isinstance(rope, RopeAxes):
+            raise TypeError("positions on several axes need a RopeAxes")
+        n = positions.shape
+        if len(n) != k_new.dim() - 1 or n[:-1] != k_new.shape[:-2] or n[-1] < rope.least_axes:
+            raise ValueError(f"positions has shape {tuple(n)}, expected the rows of k_new and {rope.least_axes} axes or more")
+        axes = (rope.axis, n[-1], _data(positions, "positions", dev, torch.int32))
+    elif isinstance(rope, RopeAxes):
+        raise TypeError("a RopeAxes goes with positions on its axes")
     st = getattr(load(), entry)(
-        arr, hkv, cos_sin, k_new.data_ptr(), v_new.data_ptr(), kv_type, _row_stride(k_new, "k_new"),
+        arr, hkv, cos_sin, *axes, k_new.data_ptr(), v_new.data_ptr(), kv_type, _row_stride(k_new, "k_new"),
         _row_stride(v_new, "v_new"), q_ptr, q_stride, out_ptr, hq, batch, n_new,
         _data(q_offsets, "q_offsets", dev, torch.int32, (batch + 1,)), rows, table, width,
         _data(start_pos, "start_pos", dev, torch.int32, (batch,)), _data(err_flag, "err_flag", dev, torch.int32),
@@ -674,6 +703,31 @@ def cai_kv4_append(pools: Sequence[KV4Pool], k_new: torch.Tensor, v_new: torch.T
     """cai_kv_append_rope into the 4-bit cache."""
     _append_rows("cai_kv4_append", KV4Pool, pools, k_new, v_new, block_table, start_pos, rope, q, q_out, q_offsets,
                  max_new, err_flag, stream)
+
+
+def cai_kv_append_rope_axes(pools: Sequence[KVPool], k_new: torch.Tensor, v_new: torch.Tensor,
+                            block_table: torch.Tensor, start_pos: torch.Tensor, rope: RopeAxes, positions: torch.Tensor,
+                            q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                            q_offsets: Optional[torch.Tensor] = None, max_new: Optional[int] = None,
+                            err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """cai_kv_append_rope with a position on several axes for each row: positions int32 [batch][n_new][axes], or
+    [rows][axes] packed."""
+    if positions is None:
+        raise ValueError("positions must be given")
+    _append_rows("cai_kv_append_rope_axes", KVPool, pools, k_new, v_new, block_table, start_pos, rope, q, q_out, q_offsets,
+                 max_new, err_flag, stream, positions)
+
+
+def cai_kv4_append_axes(pools: Sequence[KV4Pool], k_new: torch.Tensor, v_new: torch.Tensor, block_table: torch.Tensor,
+                        start_pos: torch.Tensor, rope: RopeAxes, positions: torch.Tensor,
+                        q: Optional[torch.Tensor] = None, q_out: Optional[torch.Tensor] = None,
+                        q_offsets: Optional[torch.Tensor] = None, max_new: Optional[int] = None,
+                        err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """cai_kv_append_rope_axes into the 4-bit cache."""
+    if positions is None:
+        raise ValueError("positions must be given")
+    _append_rows("cai_kv4_append_axes", KV4Pool, pools, k_new, v_new, block_table, start_pos, rope, q, q_out, q_offsets,
+                 max_new, err_flag, stream, positions)
 
 
 def _read_rows(entry: str, kind, pools, k_out, v_out, block_table, start_pos, q_offsets, max_new, err_flag,

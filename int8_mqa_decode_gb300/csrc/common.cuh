@@ -124,6 +124,11 @@ struct AppendRowsParams {
   const float* cos;             // [num_positions][rot / 2]
   const float* sin;
   int32_t num_positions, rot, interleaved;  // rot 0: no rotation
+  // Several axes: positions [rows][num_axes] (null: a row's position is that of its slot), the axis of pair i at bits
+  // 2 (i % 16) of axis_bits[i / 16].
+  const int32_t* positions;
+  int32_t num_axes;
+  uint32_t axis_bits[4];
   int32_t* err;
   // Filled by the launch: blocks that write K/V (by `groups` groups of 16 positions per sequence, or by rows
   // when 0), then blocks that rotate queries; whether the tables are 16-byte aligned.

@@ -49,8 +49,17 @@ void fill_pools(const Pool* pools, int32_t num_kv_heads, Params& p) {
 
 bool dtype_ok(cai_dtype t) { return t == CAI_FP32 || t == CAI_BF16; }
 
+constexpr int32_t kMaxAxes = 4;
+
+// Positions on several axes (num 0: none).
+struct Axes {
+  const uint8_t* axis;
+  int32_t num;
+  const int32_t* positions;
+};
+
 template <class Pool>
-cai_status append_rows(const Pool* pools, int32_t num_kv_heads, const cai_rope* rope, const void* k_new,
+cai_status append_rows(const Pool* pools, int32_t num_kv_heads, const cai_rope* rope, const Axes& axes, const void* k_new,
                        const void* v_new, cai_dtype kv_type, int64_t k_stride, int64_t v_stride, const uint16_t* q,
                        int64_t q_stride, uint16_t* q_out, int32_t num_q_heads, int32_t batch, int32_t n_new,
                        const int32_t* q_offsets, int32_t total_new, const int32_t* block_table,
@@ -74,6 +83,14 @@ cai_status append_rows(const Pool* pools, int32_t num_kv_heads, const cai_rope* 
     p.rot = rope->rot_dim;
     p.interleaved = rope->interleaved != 0;
   }
+  if (axes.num > 0) {
+    for (int i = 0; i < p.rot / 2; ++i) {
+      if (axes.axis[i] >= axes.num) return CAI_ERR_INVALID_ARG;
+      p.axis_bits[i / 16] |= (uint32_t)axes.axis[i] << (2 * (i % 16));
+    }
+    p.num_axes = axes.num;
+    p.positions = axes.positions;
+  }
   const int64_t quantum = kv_type == CAI_FP32 ? 4 : 8;  // elements of 16 bytes
   const int64_t width = (int64_t)num_kv_heads * kHeadDim;
   if (k_stride < width || v_stride < width || k_stride % quantum || v_stride % quantum) return CAI_ERR_INVALID_ARG;
@@ -85,6 +102,7 @@ cai_status append_rows(const Pool* pools, int32_t num_kv_heads, const cai_rope* 
   if (rows == 0) return CAI_OK;
   if (!k_new || !v_new || !block_table || !start_pos) return CAI_ERR_INVALID_ARG;
   if (!aligned16(k_new) || !aligned16(v_new)) return CAI_ERR_INVALID_ARG;
+  if (axes.num > 0 && (!axes.positions || (reinterpret_cast<uintptr_t>(axes.positions) & 3u))) return CAI_ERR_INVALID_ARG;
   if (num_q_heads > 0) {
     if (!q || !q_out || !aligned16(q) || !aligned16(q_out)) return CAI_ERR_INVALID_ARG;
     if (q == q_out && q_stride != (int64_t)num_q_heads * kHeadDim) return CAI_ERR_INVALID_ARG;
@@ -169,7 +187,7 @@ cai_status cai_kv_append_rope(const cai_kv_pool* kv_pools, int32_t num_kv_heads,
                               int32_t num_q_heads, int32_t batch, int32_t n_new, const int32_t* q_offsets,
                               int32_t total_new, const int32_t* block_table, int32_t max_pages_per_seq,
                               const int32_t* start_pos, int32_t* err_flag, void* stream) {
-  return append_rows(kv_pools, num_kv_heads, rope, k_new, v_new, kv_type, k_stride, v_stride, q, q_stride, q_out,
+  return append_rows(kv_pools, num_kv_heads, rope, Axes{}, k_new, v_new, kv_type, k_stride, v_stride, q, q_stride, q_out,
                      num_q_heads, batch, n_new, q_offsets, total_new, block_table, max_pages_per_seq, start_pos,
                      err_flag, false, stream);
 }
@@ -180,9 +198,35 @@ cai_status cai_kv4_append(const cai_kv4_pool* kv_pools, int32_t num_kv_heads, co
                           int32_t num_q_heads, int32_t batch, int32_t n_new, const int32_t* q_offsets,
                           int32_t total_new, const int32_t* block_table, int32_t max_pages_per_seq,
                           const int32_t* start_pos, int32_t* err_flag, void* stream) {
-  return append_rows(kv_pools, num_kv_heads, rope, k_new, v_new, kv_type, k_stride, v_stride, q, q_stride, q_out,
+  return append_rows(kv_pools, num_kv_heads, rope, Axes{}, k_new, v_new, kv_type, k_stride, v_stride, q, q_stride, q_out,
                      num_q_heads, batch, n_new, q_offsets, total_new, block_table, max_pages_per_seq, start_pos,
                      err_flag, true, stream);
+}
+
+cai_status cai_kv_append_rope_axes(const cai_kv_pool* kv_pools, int32_t num_kv_heads, const cai_rope* rope,
+                     const uint8_t* axis, int32_t num_axes, const int32_t* positions, const void* k_new,
+                     const void* v_new, cai_dtype kv_type, int64_t k_stride, int64_t v_stride, const uint16_t* q,
+                     int64_t q_stride, uint16_t* q_out, int32_t num_q_heads, int32_t batch, int32_t n_new,
+                     const int32_t* q_offsets, int32_t total_new, const int32_t* block_table,
+                     int32_t max_pages_per_seq, const int32_t* start_pos, int32_t* err_flag, void* stream) {
+  if (!rope || !axis) return CAI_ERR_INVALID_ARG;
+  if (num_axes < 1 || num_axes > kMaxAxes) return CAI_ERR_UNSUPPORTED;
+  return append_rows(kv_pools, num_kv_heads, rope, Axes{axis, num_axes, positions}, k_new, v_new, kv_type, k_stride,
+                     v_stride, q, q_stride, q_out, num_q_heads, batch, n_new, q_offsets, total_new, block_table,
+                     max_pages_per_seq, start_pos, err_flag, false, stream);
+}
+
+cai_status cai_kv4_append_axes(const cai_kv4_pool* kv_pools, int32_t num_kv_heads, const cai_rope* rope,
+                     const uint8_t* axis, int32_t num_axes, const int32_t* positions, const void* k_new,
+                     const void* v_new, cai_dtype kv_type, int64_t k_stride, int64_t v_stride, const uint16_t* q,
+                     int64_t q_stride, uint16_t* q_out, int32_t num_q_heads, int32_t batch, int32_t n_new,
+                     const int32_t* q_offsets, int32_t total_new, const int32_t* block_table,
+                     int32_t max_pages_per_seq, const int32_t* start_pos, int32_t* err_flag, void* stream) {
+  if (!rope || !axis) return CAI_ERR_INVALID_ARG;
+  if (num_axes < 1 || num_axes > kMaxAxes) return CAI_ERR_UNSUPPORTED;
+  return append_rows(kv_pools, num_kv_heads, rope, Axes{axis, num_axes, positions}, k_new, v_new, kv_type, k_stride,
+                     v_stride, q, q_stride, q_out, num_q_heads, batch, n_new, q_offsets, total_new, block_table,
+                     max_pages_per_seq, start_pos, err_flag, true, stream);
 }
 
 cai_status cai_kv_read(const cai_kv_pool* kv_pools, int32_t num_kv_heads, void* k_out, void* v_out,

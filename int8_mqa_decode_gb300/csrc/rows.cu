@@ -8,7 +8,8 @@
 //   int8:  s = max |x| / 127, code = clamp(rint(x / s)) (as cai_kv_append);
 //   4-bit: for each 32 channels s = fp16(bf16(max |x| / 7)), code = clamp(rint(x / s)) in [-7, 7].
 // The queries of the new tokens are rotated on the way (bf16 in and out), so that they need no pass
-// of their own.
+// of their own.  With several axes a pair's position is the row's on the pair's axis: the same kernels with the row's
+// positions read beside its data (kAxes), vectors of table entries where a vector's pairs share an axis.
 //
 // Bound by HBM for chunks and by launch latency for one token a sequence.  One launch, blocks of three
 // kinds: K/V blocks, in chunk calls one per 16 aligned tokens of a head, so that V, which lies by
@@ -21,33 +22,13 @@
 #include "common.cuh"
 #include "kv4.cuh"
 #include "ptx.cuh"
+#include "rows.cuh"
 
 namespace cai {
 namespace {
 
 constexpr int kRowWarps = 8;
 constexpr int kQHeads = 8;  // query heads of one warp (16: a decode step of 256 sequences 6.5 us, 8: 5.0; chunks within 5%)
-
-// New tokens of sequence b: rows [r0, r0 + n); n = -1 when its offsets are out of order, past the
-// packed rows or more than n_new.
-struct NewRows {
-  int64_t r0;
-  int n;
-};
-template <class Params>
-__device__ __forceinline__ NewRows new_rows(const Params& p, int b) {
-  if (!p.q_off) return NewRows{(int64_t)b * p.n_new, p.n_new};
-  const int32_t a = p.q_off[b], e = p.q_off[b + 1];
-  const bool ok = a >= 0 && a <= e && e <= p.total_new && e - a <= p.n_new;
-  return NewRows{a, ok ? e - a : -1};
-}
-
-// x / y for x >= 0, y > 0, in 32 bits where that is enough; and the places of a position that is not negative.
-// (A decode step of four sequences takes 5.2 us with its read, with 64-bit divisions 5.4.)
-__device__ __forceinline__ int64_t over(int64_t x, int32_t y) {
-  return x >> 32 ? x / y : (int64_t)((uint32_t)x / (uint32_t)y);
-}
-__device__ __forceinline__ int page_log2(int P) { return P == 16 ? 4 : P == 32 ? 5 : 6; }
 
 __device__ __forceinline__ uint2 to_bf16x4(const float (&x)[4]) {
   return make_uint2(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]));
@@ -60,21 +41,27 @@ struct Turn {
   int mode;          // 0: none of these channels, 1: half-split in whole vectors, 2: half-split, odd sizes, 3: interleaved
 };
 
-template <int N>
-__device__ __forceinline__ Turn<N> load_turn(const AppendRowsParams& p, int64_t pos, int c0) {
+// With axes, pair i of row `row` turns by the row's position on axis i (two bits a pair in axis_bits).
+template <bool kAxes>
+__device__ __forceinline__ int64_t pair_at(const AppendRowsParams& p, int64_t row, int64_t pos, int i) {
+  if constexpr (kAxes)
+    pos = __ldg(p.positions + row * p.num_axes + ((p.axis_bits[i >> 4] >> (2 * (i & 15))) & 3u));
+  return pos * (p.rot >> 1) + i;
+}
+template <int N, bool kAxes>
+__device__ __forceinline__ Turn<N> load_turn(const AppendRowsParams& p, int64_t row, int64_t pos, int c0) {
   Turn<N> t;
   const int half = p.rot >> 1;
   t.mode = 0;
   if (c0 >= p.rot) return t;
-  const float* cos = p.cos + pos * half;
-  const float* sin = p.sin + pos * half;
   if (p.interleaved) {
     t.mode = 3;
 #pragma unroll
-    for (int e = 0; e < N; ++e) {
+    for (int e = 0; e < N; e += 2) {
       const bool on = c0 + e < p.rot;
-      t.c[e] = on ? __ldg(cos + (c0 + e) / 2) : 1.0f;
-      t.s[e] = on ? __ldg(sin + (c0 + e) / 2) : 0.0f;
+      const int64_t at = on ? pair_at<kAxes>(p, row, pos, (c0 + e) / 2) : 0;
+      t.c[e] = t.c[e + 1] = on ? __ldg(p.cos + at) : 1.0f;
+      t.s[e] = t.s[e + 1] = on ? __ldg(p.sin + at) : 0.0f;
     }
     return t;
   }
@@ -82,19 +69,26 @@ __device__ __forceinline__ Turn<N> load_turn(const AppendRowsParams& p, int64_t 
   if (half % N == 0) {
     t.mode = 1;
     const int at = low ? c0 : c0 - half;
-    if (p.wide_tables) {
+    bool one = true;  // these pairs turn by one position
+    if constexpr (kAxes) {
+      const uint32_t bits = p.axis_bits[at >> 4] >> (2 * (at & 15)) & ((1u << (2 * N)) - 1u);
+      one = bits == (bits & 3u) * (0x5555u & ((1u << (2 * N)) - 1u));
+    }
+    if (p.wide_tables && one) {
+      const int64_t at0 = pair_at<kAxes>(p, row, pos, at);
 #pragma unroll
       for (int e = 0; e < N; e += 4) {
-        const float4 c = __ldg(reinterpret_cast<const float4*>(cos + at + e));
-        const float4 s = __ldg(reinterpret_cast<const float4*>(sin + at + e));
+        const float4 c = __ldg(reinterpret_cast<const float4*>(p.cos + at0 + e));
+        const float4 s = __ldg(reinterpret_cast<const float4*>(p.sin + at0 + e));
         t.c[e] = c.x, t.c[e + 1] = c.y, t.c[e + 2] = c.z, t.c[e + 3] = c.w;
         t.s[e] = s.x, t.s[e + 1] = s.y, t.s[e + 2] = s.z, t.s[e + 3] = s.w;
       }
     } else {
 #pragma unroll
       for (int e = 0; e < N; ++e) {
-        t.c[e] = __ldg(cos + at + e);
-        t.s[e] = __ldg(sin + at + e);
+        const int64_t i = pair_at<kAxes>(p, row, pos, at + e);
+        t.c[e] = __ldg(p.cos + i);
+        t.s[e] = __ldg(p.sin + i);
       }
     }
 #pragma unroll
@@ -107,8 +101,9 @@ __device__ __forceinline__ Turn<N> load_turn(const AppendRowsParams& p, int64_t 
     const int ch = c0 + e;
     const bool first = ch < half;
     const bool on = ch < p.rot;
-    t.c[e] = on ? __ldg(cos + (first ? ch : ch - half)) : 1.0f;
-    const float s = on ? __ldg(sin + (first ? ch : ch - half)) : 0.0f;
+    const int64_t at = on ? pair_at<kAxes>(p, row, pos, first ? ch : ch - half) : 0;
+    t.c[e] = on ? __ldg(p.cos + at) : 1.0f;
+    const float s = on ? __ldg(p.sin + at) : 0.0f;
     t.s[e] = first ? -s : s;
   }
   return t;
@@ -244,29 +239,6 @@ __device__ __forceinline__ void store_row4(uint8_t* blk, int r, bool is_v, int l
   }
 }
 
-// The sequence that packed row `row` belongs to (its rows [*a, *e)), by a search of 32 offsets at a
-// time; -1 past the last.  Offsets that decrease are flagged elsewhere; here they may lose a row.
-__device__ __forceinline__ int find_seq(const int32_t* off, int batch, int64_t row, int lane, int32_t* a, int32_t* e) {
-  int lo = 0, n = batch + 1;  // the last offset <= row lies in [lo, lo + n)
-  int32_t mine = 0;
-  while (true) {
-    const int step = (n + 31) / 32;
-    const int at = lo + lane * step;
-    mine = lane * step < n ? off[at] : 2147483647;
-    const uint32_t m = __ballot_sync(0xffffffffu, lane * step < n && mine <= row);
-    if (m == 0) return -1;
-    const int k = 31 - __clz(m);
-    lo += k * step;
-    if (step == 1) {
-      if (lo >= batch) return -1;
-      *a = __shfl_sync(0xffffffffu, mine, k);
-      *e = off[lo + 1];
-      return lo;
-    }
-    n = min(step, n - k * step);
-  }
-}
-
 // Row `row` of the call: its sequence and position.  False: none, or its sequence's offsets are invalid.
 __device__ __forceinline__ bool row_place(const AppendRowsParams& p, int64_t row, int lane, int& b, int64_t& pos) {
   int32_t a, e;
@@ -280,14 +252,21 @@ __device__ __forceinline__ bool row_place(const AppendRowsParams& p, int64_t row
   pos = (int64_t)p.start_pos[b] + (row - a);
   return true;
 }
-__device__ __forceinline__ bool pos_ok(const AppendRowsParams& p, int64_t pos) {
-  return pos >= 0 && pos < (int64_t)p.max_pages * p.page_size && (p.rot == 0 || pos < p.num_positions);
+// (Whole warp.)  The row has a slot at pos, and the tables have its position, or all of its axes'.
+template <bool kAxes>
+__device__ __forceinline__ bool pos_ok(const AppendRowsParams& p, int64_t row, int64_t pos, int lane) {
+  const bool slot = pos >= 0 && pos < (int64_t)p.max_pages * p.page_size;
+  if constexpr (kAxes)
+    return __all_sync(0xffffffffu, slot && (lane >= p.num_axes || (uint32_t)__ldg(p.positions + row * p.num_axes + lane) < (uint32_t)p.num_positions));
+  else
+    return slot && (p.rot == 0 || pos < p.num_positions);
 }
 __device__ __forceinline__ void flag(int32_t* err, int lane, int bits) {
   if (lane == 0 && err) atomicOr(err, bits);
 }
 
 // Heads h0 .. h0 + kQHeads - 1 of a token's queries.  A lane's partner channels are another lane's of its half warp.
+template <bool kAxes>
 __device__ __forceinline__ void rotate_queries(const AppendRowsParams& p, int64_t row, int h0, int lane) {
   constexpr int kN = kQHeads / 2;
   const int c0 = 8 * (lane & 15), h = h0 + (lane >> 4);
@@ -300,8 +279,8 @@ __device__ __forceinline__ void rotate_queries(const AppendRowsParams& p, int64_
   int b;
   int64_t pos;
   if (!row_place(p, row, lane, b, pos)) return;
-  if (!pos_ok(p, pos)) return flag(p.err, lane, CAI_DEVERR_LENGTH);
-  const Turn<8> turn = load_turn<8>(p, pos, c0);
+  if (!pos_ok<kAxes>(p, row, pos, lane)) return flag(p.err, lane, CAI_DEVERR_LENGTH);
+  const Turn<8> turn = load_turn<8, kAxes>(p, row, pos, c0);
   const int other = lane + partner_of<8>(p, c0) / 8;
 #pragma unroll
   for (int u = 0; u < kN; ++u) {
@@ -321,7 +300,7 @@ __device__ __forceinline__ void rotate_queries(const AppendRowsParams& p, int64_
 }
 
 // Row `row` of head h's K or V at position pos, four channels a lane.
-template <class T>
+template <class T, bool kAxes>
 __device__ __forceinline__ void load_row(const AppendRowsParams& p, int64_t row, int h, bool is_v, int64_t pos, int lane, float (&x)[4]) {
   if (is_v) {
     load_n(static_cast<const T*>(p.v) + row * p.v_stride + h * kHeadDim + 4 * lane, x);
@@ -330,23 +309,23 @@ __device__ __forceinline__ void load_row(const AppendRowsParams& p, int64_t row,
     float y[4];
     load_n(src + 4 * lane, x);
     load_n(src + 4 * lane + partner_of<4>(p, 4 * lane), y);
-    const Turn<4> turn = load_turn<4>(p, pos, 4 * lane);
+    const Turn<4> turn = load_turn<4, kAxes>(p, row, pos, 4 * lane);
     turn_row(p, turn, src, 4 * lane, x, y);
   }
 }
 
-template <bool kFour, class T>
+template <bool kFour, class T, bool kAxes>
 __device__ __forceinline__ void append_row(const AppendRowsParams& p, int64_t row, int h, bool is_v, int lane) {
   int b;
   int64_t pos;
   if (!row_place(p, row, lane, b, pos)) return;
-  if (!pos_ok(p, pos)) return flag(p.err, lane, CAI_DEVERR_LENGTH);
+  if (!pos_ok<kAxes>(p, row, pos, lane)) return flag(p.err, lane, CAI_DEVERR_LENGTH);
   const int P = p.page_size;
   const int32_t page = p.table[(int64_t)b * p.max_pages + (pos >> page_log2(P))];
   if (page < 0 || page >= p.num_pages[h]) return flag(p.err, lane, CAI_DEVERR_PAGE);
   const int slot = (int)pos & (P - 1);
   float x[4];
-  load_row<T>(p, row, h, is_v, pos, lane, x);
+  load_row<T, kAxes>(p, row, h, is_v, pos, lane, x);
   if constexpr (kFour)
     store_row4(p.pages[h] + (int64_t)page * page_bytes4(P) + (slot / kBlk) * kBlkBytes, slot % kBlk, is_v, lane, x);
   else
@@ -364,7 +343,7 @@ __device__ __forceinline__ bool has_group(const Params& p, int b, int64_t u) {
 // The u-th group of 16 aligned positions that sequence b writes, head h's K and V, by a block: warp w takes
 // tokens w and w + 8.  K rows and the rows of a group that is not written whole go out as they come;
 // a whole group's V codes are gathered in shared memory ([token][channel] bytes).
-template <bool kFour, class T>
+template <bool kFour, class T, bool kAxes>
 __device__ __forceinline__ void append_group(const AppendRowsParams& p, int b, int64_t u, int h, uint32_t (*codes)[kHeadDim / 4]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const NewRows nr = new_rows(p, b);
@@ -377,21 +356,30 @@ __device__ __forceinline__ void append_group(const AppendRowsParams& p, int b, i
   int hi = (int)(left < kBlk ? left : kBlk);
   const int P = p.page_size;
   if (pos0 < 0 || pos0 >= (int64_t)p.max_pages * P) return flag(p.err, threadIdx.x, CAI_DEVERR_LENGTH);
-  if (p.rot > 0 && pos0 + hi > p.num_positions) {
+  if (!kAxes && p.rot > 0 && pos0 + hi > p.num_positions) {
     flag(p.err, threadIdx.x, CAI_DEVERR_LENGTH);
     if (pos0 + lo >= p.num_positions) return;
     hi = (int)(p.num_positions - pos0);
   }
   const int32_t page = p.table[(int64_t)b * p.max_pages + (pos0 >> page_log2(P))];
   const int64_t row0 = nr.r0 + (pos0 - start);
-  const bool whole = lo == 0 && hi == kBlk;
+  uint32_t out = 0;  // tokens left out: a position on some axis that the tables do not have (every warp finds the same)
+  if constexpr (kAxes) {
+    bool bad = false;
+    if (lane >= lo && lane < hi)
+      for (int a = 0; a < p.num_axes; ++a)
+        bad |= (uint32_t)__ldg(p.positions + (row0 + lane) * p.num_axes + a) >= (uint32_t)p.num_positions;
+    out = __ballot_sync(0xffffffffu, bad);
+    if (out) flag(p.err, threadIdx.x, CAI_DEVERR_LENGTH);
+  }
+  const bool whole = lo == 0 && hi == kBlk && out == 0;
   float x[2][2][4];  // [token][K, V]
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int r = warp + 8 * k;
-    if (r < lo || r >= hi) continue;
-    load_row<T>(p, row0 + r, h, true, pos0 + r, lane, x[k][1]);
-    load_row<T>(p, row0 + r, h, false, pos0 + r, lane, x[k][0]);
+    if (r < lo || r >= hi || (kAxes && (out >> r & 1u))) continue;
+    load_row<T, kAxes>(p, row0 + r, h, true, pos0 + r, lane, x[k][1]);
+    load_row<T, kAxes>(p, row0 + r, h, false, pos0 + r, lane, x[k][0]);
   }
   if (page < 0 || page >= p.num_pages[h]) return flag(p.err, threadIdx.x, CAI_DEVERR_PAGE);
   const int s0 = (int)pos0 & (P - 1);
@@ -400,7 +388,7 @@ __device__ __forceinline__ void append_group(const AppendRowsParams& p, int b, i
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
     const int r = warp + 8 * k;
-    if (r < lo || r >= hi) continue;
+    if (r < lo || r >= hi || (kAxes && (out >> r & 1u))) continue;
     if constexpr (kFour) {
       store_row4(blk, r, false, lane, x[k][0]);
       if (whole) {
@@ -452,7 +440,7 @@ __device__ __forceinline__ void append_group(const AppendRowsParams& p, int b, i
 // kMany: there are fewer blocks than groups that every sequence might have; a block looks through its share of these, 32
 // at a time, for those with rows.  (A prompt of 4096 tokens beside 135 single ones, 8 K/V heads: 44 us, a block for each
 // possible group 350.)
-template <bool kFour, class T, bool kMany>
+template <bool kFour, class T, bool kAxes, bool kMany>
 __global__ void __launch_bounds__(kRowWarps * 32, 4) append_rows_kernel(const __grid_constant__ AppendRowsParams p) {
   __shared__ uint32_t codes[kBlk][kHeadDim / 4];
   grid_dependency_wait();
@@ -481,27 +469,27 @@ __global__ void __launch_bounds__(kRowWarps * 32, 4) append_rows_kernel(const __
           }
           for (uint32_t m = __ballot_sync(0xffffffffu, rows_there); m; m &= m - 1) {  // (the same in all warps)
             place(blk + (int64_t)(__ffs(m) - 1) * p.kv_blocks, b, u, h);
-            append_group<kFour, T>(p, b, u, h, codes);
+            append_group<kFour, T, kAxes>(p, b, u, h, codes);
             __syncthreads();  // the codes are read
           }
         }
       } else {
         place(blk, b, u, h);
-        append_group<kFour, T>(p, b, u, h, codes);
+        append_group<kFour, T, kAxes>(p, b, u, h, codes);
       }
       return;
     }
     const int64_t w = blk * kRowWarps + warp, row = over(w, 2 * p.num_kv_heads);
     const int unit = (int)(w - row * (2 * p.num_kv_heads));
     const bool is_v = unit >= p.num_kv_heads;
-    if (row < rows) append_row<kFour, T>(p, row, is_v ? unit - p.num_kv_heads : unit, is_v, lane);
+    if (row < rows) append_row<kFour, T, kAxes>(p, row, is_v ? unit - p.num_kv_heads : unit, is_v, lane);
     return;
   }
   blk -= p.kv_blocks;
   if (blk < p.q_blocks) {
     const int per = (p.num_q_heads + kQHeads - 1) / kQHeads;  // warps of a token
     const int64_t w = blk * kRowWarps + warp, row = over(w, per);
-    if (row < rows) rotate_queries(p, row, (int)(w - row * per) * kQHeads, lane);
+    if (row < rows) rotate_queries<kAxes>(p, row, (int)(w - row * per) * kQHeads, lane);
     return;
   }
   // Packed offsets.
@@ -714,10 +702,14 @@ int32_t most_groups(const Params& p) {
   return (int32_t)(((int64_t)(p.q_off ? std::min(p.n_new, p.total_new) : p.n_new) + 2 * kBlk - 2) / kBlk);
 }
 
+template <bool kFour, class T, bool kAxes>
+cudaError_t launch_append_axes(const AppendRowsParams& p, unsigned grid, bool many, cudaStream_t stream) {
+  return many ? launch_pdl(append_rows_kernel<kFour, T, kAxes, true>, dim3(grid), dim3(kRowWarps * 32), 0, stream, p)
+              : launch_pdl(append_rows_kernel<kFour, T, kAxes, false>, dim3(grid), dim3(kRowWarps * 32), 0, stream, p);
+}
 template <bool kFour, class T>
 cudaError_t launch_append_many(const AppendRowsParams& p, unsigned grid, bool many, cudaStream_t stream) {
-  return many ? launch_pdl(append_rows_kernel<kFour, T, true>, dim3(grid), dim3(kRowWarps * 32), 0, stream, p)
-              : launch_pdl(append_rows_kernel<kFour, T, false>, dim3(grid), dim3(kRowWarps * 32), 0, stream, p);
+  return p.positions ? launch_append_axes<kFour, T, true>(p, grid, many, stream) : launch_append_axes<kFour, T, false>(p, grid, many, stream);
 }
 template <bool kFour, class T>
 cudaError_t launch_read_many(const ReadRowsParams& p, dim3 grid, bool many, cudaStream_t stream) {
