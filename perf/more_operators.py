@@ -455,7 +455,11 @@ def _own(st):
             bytes_ = cai.cai_page_bytes(page) if eight else cai.cai_kv4_page_bytes(page)
             st["handles"] = [pool(p.numel() // bytes_, page, pages=p) for p in st["arena"]]
         if "data" in st:
-            st["summaries"] = [cai.KVSummary(x.numel() // 260, page, data=x) for x in st["data"]]
+            size = st["data"].shape[1]  # the library wants each buffer at a multiple of 16 bytes
+            room = torch.empty(hkv, -(-size // 16) * 16, dtype=torch.uint8, device=DEV)
+            room[:, :size] = st["data"]
+            st["data"] = room[:, :size]
+            st["summaries"] = [cai.KVSummary(size // 260, page, data=x) for x in st["data"]]
             st.setdefault("handles", None)
         if op.startswith("axes"):
             st["rope"] = cai.RopeAxes(st["cos"], st["sin"], st["axis"], interleaved=c["inter"])
