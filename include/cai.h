@@ -457,6 +457,80 @@ cai_status cai_kv4_prefill(const cai_kv4_pool* kv_pools, int32_t num_kv_heads, c
                            int32_t window, float softmax_scale, void* workspace, size_t workspace_bytes,
                            uint16_t* out, float* lse_out, int32_t* err_flag, void* stream);
 
+/* ---- Attention over a part of a long context --------------------------------
+ * A query of a long context needs few of its pages.  Three operators, for both caches:
+ * cai_kv_summarize keeps, for every page, the range of its keys; cai_kv_select reads these
+ * summaries (260 bytes a page and K/V head) and lists the pages in which each query may have its
+ * largest logits; cai_kv_attend_pages attends over the listed pages.  A decode step is
+ * append, summarize, select, attend, each on the same block tables; a chunk of n_new tokens a
+ * sequence is the same calls, every row with lists of its own.  Rows are given as in the
+ * section on rotated appends (n_new a sequence, or packed by q_offsets). */
+
+/* Summaries of one pool's pages: `data` holds int8 [num_pages][256], page by page the codes of
+ * the 128 channels' largest keys and of their smallest, then fp32 [num_pages], the scales.  It
+ * must be 16-byte aligned and holds cai_kv_summary_bytes(num_pages, head_dim) bytes.  A page's
+ * summary belongs to the page: sequences that share the page share it. */
+typedef struct cai_kv_summary {
+  void* data;
+  int32_t num_pages;
+  int32_t page_size; /* 16, 32 or 64 tokens */
+  int32_t head_dim;  /* 128 */
+} cai_kv_summary;
+
+/* num_pages * (2 * head_dim + 4); 0 for non-positive arguments. */
+size_t cai_kv_summary_bytes(int32_t num_pages, int32_t head_dim);
+
+/* Bring the summaries of the pages that new tokens lie in up to date: call it behind the append,
+ * with the append's table, start_pos and counts (or with start_pos 0 and the lengths, for
+ * dialogues whose summaries are not there).  Every page that holds a position of
+ * [start_pos[b], start_pos[b] + n) is computed anew from the cached keys of its tokens, those
+ * before start_pos included, none at or past start_pos[b] + n.
+ * With x the fp32 values that the cached keys stand for, hi_c and lo_c their largest and smallest
+ * of channel c: s = max_c max(|hi_c|, |lo_c|) / 127 (IEEE fp32 division), codes
+ * min(127, ceil(hi_c / s)) and max(-127, floor(lo_c / s)); all 0 when s is 0.
+ *   kv_pools, summaries   host arrays [num_kv_heads], of the same page counts
+ *   n_new, q_offsets      as for the append; q_offsets[batch] is not limited here
+ * Bad positions, page ids and offsets as in cai_kv_append_rope; other summaries are not touched. */
+cai_status cai_kv_summarize(const cai_kv_pool* kv_pools, const cai_kv_summary* summaries, int32_t num_kv_heads,
+                            int32_t batch, int32_t n_new, const int32_t* q_offsets, const int32_t* block_table,
+                            int32_t max_pages_per_seq, const int32_t* start_pos, int32_t* err_flag, void* stream);
+cai_status cai_kv4_summarize(const cai_kv4_pool* kv_pools, const cai_kv_summary* summaries, int32_t num_kv_heads,
+                             int32_t batch, int32_t n_new, const int32_t* q_offsets, const int32_t* block_table,
+                             int32_t max_pages_per_seq, const int32_t* start_pos, int32_t* err_flag, void* stream);
+
+/* For every row of queries and K/V head the pages to attend over.  Row i of sequence b sits at
+ * position p = start_pos[b] + i (decode: start_pos = context length - 1) and sees the n = p / P + 1
+ * pages of its table row.  It takes all of them where n <= num_selected; otherwise the `first`
+ * first and `last` last ones, and those of the largest scores among the rest, ties by the lower
+ * page.  A head's query becomes whole numbers q'_c = clamp(round_half_even(q_c / t), -127, 127),
+ * t = max |q_c| / 127 (IEEE fp32 divisions; 0 when t is 0); with a page's codes hi, lo and
+ * scale s, score = s * max over the group's heads of t * sum_c max(q'_c hi_c, q'_c lo_c), each of
+ * the two products rounded to fp32 once: what the largest logit of the page may be, up to the
+ * roundings and for positive softmax scales (negate q for a negative one).
+ *   summaries     host array [num_kv_heads], one per K/V head, brought up to date
+ *   q             bf16 bits [rows][num_q_heads][128] (rotated, as for the attention), 16-byte aligned
+ *   num_q_heads   a multiple of num_kv_heads; up to 128 query heads per K/V head
+ *   num_selected  pages of a row, first + last at least; first >= 0, last >= 1 (a row's own page
+ *                 is always taken)
+ *   workspace     cai_kv_select_workspace_size() bytes for the call's rows (batch * n_new, or
+ *                 total_new), 256-byte aligned; no preparation.  Calls that share it must not
+ *                 overlap on the GPU
+ *   pages_out     int32 [rows][num_kv_heads][num_selected]: page ids in the order of positions, -1
+ *                 behind the last
+ *   len_out       int32 [rows]: the tokens of these lists, the same for all K/V heads: all pages
+ *                 are whole but the row's own, which comes last
+ * A row that no sequence has (behind the last one, in a padded batch), of a sequence with invalid
+ * offsets or at a position outside the table gets a list of -1 and length 0; the latter two
+ * set CAI_DEVERR_LENGTH.  A page id outside the summaries sets CAI_DEVERR_PAGE; it has the least
+ * score, and stands in the list if it is taken all the same. */
+size_t cai_kv_select_workspace_size(int32_t batch, int32_t total_rows, int32_t num_q_heads, int32_t num_kv_heads,
+                                    int32_t max_pages_per_seq);
+cai_status cai_kv_select(const cai_kv_summary* summaries, int32_t num_kv_heads, const uint16_t* q, int32_t batch,
+                         int32_t n_new, const int32_t* q_offsets, int32_t total_new, int32_t num_q_heads,
+                         const int32_t* block_table, int32_t max_pages_per_seq, const int32_t* start_pos,
+                         int32_t num_selected, int32_t first, int32_t last, void* workspace, size_t workspace_bytes,
+                         int32_t* pages_out, int32_t* len_out, int32_t* err_flag, void* stream);
+
 /* ---- Cross-turn KV cache in host memory ----------------------------------
  * "Character.AI: inference optimization", 04 Cache between turns: the KV of
  * every processed prefix and generated message is kept in host memory in an

@@ -27,6 +27,8 @@ __all__ = [
     "cai_host_cache_stats", "cai_host_cache_restore_batch", "cai_set_wait_limit_ns", "cai_set_fault_injection", "cai_ring_pages", "cai_ring_table_row",
     "KV4Pool", "Rope", "cai_kv4_page_bytes", "cai_kv_append_rope", "cai_kv4_append", "cai_kv_read", "cai_kv4_read",
     "RopeAxes", "cai_kv_append_rope_axes", "cai_kv4_append_axes",
+    "KVSummary", "cai_kv_summary_bytes", "cai_kv_summarize", "cai_kv4_summarize",
+    "cai_kv_select_workspace_size", "cai_kv_select",
     "cai_kv4_decode_workspace_size", "cai_kv4_decode", "cai_kv4_prefill_workspace_size", "cai_kv4_prefill",
 ]
 
@@ -56,6 +58,11 @@ class cai_kv_pool(ctypes.Structure):
 
 class cai_kv4_pool(ctypes.Structure):
     _fields_ = cai_kv_pool._fields_
+
+
+class cai_kv_summary(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("num_pages", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32)]
 
 
 class cai_rope(ctypes.Structure):
@@ -138,6 +145,17 @@ def load():
         f = getattr(lib, name)
         f.argtypes = [pp, i32, vp, vp, ctypes.c_int, i32, i32, vp, i32, vp, i32, vp, vp, vp]
         f.restype = ctypes.c_int
+    sum_p = ctypes.POINTER(cai_kv_summary)
+    lib.cai_kv_summary_bytes.argtypes = [i32, i32]
+    lib.cai_kv_summary_bytes.restype = sz
+    for name, pp in (("cai_kv_summarize", pool_p), ("cai_kv4_summarize", pool4_p)):
+        f = getattr(lib, name)
+        f.argtypes = [pp, sum_p, i32, i32, i32, vp, vp, i32, vp, vp, vp]
+        f.restype = ctypes.c_int
+    lib.cai_kv_select_workspace_size.argtypes = [i32] * 5
+    lib.cai_kv_select_workspace_size.restype = sz
+    lib.cai_kv_select.argtypes = [sum_p, i32, vp, i32, i32, vp, i32, i32, vp, i32, vp, i32, i32, i32, vp, sz, vp, vp, vp, vp]
+    lib.cai_kv_select.restype = ctypes.c_int
     lib.cai_kv4_decode_workspace_size.argtypes = [i32] * 7
     lib.cai_kv4_decode_workspace_size.restype = sz
     lib.cai_kv4_decode.argtypes = [pool4_p, i32, vp, i32, i32, vp, i32, vp, i32, ctypes.c_float, i32, vp, sz, vp, vp, vp,
@@ -814,3 +832,97 @@ def cai_kv4_prefill(pools: Sequence[KV4Pool], q: torch.Tensor, block_table: torc
         _data(lse_out, "lse_out", dev, torch.float32, q.shape[:-1]), _data(err_flag, "err_flag", dev, torch.int32),
         _stream_of(stream, dev))
     _check(st, "cai_kv4_prefill")
+
+
+# ---- Attention over a part of a long context ------------------------------------------------
+
+def cai_kv_summary_bytes(num_pages: int, head_dim: int = HEAD_DIM) -> int:
+    return int(load().cai_kv_summary_bytes(num_pages, head_dim))
+
+
+class KVSummary:
+    """Summaries of one pool's pages in one uint8 CUDA tensor (cai_kv_summary_bytes): int8 codes [num_pages][256], the
+    channels' largest keys and their smallest, then fp32 scales [num_pages].  ``data`` may be given."""
+
+    def __init__(self, num_pages: int, page_size: int, head_dim: int = HEAD_DIM, device=None,
+                 data: Optional[torch.Tensor] = None):
+        nbytes = cai_kv_summary_bytes(num_pages, head_dim)
+        if data is None:
+            data = torch.zeros(nbytes, dtype=torch.uint8, device=device or "cuda")
+        if data.dtype != torch.uint8 or data.numel() != nbytes or not data.is_cuda or not data.is_contiguous():
+            raise ValueError("data must be a contiguous uint8 CUDA tensor of cai_kv_summary_bytes bytes")
+        self.data = data
+        self.num_pages, self.page_size, self.head_dim = num_pages, page_size, head_dim
+        self.struct = cai_kv_summary(data.data_ptr(), num_pages, page_size, head_dim)
+
+
+def _summary_array(summaries, dev: int):
+    if isinstance(summaries, KVSummary):
+        summaries = (summaries,)
+    for s in summaries:
+        if not isinstance(s, KVSummary):
+            raise TypeError(f"summaries must be KVSummary objects, got {type(s).__name__}")
+        if s.data.get_device() != dev:
+            raise ValueError(f"a summary is on {s.data.device}, the current device is cuda:{dev}")
+    n = len(summaries)
+    return (ctypes.byref(summaries[0].struct) if n == 1 else (cai_kv_summary * n)(*[s.struct for s in summaries])), n
+
+
+def _summarize(entry: str, kind, pools, summaries, block_table, start_pos, n_new, q_offsets, err_flag, stream) -> None:
+    dev, arr, hkv = _begin(pools, kind, block_table, "block_table")
+    sums, n = _summary_array(summaries, dev)
+    if n != hkv:
+        raise ValueError(f"{n} summaries for {hkv} pools")
+    batch = start_pos.shape[0]
+    table, width = _table(block_table, batch, dev)
+    st = getattr(load(), entry)(
+        arr, sums, hkv, batch, int(n_new), _data(q_offsets, "q_offsets", dev, torch.int32, (batch + 1,)), table, width,
+        _data(start_pos, "start_pos", dev, torch.int32, (batch,)), _data(err_flag, "err_flag", dev, torch.int32),
+        _stream_of(stream, dev))
+    _check(st, entry)
+
+
+def cai_kv_summarize(pools: Sequence[KVPool], summaries: Sequence[KVSummary], block_table: torch.Tensor,
+                     start_pos: torch.Tensor, n_new: int, q_offsets: Optional[torch.Tensor] = None,
+                     err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Summaries of the pages that hold positions start_pos[b] .. + n_new - 1 (with q_offsets: as many as sequence b has
+    rows, n_new at most) from the keys cached up to there; to be called behind the append of these tokens."""
+    _summarize("cai_kv_summarize", KVPool, pools, summaries, block_table, start_pos, n_new, q_offsets, err_flag, stream)
+
+
+def cai_kv4_summarize(pools: Sequence[KV4Pool], summaries: Sequence[KVSummary], block_table: torch.Tensor,
+                      start_pos: torch.Tensor, n_new: int, q_offsets: Optional[torch.Tensor] = None,
+                      err_flag: Optional[torch.Tensor] = None, stream=None) -> None:
+    """cai_kv_summarize of the 4-bit cache."""
+    _summarize("cai_kv4_summarize", KV4Pool, pools, summaries, block_table, start_pos, n_new, q_offsets, err_flag, stream)
+
+
+def cai_kv_select_workspace_size(batch: int, total_rows: int, num_q_heads: int, num_kv_heads: int,
+                                 max_pages_per_seq: int) -> int:
+    return int(load().cai_kv_select_workspace_size(batch, total_rows, num_q_heads, num_kv_heads, max_pages_per_seq))
+
+
+def cai_kv_select(summaries: Sequence[KVSummary], q: torch.Tensor, block_table: torch.Tensor, start_pos: torch.Tensor,
+                  first: int, last: int, workspace: torch.Tensor, pages_out: torch.Tensor, len_out: torch.Tensor,
+                  err_flag: Optional[torch.Tensor] = None, q_offsets: Optional[torch.Tensor] = None,
+                  max_new: Optional[int] = None, stream=None) -> None:
+    """The pages that each row of queries q bf16 [batch][n_new][Hq][128] (packed: [rows][Hq][128] with q_offsets and
+    max_new) takes: pages_out int32 [..rows..][K/V heads][selected], len_out int32 [..rows..]; the `first` first and
+    `last` last pages of a row's context always, the others by score."""
+    dev = q.get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"q is on {q.device}, not on the current CUDA device")
+    sums, hkv = _summary_array(summaries, dev)
+    rows, batch, n_new, hq = _rows(q, "q", q_offsets, max_new, start_pos)
+    lead = q.shape[:-2]
+    table, width = _table(block_table, batch, dev)
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    keep = pages_out.shape[-1]
+    st = load().cai_kv_select(
+        sums, hkv, _data(q, "q", dev, torch.bfloat16), batch, n_new,
+        _data(q_offsets, "q_offsets", dev, torch.int32, (batch + 1,)), rows, hq, table, width,
+        _data(start_pos, "start_pos", dev, torch.int32, (batch,)), keep, int(first), int(last),
+        _data(workspace, "workspace", dev), ws_bytes, _data(pages_out, "pages_out", dev, torch.int32, (*lead, hkv, keep)),
+        _data(len_out, "len_out", dev, torch.int32, lead), _data(err_flag, "err_flag", dev, torch.int32),
+        _stream_of(stream, dev))
+    _check(st, "cai_kv_select")

@@ -179,6 +179,38 @@ struct Decode4Params {
   int32_t overlap_prev;    // as in DecodeParams
 };
 
+// Page summaries of the pages that a call's new tokens lie in.
+struct SummarizeParams {
+  const uint8_t* pages[kMaxKvHeads];
+  int32_t num_pages[kMaxKvHeads];
+  uint8_t* data[kMaxKvHeads];   // [num_pages][256] codes, then [num_pages] scales
+  int32_t num_kv_heads, page_size, max_pages;
+  int32_t batch, n_new, total_new;
+  const int32_t* q_off;
+  const int32_t* table;
+  const int32_t* start_pos;
+  int32_t* err;
+  int32_t groups;               // filled by the launch: pages that a sequence's new tokens may lie in
+};
+
+// Selection of pages for rows of queries.
+struct SelectParams {
+  const uint8_t* data[kMaxKvHeads];
+  int32_t num_pages[kMaxKvHeads];
+  int32_t num_kv_heads, num_q_heads, page_size, max_pages;
+  int32_t batch, n_new, total_new;
+  const int32_t* q_off;
+  const int32_t* table;
+  const int32_t* start_pos;
+  const uint16_t* q;            // bf16 bits [rows][Hq][128]
+  int32_t keep, first, last;    // pages of a row, of these at its start and its end
+  float* scores;                // workspace: [rows][Hkv][stride]
+  int64_t stride;
+  int32_t* pages_out;           // [rows][Hkv][keep]
+  int32_t* len_out;             // [rows]
+  int32_t* err;
+};
+
 struct PrefillLaunch {
   const uint8_t* pages;
   int32_t num_pages, page_size, max_pages;
@@ -249,6 +281,10 @@ cudaError_t launch_append(const AppendParams* ps, int n, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeParams& p, int page_size, cudaStream_t stream);
 cudaError_t launch_append_rows(AppendRowsParams p, bool four, bool bf16, cudaStream_t stream);
 cudaError_t launch_read_rows(ReadRowsParams p, bool four, bool bf16, cudaStream_t stream);
+cudaError_t launch_summarize(SummarizeParams p, bool four, cudaStream_t stream);
+// Elements between the score rows of one query row and K/V head.
+inline int64_t score_stride(int32_t max_pages) { return ((int64_t)max_pages + 3) / 4 * 4; }
+cudaError_t launch_select(const SelectParams& p, cudaStream_t stream);
 cudaError_t launch_decode4(const Decode4Params& p, cudaStream_t stream);
 // Fills the split fields of p (batch, heads, page_size, max_pages and window given; num_splits 0: automatic) and
 // returns the workspace bytes that they need; place_decode4 then sets the workspace's pointers.

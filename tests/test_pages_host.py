@@ -59,3 +59,84 @@ def test_axes_refusals(lib, entry):
     assert call(axis=(0,) * 32 + (9,) * 32, rope=cai.cai_rope(FAKE, FAKE, 100, 64, 0), batch=0) == 0  # entries past the pairs are not read
     assert call(rope=cai.cai_rope(FAKE, FAKE, 100, 130, 0)) == 2 and call(rope=cai.cai_rope(FAKE, FAKE, 0, 64, 0)) == 1
     assert call(pools=None) == 1 and call(k=None) == 1 and call(ks=255) == 1 and call(table=None) == 1 and call(start=None) == 1
+
+
+def test_summary_bounds_its_keys():
+    rng = np.random.default_rng(1)
+    for size in (1e-30, 1.0, 1e6):
+        k = rng.normal(size=(20, 128)).astype(np.float32) * np.float32(size)
+        codes, s = pages.summarize(k)
+        hi, lo = codes[:128].astype(np.float64) * s, codes[128:].astype(np.float64) * s
+        slack = 2.0 ** -22 * np.abs(k).max()  # of the divisions' roundings
+        assert (k <= hi + slack).all() and (k >= lo - slack).all()
+        assert (hi - k.max(0) <= s + slack).all() and (k.min(0) - lo <= s + slack).all()
+        assert np.abs(codes).max() == 127
+    codes, s = pages.summarize(np.zeros((3, 128)))
+    assert s == 0 and (codes == 0).all()
+
+
+def test_scores_bound_the_logits():
+    rng = np.random.default_rng(2)
+    k = rng.normal(size=(8, 16, 128)).astype(np.float32)
+    q = kv4.bf16_round(rng.normal(size=(5, 128)).astype(np.float32))
+    codes, scale = zip(*(pages.summarize(x) for x in k))
+    got = pages.scores(q, np.stack(codes), np.array(scale))
+    logit = np.einsum("hd,btd->bht", q.astype(np.float64), k).max((1, 2))
+    # A query's channels are off by half a code, at the summary's bounds.
+    slack = np.abs(np.stack(codes)).reshape(8, 2, 128).max(1).sum(-1) * np.array(scale) * (np.abs(q).max() / 127 / 2)
+    assert (logit <= got + slack).all()
+
+
+def test_selection_takes_ends_and_ties():
+    codes, scale = np.zeros((20, 256), np.int8), np.ones(20, np.float32)
+    blocks, tokens = pages.select(np.ones((2, 128), np.float32), codes, scale, 19 * 16 + 3, 16, 6, 1, 2)
+    assert list(blocks) == [0, 1, 2, 3, 18, 19] and tokens == 5 * 16 + 4
+    codes[7, :128] = 5
+    blocks, _ = pages.select(np.ones((2, 128), np.float32), codes, scale, 19 * 16 + 3, 16, 4, 1, 2)
+    assert list(blocks) == [0, 7, 18, 19]
+    blocks, tokens = pages.select(np.ones((2, 128), np.float32), codes, scale, 37, 16, 4, 1, 2)
+    assert list(blocks) == [0, 1, 2] and tokens == 38
+
+
+def _sums(n=2, **kw):
+    a = dict(data=FAKE, num_pages=8, page_size=16, head_dim=128)
+    a.update(kw)
+    return (cai.cai_kv_summary * n)(*[cai.cai_kv_summary(a["data"], a["num_pages"], a["page_size"], a["head_dim"])] * n)
+
+
+@pytest.mark.parametrize("entry", ["cai_kv_summarize", "cai_kv4_summarize"])
+def test_summarize_refusals(lib, entry):
+    kind = cai.cai_kv_pool if "kv4" not in entry else cai.cai_kv4_pool
+
+    def call(pools=_arr(kind), sums=_sums(), hkv=2, batch=2, n=1, off=None, table=FAKE, maxp=4, start=FAKE):
+        return getattr(lib, entry)(pools, sums, hkv, batch, n, off, table, maxp, start, None, None)
+
+    assert call(batch=0) == 0 and call(n=0) == 0
+    assert call(pools=None) == 1 and call(sums=None) == 1 and call(hkv=0) == 2 and call(hkv=9) == 2
+    assert call(sums=_sums(data=None)) == 1 and call(sums=_sums(data=FAKE + 8)) == 1 and call(sums=_sums(num_pages=7)) == 1
+    assert call(sums=_sums(page_size=32)) == 1 and call(sums=_sums(page_size=24)) == 2 and call(sums=_sums(head_dim=64)) == 2
+    assert call(table=None) == 1 and call(start=None) == 1 and call(maxp=0) == 1 and call(n=-1) == 1 and call(batch=-1) == 1
+    assert call(batch=65536) == 2 and call(n=1 << 23) == 2 and call(maxp=(1 << 30) // 16 + 1) == 2
+    assert cai.cai_kv_summary_bytes(10) == 2600 and cai.cai_kv_summary_bytes(0) == cai.cai_kv_summary_bytes(4, 0) == 0
+
+
+def test_select_refusals(lib):
+    need = cai.cai_kv_select_workspace_size(2, 2, 8, 2, 64)
+    assert need >= 2 * 2 * 64 * 4
+
+    def call(sums=_sums(), hkv=2, q=FAKE, batch=2, n=1, off=None, total=0, hq=8, table=FAKE, maxp=64, start=FAKE, keep=4,
+             first=1, last=2, ws=FAKE, ws_bytes=need, pages_out=FAKE, len_out=FAKE):
+        return lib.cai_kv_select(sums, hkv, q, batch, n, off, total, hq, table, maxp, start, keep, first, last, ws, ws_bytes,
+                                 pages_out, len_out, None, None)
+
+    assert call(batch=0) == 0 and call(n=0) == 0 and call(off=FAKE, total=0) == 0
+    assert call(sums=None) == 1 and call(hkv=0) == 2 and call(sums=_sums(page_size=8)) == 2 and call(sums=_sums(data=FAKE + 4)) == 1
+    assert call(first=-1) == 1 and call(last=0) == 1 and call(first=3, last=2) == 1 and call(keep=0) == 1
+    assert call(first=2147483647, last=2147483647) == 1 and call(keep=(1 << 26) + 1) == 2
+    assert call(hq=7) == 2 and call(hq=0) == 2 and call(hq=2 * 129) == 2
+    assert call(q=None) == 1 and call(q=FAKE + 8) == 1 and call(table=None) == 1 and call(start=None) == 1
+    assert call(pages_out=None) == 1 and call(len_out=None) == 1
+    assert call(ws=None) == 3 and call(ws_bytes=need - 1) == 3 and call(ws=FAKE + 64) == 3
+    assert call(batch=-1) == 1 and call(n=-1) == 1 and call(off=FAKE, total=-1) == 1 and call(maxp=0) == 1 and call(batch=65536) == 2
+    for bad in ((0, 2, 8, 2, 64), (2, -1, 8, 2, 64), (2, 2, 7, 2, 64), (2, 2, 8, 9, 64), (2, 2, 8, 2, 0), (65536, 2, 8, 2, 64)):
+        assert cai.cai_kv_select_workspace_size(*bad) == 0
