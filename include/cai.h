@@ -531,6 +531,34 @@ cai_status cai_kv_select(const cai_kv_summary* summaries, int32_t num_kv_heads, 
                          int32_t num_selected, int32_t first, int32_t last, void* workspace, size_t workspace_bytes,
                          int32_t* pages_out, int32_t* len_out, int32_t* err_flag, void* stream);
 
+/* Attention of rows of queries over lists of pages, a list for each K/V head: over the tokens of
+ * the listed pages in turn, the first len[r] of them.  The lists of cai_kv_select, or any other:
+ * a page that stands in a list twice counts twice, and no token is masked but by len.
+ *   q             bf16 bits [rows][num_q_heads][128], 16-byte aligned; rows <= 65535
+ *   num_q_heads   a multiple of num_kv_heads; up to 128 query heads per K/V head
+ *   pages         int32 [rows][num_kv_heads][width]; entries behind ceil(len[r] / P) are not read
+ *   len           int32 [rows]; 0: out = 0, lse = -inf.  Outside [0, width * P]: the same, and
+ *                 CAI_DEVERR_LENGTH
+ *   out           bf16 bits [rows][num_q_heads][128], 16-byte aligned, rounded once from fp32
+ *   lse_out       fp32 [rows][num_q_heads], nullable
+ *   workspace     cai_kv_attend_pages_workspace_size() bytes (cai_kv4_... for the 4-bit cache), 256-byte
+ *                 aligned, no preparation; may be null when that is 0.  Calls that share it must not
+ *                 overlap on the GPU
+ *   num_splits, softmax_scale, roundings and errors otherwise as cai_kv4_decode, for the int8 cache, too
+ *   (there a V scale below 2^-100 counts as 2^-100). */
+size_t cai_kv_attend_pages_workspace_size(int32_t rows, int32_t num_q_heads, int32_t num_kv_heads, int32_t width,
+                                          int32_t page_size, int32_t num_splits);
+cai_status cai_kv_attend_pages(const cai_kv_pool* kv_pools, int32_t num_kv_heads, const uint16_t* q, int32_t rows,
+                               int32_t num_q_heads, const int32_t* pages, int32_t width, const int32_t* len,
+                               float softmax_scale, int32_t num_splits, void* workspace, size_t workspace_bytes,
+                               uint16_t* out, float* lse_out, int32_t* err_flag, void* stream);
+size_t cai_kv4_attend_pages_workspace_size(int32_t rows, int32_t num_q_heads, int32_t num_kv_heads, int32_t width,
+                                           int32_t page_size, int32_t num_splits);
+cai_status cai_kv4_attend_pages(const cai_kv4_pool* kv_pools, int32_t num_kv_heads, const uint16_t* q, int32_t rows,
+                                int32_t num_q_heads, const int32_t* pages, int32_t width, const int32_t* len,
+                                float softmax_scale, int32_t num_splits, void* workspace, size_t workspace_bytes,
+                                uint16_t* out, float* lse_out, int32_t* err_flag, void* stream);
+
 /* ---- Cross-turn KV cache in host memory ----------------------------------
  * "Character.AI: inference optimization", 04 Cache between turns: the KV of
  * every processed prefix and generated message is kept in host memory in an

@@ -28,7 +28,8 @@ __all__ = [
     "KV4Pool", "Rope", "cai_kv4_page_bytes", "cai_kv_append_rope", "cai_kv4_append", "cai_kv_read", "cai_kv4_read",
     "RopeAxes", "cai_kv_append_rope_axes", "cai_kv4_append_axes",
     "KVSummary", "cai_kv_summary_bytes", "cai_kv_summarize", "cai_kv4_summarize",
-    "cai_kv_select_workspace_size", "cai_kv_select",
+    "cai_kv_select_workspace_size", "cai_kv_select", "cai_kv_attend_pages_workspace_size", "cai_kv_attend_pages",
+    "cai_kv4_attend_pages_workspace_size", "cai_kv4_attend_pages",
     "cai_kv4_decode_workspace_size", "cai_kv4_decode", "cai_kv4_prefill_workspace_size", "cai_kv4_prefill",
 ]
 
@@ -156,6 +157,13 @@ def load():
     lib.cai_kv_select_workspace_size.restype = sz
     lib.cai_kv_select.argtypes = [sum_p, i32, vp, i32, i32, vp, i32, i32, vp, i32, vp, i32, i32, i32, vp, sz, vp, vp, vp, vp]
     lib.cai_kv_select.restype = ctypes.c_int
+    for name, pp in (("cai_kv_attend_pages", pool_p), ("cai_kv4_attend_pages", pool4_p)):
+        f = getattr(lib, name + "_workspace_size")
+        f.argtypes = [i32] * 6
+        f.restype = sz
+        f = getattr(lib, name)
+        f.argtypes = [pp, i32, vp, i32, i32, vp, i32, vp, ctypes.c_float, i32, vp, sz, vp, vp, vp, vp]
+        f.restype = ctypes.c_int
     lib.cai_kv4_decode_workspace_size.argtypes = [i32] * 7
     lib.cai_kv4_decode_workspace_size.restype = sz
     lib.cai_kv4_decode.argtypes = [pool4_p, i32, vp, i32, i32, vp, i32, vp, i32, ctypes.c_float, i32, vp, sz, vp, vp, vp,
@@ -926,3 +934,50 @@ def cai_kv_select(summaries: Sequence[KVSummary], q: torch.Tensor, block_table: 
         _data(len_out, "len_out", dev, torch.int32, lead), _data(err_flag, "err_flag", dev, torch.int32),
         _stream_of(stream, dev))
     _check(st, "cai_kv_select")
+
+
+def cai_kv_attend_pages_workspace_size(rows: int, num_q_heads: int, num_kv_heads: int, width: int, page_size: int,
+                                       num_splits: int = 0) -> int:
+    return int(load().cai_kv_attend_pages_workspace_size(rows, num_q_heads, num_kv_heads, width, page_size, num_splits))
+
+
+def cai_kv4_attend_pages_workspace_size(rows: int, num_q_heads: int, num_kv_heads: int, width: int, page_size: int,
+                                        num_splits: int = 0) -> int:
+    return int(load().cai_kv4_attend_pages_workspace_size(rows, num_q_heads, num_kv_heads, width, page_size, num_splits))
+
+
+def _attend_pages(entry: str, kind, pools, q, pages, lengths, softmax_scale, num_splits, workspace, out, lse_out, err_flag,
+                  stream) -> None:
+    dev, arr, hkv = _begin(pools, kind, q, "q")
+    n = q.shape
+    if len(n) != 3 or n[2] != HEAD_DIM:
+        raise ValueError(f"q has shape {tuple(n)}, expected [rows][heads][{HEAD_DIM}]")
+    rows, hq = n[0], n[1]
+    width = pages.shape[-1]
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    st = getattr(load(), entry)(
+        arr, hkv, _data(q, "q", dev, torch.bfloat16), rows, hq, _data(pages, "pages", dev, torch.int32, (rows, hkv, width)),
+        width, _data(lengths, "lengths", dev, torch.int32, (rows,)), float(softmax_scale), num_splits,
+        _data(workspace, "workspace", dev), ws_bytes, _data(out, "out", dev, torch.bfloat16, n),
+        _data(lse_out, "lse_out", dev, torch.float32, (rows, hq)), _data(err_flag, "err_flag", dev, torch.int32),
+        _stream_of(stream, dev))
+    _check(st, entry)
+
+
+def cai_kv_attend_pages(pools: Sequence[KVPool], q: torch.Tensor, pages: torch.Tensor, lengths: torch.Tensor,
+                        softmax_scale: float, num_splits: int, workspace: torch.Tensor, out: torch.Tensor,
+                        lse_out: Optional[torch.Tensor] = None, err_flag: Optional[torch.Tensor] = None,
+                        stream=None) -> None:
+    """Attention of q bf16 [rows][Hq][128] -> out bf16 over the first lengths[r] tokens of the pages that row r lists for
+    each K/V head, pages int32 [rows][K/V heads][width] (cai_kv_select's, its rows flattened)."""
+    _attend_pages("cai_kv_attend_pages", KVPool, pools, q, pages, lengths, softmax_scale, num_splits, workspace, out, lse_out,
+                  err_flag, stream)
+
+
+def cai_kv4_attend_pages(pools: Sequence[KV4Pool], q: torch.Tensor, pages: torch.Tensor, lengths: torch.Tensor,
+                         softmax_scale: float, num_splits: int, workspace: Optional[torch.Tensor], out: torch.Tensor,
+                         lse_out: Optional[torch.Tensor] = None, err_flag: Optional[torch.Tensor] = None,
+                         stream=None) -> None:
+    """cai_kv_attend_pages over the 4-bit cache."""
+    _attend_pages("cai_kv4_attend_pages", KV4Pool, pools, q, pages, lengths, softmax_scale, num_splits, workspace, out,
+                  lse_out, err_flag, stream)

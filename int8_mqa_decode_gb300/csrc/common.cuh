@@ -149,13 +149,14 @@ struct ReadRowsParams {
   int32_t groups;               // filled by the launch: groups of 16 positions that a sequence may have
 };
 
-// One decode launch over the 4-bit cache.  q_off / total_rows: as in DecodeJob.
+// One decode launch over the 4-bit cache, or over lists of pages of either.  q_off / total_rows: as in DecodeJob.
 struct Decode4Params {
   const uint8_t* pages[kMaxKvHeads];  // one pool per K/V head
   int32_t num_pages[kMaxKvHeads];
   int32_t num_heads, num_kv_heads, batch;
   int32_t page_size, max_pages, window;
   const int32_t* table;    // [B][max_pages]
+  int32_t lists;           // the table has a row for every K/V head: [B][num_kv_heads][max_pages]
   const int32_t* ctx_len;  // [B]
   int32_t before_new;      // ctx_len does not count the new token (prefill calls)
   const int32_t* q_off;    // nullable
@@ -169,6 +170,7 @@ struct Decode4Params {
   // block c and goes on in the next, {-1, -1} if nothing does.  A sequence counts piece_tiles more than it has.
   // chunk > 0: every sequence is cut into `splits` ranges of chunk keys; slot (unit * splits + range).
   int32_t head_groups, ranges, chunk, splits, piece_tiles;
+  int32_t eight;           // the int8 cache (attend8.cu): set before plan_decode4
   int2* meta;
   float* ws_o;             // [slot][query heads of a K/V head][128] normalised partial outputs
   float* ws_lse;           // [slot][query heads of a K/V head] log2 units

@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kWarps * 32, kBlocks4) decode4_kernel(const __
       const int mine = (steps - warp + kWarps - 1) / kWarps;  // this warp's steps: warp, warp + kWarps, ...
       const uint8_t* pages = p.pages[pc.kvh];
       const int num_pages = p.num_pages[pc.kvh];
-      const int32_t* table = p.table + (int64_t)pc.b * p.max_pages;
+      const int32_t* table = piece_table(p, pc);
       const uint16_t* q = p.q + row0 * kHeadDim;
       __syncthreads();  // the last piece's merge has left the ring
 
@@ -498,7 +498,7 @@ int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
 }  // namespace
 
 size_t plan_decode4(Decode4Params& p, int32_t num_splits) {
-  const int G = p.num_heads / p.num_kv_heads, tc = decode4_tc_heads(G);
+  const int G = p.num_heads / p.num_kv_heads, tc = tensor_heads(p);
   const int blocks = num_sms() * (tc ? 1 : kBlocks4);
   p.head_groups = tc ? (G + tc - 1) / tc : 1;
   // What the start and merge of a piece cost, in tiles, fitted from the times of blocks with different numbers of
@@ -540,7 +540,7 @@ void place_decode4(Decode4Params& p, void* workspace) {
 }
 
 cudaError_t launch_decode4(const Decode4Params& p, cudaStream_t stream) {
-  const cudaError_t e = decode4_tc_heads(p.num_heads / p.num_kv_heads) ? launch_decode4_tc(p, stream) : launch_heads8(p, stream);
+  const cudaError_t e = p.eight ? launch_attend8(p, stream) : tensor_heads(p) ? launch_decode4_tc(p, stream) : launch_heads8(p, stream);
   if (e != cudaSuccess || (p.chunk > 0 && p.splits <= 1)) return e;
   const int64_t G = p.num_heads / p.num_kv_heads, items = p.chunk == 0 ? p.ranges : (int64_t)p.batch * p.num_kv_heads;
   return launch_pdl(combine4_kernel, dim3((unsigned)(items * ((G + kCombineHeads - 1) / kCombineHeads))),

@@ -12,6 +12,9 @@ struct Piece4 {
   int32_t start, end;
   int32_t slot;         // partial's slot, or -1: the piece is the whole attended range
 };
+__device__ __forceinline__ const int32_t* piece_table(const Decode4Params& p, const Piece4& pc) {
+  return p.table + (p.lists ? (int64_t)pc.b * p.num_kv_heads + pc.kvh : (int64_t)pc.b) * p.max_pages;
+}
 constexpr int kPieces = 32;  // pieces listed at a time
 // State of the list, in shared memory.
 struct List4 {
@@ -205,5 +208,10 @@ __device__ __forceinline__ void next_pieces(const Decode4Params& p, int c, List4
 // The kernels' launches (decode4.cu: mma.m16n8k16, decode4_tc.cu: tcgen05).
 int decode4_tc_heads(int group);   // query heads per block of the tcgen05 kernel (0: the group is not its)
 cudaError_t launch_decode4_tc(const Decode4Params& p, cudaStream_t stream);
+cudaError_t launch_attend8(const Decode4Params& p, cudaStream_t stream);  // (attend8.cu: the int8 cache, any group)
+inline int tensor_heads(const Decode4Params& p) {
+  const int G = p.num_heads / p.num_kv_heads;
+  return p.eight && G <= 8 ? 16 : decode4_tc_heads(G);
+}
 
 }  // namespace cai

@@ -53,6 +53,60 @@ cai_status summarize(const Pool* pools, const cai_kv_summary* summaries, int32_t
   return cuda_status(launch_summarize(p, four, static_cast<cudaStream_t>(stream)));
 }
 
+// Attention over lists of pages is a decode step whose tables have a row for every K/V head and hold the listed pages
+// alone; its sequences are the call's rows.
+size_t attend_bytes(int32_t rows, int32_t num_q_heads, int32_t num_kv_heads, int32_t width, int32_t page_size,
+                    int32_t num_splits, bool eight) {
+  if (num_kv_heads < 1 || num_kv_heads > kMaxKvHeads || num_q_heads < 1 || num_q_heads % num_kv_heads != 0 ||
+      num_q_heads / num_kv_heads > kMaxGroup || rows <= 0 || rows > 65535 || width <= 0 || !page_size_ok(page_size) ||
+      (int64_t)width * page_size > (1ll << 30) || num_splits < 0 || num_splits > kMaxSplits)
+    return 0;
+  Decode4Params p = {};
+  p.num_heads = num_q_heads;
+  p.num_kv_heads = num_kv_heads;
+  p.batch = rows;
+  p.page_size = page_size;
+  p.max_pages = width;
+  p.eight = eight;
+  return plan_decode4(p, num_splits);
+}
+
+template <class Pool>
+cai_status attend_pages(const Pool* kv_pools, int32_t num_kv_heads, const uint16_t* q, int32_t rows,
+                        int32_t num_q_heads, const int32_t* pages, int32_t width, const int32_t* len,
+                        float softmax_scale, int32_t num_splits, void* workspace, size_t workspace_bytes,
+                        uint16_t* out, float* lse_out, int32_t* err_flag, bool eight, void* stream) {
+  const cai_status st = check_pools(kv_pools, num_kv_heads);
+  if (st != CAI_OK) return st;
+  if (rows < 0 || width <= 0 || num_splits < 0 || num_splits > kMaxSplits || !std::isfinite(softmax_scale))
+    return CAI_ERR_INVALID_ARG;
+  if (num_q_heads < 1 || num_q_heads % num_kv_heads != 0 || num_q_heads / num_kv_heads > kMaxGroup)
+    return CAI_ERR_UNSUPPORTED;
+  if ((int64_t)width * kv_pools[0].page_size > (1ll << 30) || rows > 65535) return CAI_ERR_UNSUPPORTED;
+  if (rows == 0) return CAI_OK;
+  if (!q || !pages || !len || !out || !aligned16(q) || !aligned16(out)) return CAI_ERR_INVALID_ARG;
+  Decode4Params p = {};
+  fill_pools(kv_pools, num_kv_heads, p);
+  p.num_heads = num_q_heads;
+  p.batch = rows;
+  p.max_pages = width;
+  p.table = pages;
+  p.lists = 1;
+  p.eight = eight;
+  p.ctx_len = len;
+  p.q = q;
+  p.out = out;
+  p.lse_out = lse_out;
+  const size_t need = plan_decode4(p, num_splits);
+  if (need > 0 && (!workspace || workspace_bytes < need || !aligned256(workspace))) return CAI_ERR_WORKSPACE;
+  place_decode4(p, workspace);
+  p.scale_log2 = softmax_scale * kLog2e;
+  p.err = err_flag;
+  p.wait_ns = wait_limit_ns();
+  p.drop_stage = fault_drop_stage();
+  return cuda_status(launch_decode4(p, static_cast<cudaStream_t>(stream)));
+}
+
 }  // namespace
 
 extern "C" {
@@ -128,6 +182,32 @@ cai_status cai_kv_select(const cai_kv_summary* summaries, int32_t num_kv_heads, 
   p.len_out = len_out;
   p.err = err_flag;
   return cuda_status(launch_select(p, static_cast<cudaStream_t>(stream)));
+}
+
+size_t cai_kv_attend_pages_workspace_size(int32_t rows, int32_t num_q_heads, int32_t num_kv_heads, int32_t width,
+                                          int32_t page_size, int32_t num_splits) {
+  return attend_bytes(rows, num_q_heads, num_kv_heads, width, page_size, num_splits, true);
+}
+
+cai_status cai_kv_attend_pages(const cai_kv_pool* kv_pools, int32_t num_kv_heads, const uint16_t* q, int32_t rows,
+                               int32_t num_q_heads, const int32_t* pages, int32_t width, const int32_t* len,
+                               float softmax_scale, int32_t num_splits, void* workspace, size_t workspace_bytes,
+                               uint16_t* out, float* lse_out, int32_t* err_flag, void* stream) {
+  return attend_pages(kv_pools, num_kv_heads, q, rows, num_q_heads, pages, width, len, softmax_scale, num_splits,
+                      workspace, workspace_bytes, out, lse_out, err_flag, true, stream);
+}
+
+size_t cai_kv4_attend_pages_workspace_size(int32_t rows, int32_t num_q_heads, int32_t num_kv_heads, int32_t width,
+                                          int32_t page_size, int32_t num_splits) {
+  return attend_bytes(rows, num_q_heads, num_kv_heads, width, page_size, num_splits, false);
+}
+
+cai_status cai_kv4_attend_pages(const cai_kv4_pool* kv_pools, int32_t num_kv_heads, const uint16_t* q, int32_t rows,
+                               int32_t num_q_heads, const int32_t* pages, int32_t width, const int32_t* len,
+                               float softmax_scale, int32_t num_splits, void* workspace, size_t workspace_bytes,
+                               uint16_t* out, float* lse_out, int32_t* err_flag, void* stream) {
+  return attend_pages(kv_pools, num_kv_heads, q, rows, num_q_heads, pages, width, len, softmax_scale, num_splits,
+                      workspace, workspace_bytes, out, lse_out, err_flag, false, stream);
 }
 
 }  // extern "C"

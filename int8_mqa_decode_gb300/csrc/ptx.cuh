@@ -246,6 +246,15 @@ __device__ __forceinline__ void bulk_g2s_hint(void* dst_smem, const void* src_gm
       : "memory");
 }
 
+// 2-D tensor copy (TMA) of one box at element coordinates (x, y).
+__device__ __forceinline__ void tma_load_2d(void* dst_smem, const void* map, int x, int y, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          smem_addr(dst_smem)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_addr(bar))
+      : "memory");
+}
+
 // 2-D tensor copy (TMA) of one box at element coordinates (x, y), with an L2
 // eviction-priority hint; `map` is a __grid_constant__ CUtensorMap.
 __device__ __forceinline__ void tma_load_2d_hint(void* dst_smem, const void* map, int x, int y, uint64_t* bar,

@@ -5,6 +5,8 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
+#include "common.cuh"
+
 namespace cai {
 
 inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
@@ -18,6 +20,24 @@ inline PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
       fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
   }
   return fn;
+}
+
+// The page pool as a 2-D tensor of 128-byte rows (a page of P tokens is
+// page_bytes(P) / 128 consecutive rows: P K-code rows, P V-code rows, then the
+// scale rows); one box is the 2P code rows of a page, landing 128-byte
+// swizzled in shared memory.
+inline bool encode_pool_map(CUtensorMap* map, const void* pages, int64_t num_pages, int P) {
+  auto fn = tensor_map_encoder();
+  if (!fn) return false;
+  const int64_t rows = num_pages * (page_bytes(P) / 128);
+  if (rows <= 0 || rows > 2147483647ll) return false;
+  cuuint64_t dims[2] = {128, (cuuint64_t)rows};
+  cuuint64_t strides[1] = {128};
+  cuuint32_t box[2] = {128, (cuuint32_t)(2 * P)};
+  cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(pages), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace cai

@@ -274,3 +274,331 @@ def test_select_leaves_its_neighbours_alone():
     cai.cai_kv_select(sums, q, dev(table), dev(np.array([479], np.int32)), 1, 1, ws, room[1].view(1, 1, 1, 7), length, err)
     assert err.item() == 0 and (room[0] == -7).all() and (room[2] == -7).all() and (room[1] >= 0).all()
     assert room[1, 0] == table[0, 0] and room[1, 6] == table[0, 29] and length.item() == 7 * 16
+
+
+# ------------------------------------------------------------------------ attention over lists
+
+"""Bounds of the attention.  q, K and V enter the products exactly; a weight is 2^z rounded to fp16, 2^-11 of it, with z off
+by the fp32 sums' rounding, 2^-12 of the weight at most for the logits here (checked by the bound on lse); weights among
+fp16's subnormals are off by 2^-32 of the largest that enters a product, so by 2^-32 max|v| of the output each; the output is
+rounded to bf16 once: |out - ref| <= 2^-8 |ref| + (1 + 2^-8) ((2^-11 + 2^-12) sum p|v| + n 2^-32 max|v|).
+lse: 2^-20 of scale * sum |q k|, of 1 + |lse| and, where V's scale goes through the exponent, of its logarithm."""
+
+
+def attend(d, q, lists, lens, scale=SCALE, splits=0, bits=0, poison=0xFF):
+    size = cai.cai_kv4_attend_pages_workspace_size if d.four else cai.cai_kv_attend_pages_workspace_size
+    n = size(q.shape[0], q.shape[1], d.hkv, lists.shape[2], d.page, splits)
+    ws = torch.full((n,), poison, dtype=torch.uint8, device=DEV) if n else None
+    out = torch.full(q.shape, float("nan"), dtype=torch.bfloat16, device=DEV)
+    lse, err = torch.full(q.shape[:2], float("nan"), device=DEV), flag()
+    f = cai.cai_kv4_attend_pages if d.four else cai.cai_kv_attend_pages
+    f(d.pools, q, dev(np.ascontiguousarray(lists, np.int32)), dev(np.array(lens, np.int32)), scale, splits, ws, out, lse, err)
+    torch.cuda.synchronize()
+    assert err.item() == bits
+    return host(out), host(lse)
+
+
+def page_values(d):
+    """K and V float64 [hkv][pages][P][128] by page id (NaN where nothing is), and V's scales' logarithms' largest magnitude."""
+    k = np.full((d.hkv, d.num_pages, d.page, 128), np.nan)
+    v = np.full_like(k, np.nan)
+    for j in range(d.hkv):
+        for b, n in enumerate(d.lengths):
+            for i in range(-(-n // d.page)):
+                x = slice(i * d.page, min(n, (i + 1) * d.page))
+                k[j, d.table_np[b, i], :x.stop - x.start] = d.k[j][b][x]
+                v[j, d.table_np[b, i], :x.stop - x.start] = d.v[j][b][x]
+    return k, v
+
+
+def check_attend(d, q, lists, lens, out, lse, scale=SCALE, skip=()):
+    k, v = page_values(d)
+    g = q.shape[1] // d.hkv
+    qh = host(q).astype(np.float64)
+    for r, n in enumerate(lens):
+        if r in skip:
+            continue
+        for j in range(d.hkv):
+            ids = lists[r, j, :-(-n // d.page)]
+            kk, vv = (x[j, ids].reshape(-1, 128)[:n] for x in (k, v))
+            hs = slice(j * g, (j + 1) * g)
+            ref, rl, a, big = kv4.attend_rows(qh[r:r + 1, hs], kk, vv, scale, np.ones((1, n), bool))
+            got, gl = out[r:r + 1, hs].astype(np.float64), lse[r:r + 1, hs].astype(np.float64)
+            if n == 0:
+                assert (got == 0).all() and (gl == -np.inf).all(), (r, j)
+                continue
+            assert np.isfinite(got).all() and np.isfinite(gl).all(), (r, j)
+            top = np.abs(vv).max(initial=0)
+            bound = 2.0 ** -8 * np.abs(ref) + (1 + 2.0 ** -8) * ((2.0 ** -11 + 2.0 ** -12) * a + n * 2.0 ** -32 * top) + 2.0 ** -133
+            err = np.abs(got - ref)
+            assert (err <= bound).all(), (r, j, (err - bound).max(), err.max())
+            vs = np.abs(vv).max(-1) / 127  # (of int8 tokens; 2^-100 at least)
+            lv = 0.0 if d.four else np.abs(np.log2(np.maximum(vs, 2.0 ** -100))).max()
+            assert (np.abs(gl - rl) <= 2.0 ** -20 * (big + 1 + np.abs(rl) + lv)).all(), (r, j, np.abs(gl - rl).max())
+
+
+def random_lists(rng, d, rows, width, lens):
+    """For every row and K/V head pages of one sequence in any order, whole ones but the last."""
+    lists = np.full((rows, d.hkv, width), -1, np.int64)
+    for r, n in enumerate(lens):
+        for j in range(d.hkv):
+            whole = np.concatenate([d.table_np[b, :m // d.page] for b, m in enumerate(d.lengths)])
+            lists[r, j, :-(-n // d.page)] = rng.choice(whole, -(-n // d.page))  # (a page may stand there twice)
+    return lists
+
+
+ATTEND = [  # hkv, heads of a group, page, splits
+    (1, 1, 16, 0), (2, 3, 32, 0), (8, 4, 64, 0), (1, 8, 16, 3), (2, 9, 32, 0), (1, 16, 64, 1), (2, 17, 16, 0), (1, 32, 32, 0),
+    (1, 33, 16, 0), (2, 40, 64, 2), (1, 64, 32, 0), (1, 65, 16, 0), (1, 128, 64, 0),
+]
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("hkv,g,page,splits", ATTEND)
+def test_attend_lists(four, hkv, g, page, splits):
+    rng = np.random.default_rng(g)
+    d = Dialogues(four, [700, 64, 333], hkv, page, seed=g)
+    lens = [0, 1, page, page + 1, 127, 128, 129, 640, 255, 0, 5 * page + 3]
+    width = 640 // page + 1
+    lists = random_lists(rng, d, len(lens), width, lens)
+    q = dev(rng.normal(size=(len(lens), hkv * g, 128)).astype(np.float32) * 1.5, torch.bfloat16)
+    out, lse = attend(d, q, lists, lens, splits=splits)
+    check_attend(d, q, lists, lens, out, lse)
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("g", [4, 32, 64])
+def test_attend_many_rows(four, g):
+    """More rows than blocks, and few long ones that are cut; the same again to the bit."""
+    rng = np.random.default_rng(g)
+    d = Dialogues(four, [900, 2000], 1, 16, seed=g + 1)
+    for rows, width in ((400, 12), (3, 125)):
+        lens = rng.integers(0, width * 16 + 1, rows)
+        lens[0] = width * 16
+        lists = random_lists(rng, d, rows, width, lens)
+        q = dev(rng.normal(size=(rows, g, 128)).astype(np.float32), torch.bfloat16)
+        out, lse = attend(d, q, lists, lens)
+        check_attend(d, q, lists, lens, out, lse)
+        again = attend(d, q, lists, lens, poison=0)
+        assert np.array_equal(out, again[0]) and np.array_equal(lse, again[1])
+
+
+def test_attend_whole_contexts_is_the_decode():
+    """Lists of all pages of a 4-bit context give the decode's bits."""
+    rng = np.random.default_rng(1)
+    for g in (4, 24):
+        d = Dialogues(True, [500, 1, 129], 1, 16, seed=g)
+        q = dev(rng.normal(size=(3, g, 128)).astype(np.float32), torch.bfloat16)
+        out, lse = attend(d, q, d.table_np[:, None], d.lengths)
+        n = cai.cai_kv4_decode_workspace_size(3, g, 1, d.table.shape[1], 16, 0, 0)
+        ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+        o2, l2 = torch.empty_like(q), torch.empty(3, g, device=DEV)
+        cai.cai_kv4_decode(d.pools, q, d.table, dev(np.array(d.lengths, np.int32)), 0, SCALE, 0, ws, o2, l2)
+        assert np.array_equal(out, host(o2)) and np.array_equal(lse, host(l2))
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("size", [2.0 ** -60, 2.0 ** -24, 2.0 ** -10, 2.0 ** 12])
+def test_attend_values_of_any_size(four, size):
+    """Small and large values keep their precision (the 4-bit scales are fp16: 2^-14 and up), zero vectors among them."""
+    if four and size < 2.0 ** -11:
+        pytest.skip("fp16 scales")
+    rng = np.random.default_rng(2)
+    d = Dialogues(four, [400], 1, 16, seed=3)
+    x = rng.normal(size=(2, 1, 400, 1, 128)).astype(np.float32)
+    x[1] *= size
+    x[1, 0, ::7] = 0
+    append = cai.cai_kv4_append if four else cai.cai_kv_append_rope
+    append(d.pools, dev(x[0]), dev(x[1]), d.table, torch.zeros(1, dtype=torch.int32, device=DEV))
+    d.k, d.v = [[d.stored(x[0, 0, :, 0])]], [[d.stored(x[1, 0, :, 0])]]
+    for g in (4, 32):
+        q = dev(rng.normal(size=(1, g, 128)).astype(np.float32), torch.bfloat16)
+        out, lse = attend(d, q, d.table_np[:, None], [400])
+        check_attend(d, q, d.table_np[:, None], [400], out, lse)
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("first", [True, False])
+def test_attend_one_heavy_key(four, first):
+    """One key far above a flat rest whose weights are small but many, at the list's start or its end."""
+    rng = np.random.default_rng(4)
+    n = 2048
+    d = Dialogues(four, [n], 1, 32, seed=5)
+    x = np.zeros((2, 1, n, 1, 128), np.float32)
+    x[0, 0, 0 if first else n - 1] = 1.0
+    x[1] = rng.normal(size=(1, n, 1, 128)) + 3
+    append = cai.cai_kv4_append if four else cai.cai_kv_append_rope
+    append(d.pools, dev(x[0]), dev(x[1]), d.table, torch.zeros(1, dtype=torch.int32, device=DEV))
+    d.k, d.v = [[d.stored(x[0, 0, :, 0])]], [[d.stored(x[1, 0, :, 0])]]
+    for g in (2, 20, 64):
+        q = torch.full((1, g, 128), 1.0, dtype=torch.bfloat16, device=DEV)
+        for scale in (5.0 / 128, 12.0 / 128, -12.0 / 128, 0.0):
+            out, lse = attend(d, q, d.table_np[:, None], [n], scale=scale)
+            check_attend(d, q, d.table_np[:, None], [n], out, lse, scale=scale)
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("g", [4, 32])
+def test_attend_bad_arguments_on_the_device(four, g):
+    """Bad lengths give zeros, bad page ids are flagged and left out; other rows do not notice."""
+    rng = np.random.default_rng(6)
+    d = Dialogues(four, [300], 1, 16, seed=7)
+    lists = np.repeat(d.table_np[:, None, :10], 4, 0).astype(np.int64)
+    q = dev(rng.normal(size=(4, g, 128)).astype(np.float32), torch.bfloat16)
+    out, lse = attend(d, q, lists, [160, 161, -1, 31], bits=cai.CAI_DEVERR_LENGTH)
+    for r in (1, 2):
+        assert (out[r] == 0).all() and (lse[r] == -np.inf).all()
+    check_attend(d, q, lists, [160, 0, 0, 31], out, lse, skip=(1, 2))
+    for bad in (-1, d.num_pages, 2147483647, -2147483648):
+        broken = lists.copy()
+        broken[1, 0, 3] = bad
+        out, lse = attend(d, q, broken, [160, 160, 16, 31], bits=cai.CAI_DEVERR_PAGE)
+        without = lists.copy()
+        without[1, 0, 3:9] = lists[1, 0, 4:10]
+        check_attend(d, q, without, [160, 144, 16, 31], out, lse)
+    broken = lists.copy()
+    broken[1, 0, 3:] = 1 << 29  # behind the length: not read
+    out, lse = attend(d, q, broken, [160, 48, 16, 31])
+    check_attend(d, q, broken, [160, 48, 16, 31], out, lse)
+
+
+@pytest.mark.parametrize("g", [4, 32, 64])
+@pytest.mark.parametrize("stage", [0, 1, 4])
+def test_attend_timeout_is_reported(g, stage):
+    """A copy that never comes: the wait ends, the flag says so, and the next call is right."""
+    rng = np.random.default_rng(8)
+    d = Dialogues(False, [900], 1, 16, seed=9)
+    q = dev(rng.normal(size=(2, g, 128)).astype(np.float32), torch.bfloat16)
+    lists, lens = np.repeat(d.table_np[:, None, :56], 2, 0), [896, 896]
+    cai.cai_set_wait_limit_ns(20_000_000)
+    cai.cai_set_fault_injection(stage)
+    try:
+        attend(d, q, lists, lens, splits=1, bits=cai.CAI_DEVERR_TIMEOUT)
+    finally:
+        cai.cai_set_fault_injection(-1)
+        cai.cai_set_wait_limit_ns(0)
+    out, lse = attend(d, q, lists, lens, splits=1)
+    check_attend(d, q, lists, lens, out, lse)
+
+
+# ------------------------------------------------------------------------------- a run together
+
+def sparse_step(d, sums, rope, qkv, hq, start, new, keep, first, last, ws, outs):
+    """append (axes) -> summarize -> select -> attend, packed rows."""
+    hkv, n = d.hkv, qkv.shape[0]
+    off, pos = ws["offsets"], ws["positions"]
+    append = cai.cai_kv4_append_axes if d.four else cai.cai_kv_append_rope_axes
+    append(d.pools, qkv[:, hq:hq + hkv], qkv[:, hq + hkv:], d.table, start, rope, pos, q=qkv[:, :hq], q_out=outs["q"],
+           q_offsets=off, max_new=new, err_flag=ws["err"])
+    (cai.cai_kv4_summarize if d.four else cai.cai_kv_summarize)(d.pools, sums, d.table, start, new, q_offsets=off, err_flag=ws["err"])
+    cai.cai_kv_select(sums, outs["q"], d.table, start, first, last, ws["select"], outs["pages"], outs["len"], ws["err"], off, new)
+    (cai.cai_kv4_attend_pages if d.four else cai.cai_kv_attend_pages)(
+        d.pools, outs["q"], outs["pages"], outs["len"], SCALE, 0, ws["attend"], outs["out"], outs["lse"], ws["err"])
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("hkv,g,page", [(1, 32, 16), (2, 4, 32)])
+def test_sparse_steps(four, hkv, g, page):
+    """A chunk, then decode steps in a padded batch, eagerly and from a captured graph: every stage against the oracle."""
+    rng = np.random.default_rng(11)
+    before, new, hq, keep, first, last = np.array([900, 0, 33, 1500]), np.array([40, 3, 0, 1]), hkv * g, 8, 1, 2
+    d = Dialogues(four, before, hkv, page, seed=12, width=-(-1600 // page))
+    # Room for the tokens to come: pages behind the pool that the dialogues use.
+    bytes_ = kv4.page_bytes4(page) if four else oracle.page_bytes(page)
+    cls = cai.KV4Pool if four else cai.KVPool
+    used = d.num_pages
+    d.pools = [cls(used + 64, page, pages=torch.cat((p.pages, torch.full((64 * bytes_,), 0xFF, dtype=torch.uint8, device=DEV)))) for p in d.pools]
+    d.num_pages = used + 64
+    at = 0
+    for b in range(4):
+        have = -(-int(before[b]) // page)
+        for i in range(have, -(-(int(before[b]) + 50) // page)):
+            d.table_np[b, i] = used + at
+            at += 1
+    d.table = dev(d.table_np)
+    sums = d.summaries(fill=0xEE)
+    d.summarize(sums, [0] * 4, int(before.max()), np.concatenate([[0], np.cumsum(before)]))
+    half = 64
+    ang = np.arange(2000)[:, None] * (1e4 ** (-np.arange(half) / half))
+    cos, sin = np.cos(ang).astype(np.float32), np.sin(ang).astype(np.float32)
+    axis = [i * 3 // half for i in range(half)]
+    rope = cai.RopeAxes(dev(cos), dev(sin), axis)
+    k, v = [[list(x) for x in d.k[j]] for j in range(hkv)], [[list(x) for x in d.v[j]] for j in range(hkv)]
+
+    def buffers(rows):
+        return (dict(offsets=torch.zeros(5, dtype=torch.int32, device=DEV), positions=torch.zeros(rows, 3, dtype=torch.int32, device=DEV),
+                     err=flag(), select=torch.empty(cai.cai_kv_select_workspace_size(4, rows, hq, hkv, d.table.shape[1]), dtype=torch.uint8, device=DEV),
+                     attend=torch.empty((cai.cai_kv4_attend_pages_workspace_size if four else cai.cai_kv_attend_pages_workspace_size)(
+                         rows, hq, hkv, keep, page), dtype=torch.uint8, device=DEV)),
+                dict(q=torch.zeros(rows, hq, 128, dtype=torch.bfloat16, device=DEV), pages=torch.full((rows, hkv, keep), -9, dtype=torch.int32, device=DEV),
+                     len=torch.full((rows,), -9, dtype=torch.int32, device=DEV), out=torch.full((rows, hq, 128), float("nan"), dtype=torch.bfloat16, device=DEV),
+                     lse=torch.full((rows, hq), float("nan"), device=DEV)))
+
+    def check(start, new, qkv, pos, outs, total):
+        pos_np, q_in = pos, host(qkv)
+        turned = pages.rotate_axes(q_in[:, :hq + hkv], pos_np, axis, cos, sin, False)
+        off = np.concatenate([[0], np.cumsum(new)])
+        for j in range(hkv):
+            for b in range(4):
+                r = slice(off[b], off[b + 1])
+                k[j][b] += list(d.stored(turned[r, hq + j]))
+                v[j][b] += list(d.stored(q_in[r, hq + hkv + j]))
+        d.lengths = [int(s + n) for s, n in zip(start, new)]
+        d.k, d.v = ([[np.array(x, np.float32).reshape(-1, 128) for x in y] for y in z] for z in (k, v))
+        q = kv4.bf16_round(turned[:, :hq])
+        n = off[-1]
+        assert np.array_equal(host(outs["q"])[:n], q[:n])
+        lists, length = outs["pages"].cpu().numpy(), outs["len"].cpu().numpy()
+        for j in range(hkv):
+            for b in range(4):
+                codes, scale = zip(*(pages.summarize(d.k[j][b][i:i + page]) for i in range(0, max(1, d.lengths[b]), page))) if d.lengths[b] else ((), ())
+                for i in range(new[b]):
+                    blocks, tokens = pages.select(q[off[b] + i, j * g:(j + 1) * g], np.array(codes), np.array(scale), int(start[b] + i), page, keep, first, last)
+                    want = np.full(keep, -1)
+                    want[:len(blocks)] = d.table_np[b, blocks]
+                    assert np.array_equal(lists[off[b] + i, j], want) and length[off[b] + i] == tokens
+        assert (lists[n:] == -1).all() and (length[n:] == 0).all()
+        check_attend(d, outs["q"], lists, length, host(outs["out"]), host(outs["lse"]))
+        assert (outs["out"][n:total] == 0).all()
+
+    # The chunk.
+    rows = int(new.sum())
+    ws, outs = buffers(rows)
+    ws["offsets"].copy_(dev(np.concatenate([[0], np.cumsum(new)]).astype(np.int32)))
+    pos = rng.integers(0, 2000, (rows, 3)).astype(np.int32)
+    ws["positions"].copy_(dev(pos))
+    qkv = dev(rng.normal(size=(rows, hq + 2 * hkv, 128)).astype(np.float32) * 1.5, torch.bfloat16)
+    sparse_step(d, sums, rope, qkv, hq, dev(before.astype(np.int32)), 40, keep, first, last, ws, outs)
+    torch.cuda.synchronize()
+    assert ws["err"].item() == 0
+    check(before, new, qkv, pos, outs, rows)
+
+    # Decode steps of three of the four sequences, a batch padded to six rows, from one graph on another stream.
+    ws, outs = buffers(6)
+    start = dev((before + new).astype(np.int32))
+    qkv = torch.zeros(6, hq + 2 * hkv, 128, dtype=torch.bfloat16, device=DEV)
+    one = np.array([1, 1, 0, 1])
+    ws["offsets"].copy_(dev(np.concatenate([[0], np.cumsum(one)]).astype(np.int32)))
+    stream, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    keep_pages = [p.pages.clone() for p in d.pools]
+    keep_sums = [s.data.clone() for s in sums]
+    with torch.cuda.stream(stream):
+        sparse_step(d, sums, rope, qkv, hq, start, 1, keep, first, last, ws, outs)  # (a warm-up; undone below)
+        with torch.cuda.graph(graph, stream=stream):
+            sparse_step(d, sums, rope, qkv, hq, start, 1, keep, first, last, ws, outs)
+    torch.cuda.synchronize()
+    for a, b in zip([p.pages for p in d.pools] + [s.data for s in sums], keep_pages + keep_sums):
+        a.copy_(b)
+    now = before + new
+    for step in range(3):
+        pos = rng.integers(0, 2000, (6, 3)).astype(np.int32)
+        ws["positions"].copy_(dev(pos))
+        qkv.copy_(dev(rng.normal(size=tuple(qkv.shape)).astype(np.float32) * 1.5, torch.bfloat16))
+        start.copy_(dev(now.astype(np.int32)))
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert ws["err"].item() == 0
+        check(now, one, qkv, pos, outs, 6)
+        now = now + one

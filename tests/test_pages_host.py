@@ -140,3 +140,27 @@ def test_select_refusals(lib):
     assert call(batch=-1) == 1 and call(n=-1) == 1 and call(off=FAKE, total=-1) == 1 and call(maxp=0) == 1 and call(batch=65536) == 2
     for bad in ((0, 2, 8, 2, 64), (2, -1, 8, 2, 64), (2, 2, 7, 2, 64), (2, 2, 8, 9, 64), (2, 2, 8, 2, 0), (65536, 2, 8, 2, 64)):
         assert cai.cai_kv_select_workspace_size(*bad) == 0
+
+
+@pytest.mark.parametrize("four", [False, True])
+def test_attend_refusals(lib, four):
+    entry = lib.cai_kv4_attend_pages if four else lib.cai_kv_attend_pages
+    size = cai.cai_kv4_attend_pages_workspace_size if four else cai.cai_kv_attend_pages_workspace_size
+    kind = cai.cai_kv4_pool if four else cai.cai_kv_pool
+    need = size(3, 64, 2, 100, 16, 4)
+
+    def call(pools=_arr(kind), hkv=2, q=FAKE, rows=3, hq=64, pages=FAKE, width=100, length=FAKE, scale=0.1, splits=4, ws=FAKE,
+             ws_bytes=need, out=FAKE):
+        return entry(pools, hkv, q, rows, hq, pages, width, length, scale, splits, ws, ws_bytes, out, None, None, None)
+
+    assert need > 0 and call(rows=0) == 0
+    assert call(pools=None) == 1 and call(hkv=0) == 2 and call(hkv=9) == 2 and call(pools=_arr(kind, page_size=24)) == 2
+    assert call(hq=0) == 2 and call(hq=63) == 2 and call(hq=2 * 129) == 2
+    assert call(q=None) == 1 and call(q=FAKE + 8) == 1 and call(pages=None) == 1 and call(length=None) == 1
+    assert call(out=None) == 1 and call(out=FAKE + 8) == 1
+    assert call(rows=-1) == 1 and call(rows=65536) == 2 and call(width=0) == 1 and call(width=(1 << 26) + 1) == 2
+    assert call(scale=float("inf")) == 1 and call(splits=-1) == 1 and call(splits=65) == 1
+    assert call(ws=None) == 3 and call(ws_bytes=need - 1) == 3 and call(ws=FAKE + 128) == 3
+    for bad in ((0, 64, 2, 100, 16, 0), (3, 63, 2, 100, 16, 0), (3, 64, 9, 100, 16, 0), (3, 64, 2, 0, 16, 0), (3, 64, 2, 100, 24, 0),
+                (3, 64, 2, 100, 16, 65), (65536, 64, 2, 100, 16, 0), (3, 258, 2, 100, 16, 0)):
+        assert size(*bad) == 0
