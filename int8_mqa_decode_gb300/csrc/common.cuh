@@ -211,6 +211,7 @@ struct SelectParams {
   int32_t* pages_out;           // [rows][Hkv][keep]
   int32_t* len_out;             // [rows]
   int32_t* err;
+  uint64_t wait_ns;
 };
 
 struct PrefillLaunch {

@@ -7,8 +7,12 @@
 // the selection.  The first and last pages of a row's context are always taken, the others by score, ties by the lower page.
 //
 // As a product: with q+ = max(q, 0), q- = min(q, 0), D = q+ . hi + q- . lo, so pages are the rows (256 codes) and heads
-// the columns of one matrix product.  mma.m16n8k16 in fp16: codes are exact in it, and become its A operand in
-// registers (16 bytes of a row a lane, in the order of memory, with the same order of channels in B).
+// the columns of one matrix product: tcgen05.mma kind::f16 (codes are exact in fp16), 128 pages by up to 128 columns (query
+// rows x heads of a sequence), K = 256.  A block keeps its columns in shared memory and goes through tiles of pages:
+// its eight warps turn the codes, 16 bytes of a row a lane, into the A operand in tensor memory as they come (the order of
+// the columns' channels follows), one lane issues the products, and while they run the next tile's codes are on their
+// way; then a thread has a page and all columns, and takes the largest of each query row.  Two blocks share an SM, one
+// converting while the other's products run.
 #include <algorithm>
 
 #include "ptx.cuh"
@@ -18,20 +22,14 @@ namespace cai {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kCols = 128;                       // columns (query rows x heads) of a block at most
-constexpr int kColBytes = 2 * 2 * kHeadDim + 16; // q+ and q- of a column in fp16, and a shift of banks
-constexpr int kChunk = 256;                      // pages of a block
+constexpr int kThreads = 32 * kWarps;
+constexpr int kCols = 128;                        // columns (query rows x heads) of a block at most
+constexpr int kTilePages = 128;
+constexpr int kColBytes = 2 * 2 * kHeadDim;       // q+ and q- of a column in fp16
+constexpr uint32_t kTmem = 256, kColD = 128;      // tensor memory: A (128 columns), D
 
 // Columns that a row's group of G heads takes: a power of two up to 8, then a multiple of 8.
 __host__ __device__ inline int padded_heads(int G) { return G <= 1 ? 1 : G <= 2 ? 2 : G <= 4 ? 4 : (G + 7) / 8 * 8; }
-
-__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                          uint32_t b1) {
-  asm(
-      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 
 // Tile `tile` of the call: rows [row0, row0 + n) of sequence b, at positions pos0 .. (n = 0: none).
 struct RowTile {
@@ -51,7 +49,7 @@ __device__ __forceinline__ RowTile find_tile(const SelectParams& p, int64_t tile
   }
   // Tiles of the sequences before: every thread sums a run of them.
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int run = (p.batch + kWarps * 32 - 1) / (kWarps * 32);
+  const int run = (p.batch + kThreads - 1) / (kThreads);
   const int b0 = min(p.batch, tid * run), b1 = min(p.batch, b0 + run);
   int64_t sum = 0;
   for (int b = b0; b < b1; ++b) sum += (max(new_rows(p, b).n, 0) + per - 1) / per;
@@ -88,129 +86,214 @@ __device__ __forceinline__ RowTile find_tile(const SelectParams& p, int64_t tile
   return *found;
 }
 
-// Scores of a tile's rows over a chunk of their pages.  Block: (tile, K/V head, chunk), the chunk fastest.
-__global__ void __launch_bounds__(kWarps * 32) score_kernel(const __grid_constant__ SelectParams p, int per, int chunks) {
-  extern __shared__ __align__(16) uint8_t cols[];  // [columns][kColBytes]
-  __shared__ float scale_of[kCols];
+// The largest of t_c D_c over columns c0 .. c0 + gp - 1 (8 N of them) of this thread's page.
+template <int N>
+__device__ __forceinline__ float largest(uint32_t tmem, const float* scale_of, int gp) {
+  float m = -INFINITY;
+  for (int c = 0; c < gp; c += N) {
+    uint32_t r[N];
+    if constexpr (N == 32) tmem_ld_32x32b_x32(tmem + c, r);
+    else if constexpr (N == 16) tmem_ld_32x32b_x16(tmem + c, r);
+    else tmem_ld_32x32b_x8(tmem + c, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int e = 0; e < N; e += 4) {
+      const float4 t = *reinterpret_cast<const float4*>(scale_of + c + e);
+      float z[4];
+      f2_split(f2_mul(f2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), f2(t.x, t.y)), z[0], z[1]);
+      f2_split(f2_mul(f2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), f2(t.z, t.w)), z[2], z[3]);
+      m = fmax3(fmax3(m, z[0], z[1]), z[2], z[3]);
+    }
+  }
+  return m;
+}
+
+// rint(x / t), the division IEEE: by the inverse, and by the division itself where that may round the other way.
+__device__ __forceinline__ float whole(float x, float t, float inv) {
+  const float y = x * inv;
+  float c = rintf(y);
+  if (!(fabsf(y - c) < 0.499f)) c = rintf(__fdiv_rn(x, t));
+  return fminf(fmaxf(c, -127.0f), 127.0f);
+}
+
+// Scores of a tile of rows over `span` tiles of their pages.  Block: (row tile, K/V head, span), the span fastest.
+__global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constant__ SelectParams p, int per, int spans, int span) {
+  extern __shared__ __align__(128) uint8_t cols[];  // column n, channels of unit u (8 of K's 256): (n / 8) 4096 + 128 u + 16 (n % 8)
+  __shared__ __align__(16) float scale_of[kCols];
   __shared__ __align__(16) int shared[2 * kWarps + (sizeof(RowTile) + 3) / 4];
+  __shared__ uint64_t done;  // a tile's products
+  __shared__ WaitState wait;
+  __shared__ uint32_t slot;
+  volatile WaitState* wctl = &wait;
   grid_dependency_wait();
   grid_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t item = over(blockIdx.x, chunks);
-  const int chunk = (int)(blockIdx.x - item * chunks);
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const int64_t item = over(blockIdx.x, spans);
   const int64_t tile = over(item, p.num_kv_heads);
   const int h = (int)(item - tile * p.num_kv_heads);
   const RowTile rt = find_tile(p, tile, per, shared);
   if (rt.n == 0) return;
   const int lg = page_log2(p.page_size);
-  const int64_t end = min(rt.pos0 + rt.n, (int64_t)p.max_pages << lg);  // positions past the table are refused by the selection
-  if (end <= 0) return;
-  const int blocks = (int)((end - 1) >> lg) + 1;  // of the last row
-  const int c0 = chunk * kChunk, c1 = min(c0 + kChunk, blocks - p.last);
+  const int64_t last_pos = min(rt.pos0 + rt.n, (int64_t)p.max_pages << lg);  // (positions past the table are refused by the selection)
+  if (last_pos <= 0) return;
+  const int blocks = (int)((last_pos - 1) >> lg) + 1;  // of the last row
+  const int c0 = (int)(blockIdx.x - item * spans) * span * kTilePages, c1 = min(c0 + span * kTilePages, blocks - p.last);
   if (blocks <= p.keep || c0 >= c1) return;
 
-  // Columns: whole numbers of the rows' heads, fp16.  A group that does not fill its columns repeats its last head.
-  const int G = p.num_q_heads / p.num_kv_heads, gp = padded_heads(G);
-  const int used = (rt.n * gp + 7) / 8 * 8;
-  for (int c = warp; c < used; c += kWarps) {
-    const int i = c / gp, head = min(c - i * gp, G - 1);
-    uint2 w = make_uint2(0u, 0u);
-    if (i < rt.n)
-      w = __ldg(reinterpret_cast<const uint2*>(p.q + ((rt.row0 + i) * p.num_q_heads + h * G + head) * kHeadDim) + lane);
-    const float x[4] = {__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                        __uint_as_float(w.y & 0xFFFF0000u)};
-    float amax = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const float t = __fdiv_rn(amax, 127.0f);
-    float code[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) code[e] = t > 0.0f ? fminf(fmaxf(rintf(__fdiv_rn(x[e], t)), -127.0f), 127.0f) : 0.0f;
-    uint2* dst = reinterpret_cast<uint2*>(cols + c * kColBytes) + lane;
-    dst[0] = make_uint2(pack_f16x2(fmaxf(code[0], 0.0f), fmaxf(code[1], 0.0f)), pack_f16x2(fmaxf(code[2], 0.0f), fmaxf(code[3], 0.0f)));
-    dst[32] = make_uint2(pack_f16x2(fminf(code[0], 0.0f), fminf(code[1], 0.0f)), pack_f16x2(fminf(code[2], 0.0f), fminf(code[3], 0.0f)));
-    if (lane == 0) scale_of[c] = t;
+  if (warp == 0) tmem_alloc(&slot, kTmem);
+  if (tid == 0) {
+    mbar_init(&done, 1);
+    wait.abort = 0;
+    wait.limit_ns = p.wait_ns;
+    fence_barrier_init();
   }
-  __syncthreads();
-
-  const int g = lane >> 2, t = lane & 3;
+  const int g = lane >> 2, t4 = lane & 3, quarter = warp & 3, half = warp >> 2;
   const int32_t* table = p.table + (int64_t)rt.b * p.max_pages;
   const uint8_t* data = p.data[h];
   const float* scales = reinterpret_cast<const float*>(data + (int64_t)p.num_pages[h] * (2 * kHeadDim));
-  for (int base = c0 + 16 * warp; base < c1; base += 16 * kWarps) {
-    // Rows of A: pages base + g and base + g + 8.
-    uint32_t a[2][4][8];  // [row][64 codes][fp16 pairs]
-    float s[2];
+  const auto page_of = [&](int blk) -> int32_t {
+    const int32_t page = blk < c1 ? __ldg(table + blk) : 0;
+    return (uint32_t)page < (uint32_t)p.num_pages[h] ? page : -1;
+  };
+  // This lane's 64 codes, 16 of every 64, of pages (quarter, half) 16 + g and + 8 of a tile.
+  uint4 a[2][4];
+  const auto load = [&](int base) {
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int blk = base + g + 8 * r;
-      const int32_t page = blk < c1 ? __ldg(table + blk) : -1;
-      const bool ok = (uint32_t)page < (uint32_t)p.num_pages[h];
-      if (blk < c1 && !ok && t == 0 && p.err) atomicOr(p.err, CAI_DEVERR_PAGE);
-      const uint4* row = reinterpret_cast<const uint4*>(data + (int64_t)(ok ? page : 0) * (2 * kHeadDim)) + t;
-      s[r] = __ldg(scales + (ok ? page : 0));
+      const int32_t page = page_of(base + 32 * quarter + 16 * half + g + 8 * r);
+      const uint4* row = reinterpret_cast<const uint4*>(data + (int64_t)max(page, 0) * (2 * kHeadDim)) + t4;
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint4 w = __ldg(row + 4 * c);
-        const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) i8x4_to_f16x4(ws[e], a[r][c][2 * e], a[r][c][2 * e + 1]);
-      }
-      if (!ok) s[r] = -INFINITY;
+      for (int c = 0; c < 4; ++c) a[r][c] = __ldg(row + 4 * c);
     }
-    float m[2] = {-INFINITY, -INFINITY};
-    const int tiles = used / 8, per_row = gp / 8;  // (per_row 0: several rows a tile)
-    int in_row = 0, row = 0;
-    for (int n = 0; n < tiles; ++n) {
-      float acc[4] = {0.f, 0.f, 0.f, 0.f};
-      const uint8_t* col = cols + (8 * n + g) * kColBytes + 32 * t;
+  };
+  load(c0);
+
+  // Columns: whole numbers of the rows' heads, eight columns a warp, lane (g, t) channels 64 c + 16 t .. + 15 of column g: they
+  // stand at words t of units 8 c + e (q+) and 16 + 8 c + e (q-).  A group that does not fill its columns repeats its
+  // last head, columns past the rows are 0.
+  const int G = p.num_q_heads / p.num_kv_heads, gp = padded_heads(G);
+  const int used = (rt.n * gp + 15) / 16 * 16;
+  for (int n0 = 8 * warp; n0 < used; n0 += 8 * kWarps) {
+    const int n = n0 + g, i = n / gp, head = min(n - i * gp, G - 1);
+    uint4 w[2][2];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint4 b0 = *reinterpret_cast<const uint4*>(col + 128 * c), b1 = *reinterpret_cast<const uint4*>(col + 128 * c + 16);
-        const uint32_t b[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mma_16816(acc, a[0][c][2 * e], a[1][c][2 * e], a[0][c][2 * e + 1], a[1][c][2 * e + 1], b[2 * e], b[2 * e + 1]);
+      for (int k = 0; k < 2; ++k)
+        w[c][k] = i < rt.n ? __ldg(reinterpret_cast<const uint4*>(p.q + ((rt.row0 + i) * p.num_q_heads + h * G + head) * kHeadDim + 64 * c + 16 * t4) + k)
+                           : make_uint4(0u, 0u, 0u, 0u);
+    float amax = 0.0f;
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+      const uint4& v = w[x >> 3][x >> 2 & 1];
+      const uint32_t u = (x & 3) == 0 ? v.x : (x & 3) == 1 ? v.y : (x & 3) == 2 ? v.z : v.w;
+      amax = fmax3(amax, fabsf(__uint_as_float(u << 16)), fabsf(__uint_as_float(u & 0xFFFF0000u)));
+    }
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+    const float t = __fdiv_rn(amax, 127.0f), inv = __frcp_rn(t);
+    uint32_t* dst = reinterpret_cast<uint32_t*>(cols + (n0 >> 3) * (8 * kColBytes) + g * 16 + t4 * 4);
+#pragma unroll
+    for (int x = 0; x < 16; ++x) {
+      const uint4& v = w[x >> 3][x >> 2 & 1];
+      const uint32_t u = (x & 3) == 0 ? v.x : (x & 3) == 1 ? v.y : (x & 3) == 2 ? v.z : v.w;
+      const float q0 = t > 0.0f ? whole(__uint_as_float(u << 16), t, inv) : 0.0f;
+      const float q1 = t > 0.0f ? whole(__uint_as_float(u & 0xFFFF0000u), t, inv) : 0.0f;
+      dst[x * 32] = pack_f16x2(fmaxf(q0, 0.0f), fmaxf(q1, 0.0f));
+      dst[(16 + x) * 32] = pack_f16x2(fminf(q0, 0.0f), fminf(q1, 0.0f));
+    }
+    if (t4 == 0) scale_of[n] = t;
+  }
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, slot, 0);
+  const uint32_t mine = tmem + ((uint32_t)(32 * quarter) << 16);
+  const uint64_t dq = smem_desc(smem_addr(cols), 128, 8 * kColBytes);
+  const uint32_t idesc = idesc_f16_f32(kTilePages, used, 0, 0);
+
+  bool ok = true;
+  int phase = 0;
+  for (int base = c0; base < c1; base += kTilePages, phase ^= 1) {
+    // ---- A: column 32 c + 4 e + t holds channels 64 c + 16 t + 2 e, + 1 of the 256 codes.
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t r[16];
+      const uint32_t x[4] = {a[0][c].x, a[0][c].y, a[0][c].z, a[0][c].w}, y[4] = {a[1][c].x, a[1][c].y, a[1][c].z, a[1][c].w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        i8x4_to_f16x4(x[e], r[4 * e], r[4 * e + 2]);
+        i8x4_to_f16x4(y[e], r[4 * e + 1], r[4 * e + 3]);
       }
-      const float t0 = scale_of[8 * n + 2 * t], t1 = scale_of[8 * n + 2 * t + 1];
-      const float z[4] = {__fmul_rn(acc[0], t0), __fmul_rn(acc[1], t1), __fmul_rn(acc[2], t0), __fmul_rn(acc[3], t1)};
-      // The score of page `blk` for row i of the tile.
-      const auto put = [&](int i, int r, float best) {
-        const int blk = base + g + 8 * r;
-        if (i < rt.n && blk < c1)
-          p.scores[((rt.row0 + i) * p.num_kv_heads + h) * p.stride + blk] =
-              s[r] == -INFINITY ? -INFINITY : __fadd_rn(__fmul_rn(best, s[r]), 0.0f);  // (-0 becomes 0)
-      };
-      if (per_row > 0) {
-        m[0] = fmaxf(m[0], fmaxf(z[0], z[1]));
-        m[1] = fmaxf(m[1], fmaxf(z[2], z[3]));
-        if (++in_row == per_row) {
+      tmem_st_16x128b_x8(mine + ((uint32_t)(16 * half) << 16) + 32 * c, r);
+    }
+    tmem_wait_st();
+    tc_fence_before();
+    __syncthreads();  // A is there, and D was read
+    if (warp == 0) {
+      tc_fence_after();
+      if (elect_one()) {
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            m[r] = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], 1));
-            m[r] = fmaxf(m[r], __shfl_xor_sync(0xffffffffu, m[r], 2));
+        for (int k = 0; k < 16; ++k) mma_f16_ts(tmem + kColD, tmem + 8 * k, dq + (uint64_t)(k * 16), idesc, k > 0 ? 1u : 0u);
+        mma_commit(&done);
+      }
+      __syncwarp();
+    }
+    const int blk = base + 32 * quarter + lane;  // this thread's page of D
+    const int32_t page = page_of(blk);
+    const float s = page >= 0 ? __ldg(scales + page) : 0.0f;
+    if (page < 0 && half == 0 && p.err) atomicOr(p.err, CAI_DEVERR_PAGE);
+    if (base + kTilePages < c1) load(base + kTilePages);
+    ok = mbar_wait_lean(&done, phase, wctl) && ok;
+    __syncwarp();
+    tc_fence_after();
+    // ---- D: the two warps of a quarter take rows (below 8 columns a row: groups of 8 columns) in turn.
+    const auto put = [&](int i, float best) {
+      if (i < rt.n && blk < c1)
+        p.scores[((rt.row0 + i) * p.num_kv_heads + h) * p.stride + blk] =
+            page >= 0 ? __fadd_rn(__fmul_rn(best, s), 0.0f) : -INFINITY;  // (-0 becomes 0)
+    };
+    if (gp >= 8) {
+      for (int i = half; i < rt.n; i += 2) {
+        const uint32_t at = mine + kColD + i * gp;
+        const float* t = scale_of + i * gp;
+        put(i, (gp & 31) == 0 ? largest<32>(at, t, gp) : (gp & 15) == 0 ? largest<16>(at, t, gp) : largest<8>(at, t, gp));
+      }
+    } else {
+      for (int n0 = 8 * half; n0 < rt.n * gp; n0 += 16) {
+        uint32_t r[8];
+        tmem_ld_32x32b_x8(mine + kColD + n0, r);
+        tmem_wait_ld();
+        float z[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) z[e] = __fmul_rn(__uint_as_float(r[e]), scale_of[n0 + e]);
+#pragma unroll
+        for (int e = 0; e < 8; e += 4) {
+          const int i = (n0 + e) / gp;
+          if (gp == 1) {
+            put(i, z[e]);
+            put(i + 1, z[e + 1]);
+            put(i + 2, z[e + 2]);
+            put(i + 3, z[e + 3]);
+          } else if (gp == 2) {
+            put(i, fmaxf(z[e], z[e + 1]));
+            put(i + 1, fmaxf(z[e + 2], z[e + 3]));
+          } else {
+            put(i, fmaxf(fmaxf(z[e], z[e + 1]), fmaxf(z[e + 2], z[e + 3])));
           }
-          if (t < 2) put(row, t, t ? m[1] : m[0]);
-          ++row;
-          in_row = 0;
-          m[0] = m[1] = -INFINITY;
-        }
-      } else if (gp == 1) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) put(8 * n + 2 * t + (e & 1), e >> 1, z[e]);
-      } else {
-        float x[2] = {fmaxf(z[0], z[1]), fmaxf(z[2], z[3])};
-        if (gp == 4) {
-#pragma unroll
-          for (int r = 0; r < 2; ++r) x[r] = fmaxf(x[r], __shfl_xor_sync(0xffffffffu, x[r], 1));
-          if (!(t & 1)) put(2 * n + (t >> 1), 0, x[0]);
-          else put(2 * n + (t >> 1), 1, x[1]);
-        } else {
-          put(4 * n + t, 0, x[0]);
-          put(4 * n + t, 1, x[1]);
         }
       }
     }
+    tc_fence_before();
+    if (__syncthreads_or(!ok)) break;  // (D is read; a wait that gave up stops the block)
+  }
+  if (tid == 0 && wctl->abort && p.err) atomicOr(p.err, CAI_DEVERR_TIMEOUT);
+  tc_fence_after();
+  if (warp == 0) {
+    if (!ok) mbar_wait_drain(&done, phase);  // the products have ended before tensor memory goes
+    __syncwarp();
+    tmem_dealloc(tmem, kTmem);
   }
 }
 
@@ -222,7 +305,7 @@ __device__ __forceinline__ uint32_t order_of(float x) {
 
 // A block per (row, K/V head).  The keep - first - last largest of the scores between: their least by a radix search of
 // eight bits at a time, then the pages in order, ties from the front.
-__global__ void __launch_bounds__(kWarps * 32) select_kernel(const __grid_constant__ SelectParams p) {
+__global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ SelectParams p) {
   __shared__ int hist[256];
   __shared__ uint32_t found[2];  // digits so far, how many of the least score are taken
   __shared__ int sums[2][kWarps];
@@ -244,13 +327,13 @@ __global__ void __launch_bounds__(kWarps * 32) select_kernel(const __grid_consta
     pos = (int64_t)p.start_pos[b] + (row - (int64_t)b * p.n_new);
   }
   if (p.q_off && blockIdx.x == 0)
-    for (int i = tid; i < p.batch; i += kWarps * 32)
+    for (int i = tid; i < p.batch; i += kThreads)
       if (new_rows(p, i).n < 0 && p.err) atomicOr(p.err, CAI_DEVERR_LENGTH);
   const int lg = page_log2(p.page_size);
   const bool ok = b >= 0 && pos >= 0 && pos < (int64_t)p.max_pages << lg;
   if (!ok) {
     if (b >= 0 && tid == 0 && p.err) atomicOr(p.err, CAI_DEVERR_LENGTH);
-    for (int i = tid; i < p.keep; i += kWarps * 32) out[i] = -1;
+    for (int i = tid; i < p.keep; i += kThreads) out[i] = -1;
     if (h == 0 && tid == 0) p.len_out[row] = 0;
     return;
   }
@@ -259,7 +342,7 @@ __global__ void __launch_bounds__(kWarps * 32) select_kernel(const __grid_consta
   const auto bad = [&](int32_t page) { return (uint32_t)page >= (uint32_t)p.num_pages[h]; };
   if (h == 0 && tid == 0) p.len_out[row] = n <= p.keep ? (int)pos + 1 : ((p.keep - 1) << lg) + (int)(pos & (p.page_size - 1)) + 1;
   if (n <= p.keep) {
-    for (int i = tid; i < p.keep; i += kWarps * 32) {
+    for (int i = tid; i < p.keep; i += kThreads) {
       const int32_t page = i < n ? table[i] : -1;
       if (i < n && bad(page) && p.err) atomicOr(p.err, CAI_DEVERR_PAGE);
       out[i] = page;
@@ -275,7 +358,7 @@ __global__ void __launch_bounds__(kWarps * 32) select_kernel(const __grid_consta
     for (int shift = 24; shift >= 0; shift -= 8) {
       hist[tid] = 0;
       __syncthreads();
-      for (int i = lo + tid; i < hi; i += kWarps * 32) {
+      for (int i = lo + tid; i < hi; i += kThreads) {
         const uint32_t x = order_of(scores[i]);
         if ((x & mask) == prefix) atomicAdd(&hist[(x >> shift) & 255u], 1);
       }
@@ -309,7 +392,7 @@ __global__ void __launch_bounds__(kWarps * 32) select_kernel(const __grid_consta
   }
   int at = 0;        // pages written by the block so far
   uint32_t tied = 0; // of the least score seen so far
-  for (int i0 = 0; i0 < n; i0 += kWarps * 32) {
+  for (int i0 = 0; i0 < n; i0 += kThreads) {
     const int i = i0 + tid;
     const bool forced = i < lo || i >= hi;
     const uint32_t x = i < n && !forced ? order_of(scores[i]) : 0u;
@@ -356,16 +439,19 @@ cudaError_t launch_select(const SelectParams& p, cudaStream_t stream) {
     const int most = p.q_off ? std::min(p.n_new, p.total_new) : p.n_new;
     const int per = std::max(1, std::min(most, kCols / gp));
     const int64_t tiles = p.q_off ? rows / per + p.batch : (int64_t)p.batch * ((p.n_new + per - 1) / per);
-    const int64_t chunks = ((int64_t)p.max_pages + kChunk - 1) / kChunk;
-    const int64_t grid = tiles * p.num_kv_heads * chunks;
+    // Page tiles of a block: as many as leave four blocks an SM.
+    const int64_t units = tiles * p.num_kv_heads, page_tiles = ((int64_t)p.max_pages + kTilePages - 1) / kTilePages;
+    const int64_t want = std::max<int64_t>(1, 4 * num_sms() / units);
+    const int span = (int)((page_tiles + want - 1) / want), spans = (int)((page_tiles + span - 1) / span);
+    const int64_t grid = units * spans;
     if (grid > 2147483647ll) return cudaErrorInvalidValue;
-    const size_t smem = (size_t)((per * gp + 7) / 8 * 8) * kColBytes;
-    const cudaError_t e = launch_pdl(score_kernel, dim3((unsigned)grid), dim3(kWarps * 32), smem, stream, p, per, (int)chunks);
+    const size_t smem = (size_t)((per * gp + 15) / 16 * 16) * kColBytes;
+    const cudaError_t e = launch_pdl(score_kernel, dim3((unsigned)grid), dim3(kThreads), smem, stream, p, per, spans, span);
     if (e != cudaSuccess) return e;
   }
   const int64_t grid = rows * p.num_kv_heads;
   if (grid > 2147483647ll) return cudaErrorInvalidValue;
-  return launch_pdl(select_kernel, dim3((unsigned)grid), dim3(kWarps * 32), 0, stream, p);
+  return launch_pdl(select_kernel, dim3((unsigned)grid), dim3(kThreads), 0, stream, p);
 }
 
 }  // namespace cai
