@@ -303,8 +303,263 @@ __device__ __forceinline__ uint32_t order_of(float x) {
   return u ^ (u >> 31 ? 0xFFFFFFFFu : 0x80000000u);
 }
 
-// A block per (row, K/V head).  The keep - first - last largest of the scores between: their least by a radix search of
-// eight bits at a time, then the pages in order, ties from the front.
+// What a row takes.  b < 0: no sequence has it; n = 0: nothing (flagged by the caller where b >= 0).
+struct Row {
+  int b, n;
+  int64_t pos;
+};
+__device__ __forceinline__ Row find_row(const SelectParams& p, int64_t row, int lane) {
+  Row r = {-1, 0, -1};
+  if (p.q_off) {
+    int32_t a, e;
+    r.b = find_seq(p.q_off, p.batch, row, lane, &a, &e);
+    if (r.b >= 0 && !(a >= 0 && row < e && e <= p.total_new && e - a <= p.n_new)) r.b = -1;
+    if (r.b >= 0) r.pos = (int64_t)p.start_pos[r.b] + (row - a);
+  } else {
+    r.b = (int)over(row, p.n_new);
+    r.pos = (int64_t)p.start_pos[r.b] + (row - (int64_t)r.b * p.n_new);
+  }
+  const int lg = page_log2(p.page_size);
+  if (r.b >= 0 && r.pos >= 0 && r.pos < (int64_t)p.max_pages << lg) r.n = (int)(r.pos >> lg) + 1;
+  return r;
+}
+__device__ __forceinline__ int row_length(const SelectParams& p, const Row& r) {
+  const int lg = page_log2(p.page_size);
+  return r.n <= p.keep ? (int)r.pos + 1 : ((p.keep - 1) << lg) + (int)(r.pos & (p.page_size - 1)) + 1;
+}
+// The list of a row that takes all of its pages (or none), by `threads` threads.
+__device__ __forceinline__ void take_all(const SelectParams& p, const Row& r, int h, int32_t* out, int tid, int threads) {
+  const int32_t* table = p.table + (int64_t)max(r.b, 0) * p.max_pages;
+  bool bad = false;
+  for (int i = tid; i < p.keep; i += threads) {
+    const int32_t page = i < r.n ? __ldg(table + i) : -1;
+    bad |= i < r.n && (uint32_t)page >= (uint32_t)p.num_pages[h];
+    out[i] = page;
+  }
+  if (bad && p.err) atomicOr(p.err, CAI_DEVERR_PAGE);
+}
+
+// The m-th largest of the values of a group of threads, kItems each (0: none): the values above `least` and the first
+// `ties` of it are the m largest.  Bit by bit from the first in which the values differ: as soon as a prefix has exactly m
+// values at or above it these are they, so rows of distinct scores rarely need all 32 bits.
+template <int kItems, class Group>
+__device__ __forceinline__ void find_least(const Group& group, const uint32_t (&x)[kItems], int items, int m, uint32_t& least, uint32_t& ties) {
+  uint32_t low = 0xFFFFFFFFu, high = 0u;
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    if (k >= items) break;
+    high = max(high, x[k]);
+    low = min(low, x[k] ? x[k] : 0xFFFFFFFFu);
+  }
+  group.range(low, high);
+  const auto count = [&](uint32_t c) {  // values at or above c
+    uint32_t n = 0;
+#pragma unroll
+    for (int k = 0; k < kItems; ++k) {
+      if (k >= items) break;
+      n += x[k] >= c ? 1u : 0u;
+    }
+    return (int)group.sum(n);
+  };
+  least = high;
+  if (low != high) {
+    const int top = 31 - __clz(low ^ high);
+    least = high & ~((2u << top) - 1u);  // at least m values are at or above it
+    for (int bit = top; bit >= 0; --bit) {
+      const uint32_t c = least | 1u << bit;
+      const int n = count(c);
+      if (n >= m) least = c;
+      if (n == m) {
+        least -= 1;  // all values at or above c, none of the ones below
+        ties = 0;
+        return;
+      }
+    }
+  }
+  ties = (uint32_t)(m - (least == 0xFFFFFFFFu ? 0 : count(least + 1)));
+}
+struct WarpGroup {
+  __device__ __forceinline__ void range(uint32_t& low, uint32_t& high) const {
+    low = __reduce_min_sync(0xffffffffu, low);
+    high = __reduce_max_sync(0xffffffffu, high);
+  }
+  __device__ __forceinline__ uint32_t sum(uint32_t n) const { return __reduce_add_sync(0xffffffffu, n); }
+};
+// A block: the warps' parts through shared memory, two buffers in turn so that one barrier a step is enough.
+struct BlockGroup {
+  uint32_t (*part)[2 * kWarps];
+  mutable int turn = 0;
+  __device__ __forceinline__ void range(uint32_t& low, uint32_t& high) const {
+    WarpGroup{}.range(low, high);
+    uint32_t* mine = part[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) {
+      mine[threadIdx.x >> 5] = low;
+      mine[kWarps + (threadIdx.x >> 5)] = high;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      low = min(low, mine[w]);
+      high = max(high, mine[kWarps + w]);
+    }
+  }
+  __device__ __forceinline__ uint32_t sum(uint32_t n) const {
+    n = WarpGroup{}.sum(n);
+    uint32_t* mine = part[turn];
+    turn ^= 1;
+    if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = n;
+    __syncthreads();
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) n += mine[w];
+    return n;
+  }
+};
+
+// A warp per (row, K/V head), for contexts of up to 32 kItems pages: the scores stay in registers, page 32 k + l in lane l.
+template <int kItems>
+__global__ void __launch_bounds__(kThreads) select_warp_kernel(const __grid_constant__ SelectParams p, int64_t units) {
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (p.q_off && blockIdx.x == 0)
+    for (int i = tid; i < p.batch; i += kThreads)
+      if (new_rows(p, i).n < 0 && p.err) atomicOr(p.err, CAI_DEVERR_LENGTH);
+  const int64_t unit = (int64_t)blockIdx.x * kWarps + (tid >> 5);
+  if (unit >= units) return;
+  const int64_t row = over(unit, p.num_kv_heads);
+  const int h = (int)(unit - row * p.num_kv_heads);
+  int32_t* out = p.pages_out + unit * p.keep;
+  const Row r = find_row(p, row, lane);
+  if (lane == 0) {
+    if (r.n == 0 && r.b >= 0 && p.err) atomicOr(p.err, CAI_DEVERR_LENGTH);
+    if (h == 0) p.len_out[row] = r.n ? row_length(p, r) : 0;
+  }
+  if (r.n <= p.keep) return take_all(p, r, h, out, lane, 32);
+  const float* scores = p.scores + unit * p.stride;
+  const int lo = p.first, hi = r.n - p.last, items = (r.n + 31) / 32;
+  uint32_t x[kItems];
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    const int i = 32 * k + lane;
+    x[k] = i >= lo && i < hi ? order_of(__ldcs(scores + i)) : 0u;
+  }
+  uint32_t least = 0xFFFFFFFFu, ties = 0;
+  if (p.keep > p.first + p.last) find_least(WarpGroup{}, x, items, p.keep - p.first - p.last, least, ties);
+  const int32_t* table = p.table + (int64_t)r.b * p.max_pages;
+  const uint32_t below = (1u << lane) - 1u;
+  int at = 0;
+  uint32_t tied = 0;
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    if (k >= items) break;
+    const int i = 32 * k + lane;
+    bool take = i < r.n && (i < lo || i >= hi || x[k] > least);
+    if (ties > tied) {  // (the same in the whole warp)
+      const bool tie = i >= lo && i < hi && x[k] == least;
+      const uint32_t m = __ballot_sync(0xffffffffu, tie);
+      take |= tie && tied + __popc(m & below) < ties;
+      tied += __popc(m);
+    }
+    const uint32_t m = __ballot_sync(0xffffffffu, take);
+    const int to = at + __popc(m & below);
+    if (take && to < p.keep) {
+      const int32_t page = __ldg(table + i);
+      bad |= (uint32_t)page >= (uint32_t)p.num_pages[h];
+      out[to] = page;
+    }
+    at += __popc(m);
+  }
+  if (bad && p.err) atomicOr(p.err, CAI_DEVERR_PAGE);
+}
+
+// A block per (row, K/V head), for contexts of up to 256 kItems pages: page 256 k + t in thread t.
+template <int kItems>
+__global__ void __launch_bounds__(kThreads) select_block_kernel(const __grid_constant__ SelectParams p) {
+  __shared__ uint32_t part[2][2 * kWarps];
+  __shared__ uint32_t counts[kItems * kWarps];  // pages taken, and of the least score, of item k in warp w: low and high half
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t row = over(blockIdx.x, p.num_kv_heads);
+  const int h = (int)(blockIdx.x - row * p.num_kv_heads);
+  int32_t* out = p.pages_out + (int64_t)blockIdx.x * p.keep;
+  if (p.q_off && blockIdx.x == 0)
+    for (int i = tid; i < p.batch; i += kThreads)
+      if (new_rows(p, i).n < 0 && p.err) atomicOr(p.err, CAI_DEVERR_LENGTH);
+  const Row r = find_row(p, row, lane);
+  if (tid == 0) {
+    if (r.n == 0 && r.b >= 0 && p.err) atomicOr(p.err, CAI_DEVERR_LENGTH);
+    if (h == 0) p.len_out[row] = r.n ? row_length(p, r) : 0;
+  }
+  if (r.n <= p.keep) return take_all(p, r, h, out, tid, kThreads);
+  const float* scores = p.scores + (int64_t)blockIdx.x * p.stride;
+  const int lo = p.first, hi = r.n - p.last, items = (r.n + kThreads - 1) / kThreads;
+  uint32_t x[kItems];
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    const int i = kThreads * k + tid;
+    x[k] = i >= lo && i < hi ? order_of(__ldcs(scores + i)) : 0u;
+  }
+  uint32_t least = 0xFFFFFFFFu, ties = 0;
+  const BlockGroup group = {part};
+  if (p.keep > p.first + p.last) find_least(group, x, items, p.keep - p.first - p.last, least, ties);
+  // Every (item, warp)'s counts, then what comes before it.
+  const uint32_t below = (1u << lane) - 1u;
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    if (k >= items) break;
+    const int i = kThreads * k + tid;
+    const bool sure = i < r.n && (i < lo || i >= hi || x[k] > least);
+    const bool tie = ties > 0 && i >= lo && i < hi && x[k] == least;
+    const uint32_t ms = __ballot_sync(0xffffffffu, sure), mt = __ballot_sync(0xffffffffu, tie);
+    if (lane == 0) counts[k * kWarps + warp] = (uint32_t)__popc(ms) | (uint32_t)__popc(mt) << 16;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    const int total = items * kWarps, run = (total + 31) / 32, i0 = min(total, lane * run), i1 = min(total, i0 + run);
+    uint32_t sum = 0;
+    for (int i = i0; i < i1; ++i) sum += counts[i];
+    uint32_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    uint32_t at = incl - sum;
+    for (int i = i0; i < i1; ++i) {
+      const uint32_t c = counts[i];
+      counts[i] = at;
+      at += c;
+    }
+  }
+  __syncthreads();
+  const int32_t* table = p.table + (int64_t)r.b * p.max_pages;
+  bool bad = false;
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {
+    if (k >= items) break;
+    const int i = kThreads * k + tid;
+    const bool sure = i < r.n && (i < lo || i >= hi || x[k] > least);
+    const bool tie = ties > 0 && i >= lo && i < hi && x[k] == least;
+    const uint32_t ms = __ballot_sync(0xffffffffu, sure), mt = __ballot_sync(0xffffffffu, tie);
+    if (!(ms | mt)) continue;
+    const uint32_t before = counts[k * kWarps + warp];
+    const uint32_t rank = (before >> 16) + __popc(mt & below);           // ties before this page
+    const uint32_t to = (before & 0xFFFFu) + __popc(ms & below) + min(rank, ties);
+    if ((sure || (tie && rank < ties)) && to < (uint32_t)p.keep) {
+      const int32_t page = __ldg(table + i);
+      bad |= (uint32_t)page >= (uint32_t)p.num_pages[h];
+      out[to] = page;
+    }
+  }
+  if (bad && p.err) atomicOr(p.err, CAI_DEVERR_PAGE);
+}
+
+// A block per (row, K/V head), for contexts of any length.  The keep - first - last largest of the scores between: their
+// least by a radix search of eight bits at a time, then the pages in order, ties from the front.
 __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ SelectParams p) {
   __shared__ int hist[256];
   __shared__ uint32_t found[2];  // digits so far, how many of the least score are taken
@@ -315,40 +570,18 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
   const int64_t row = over(blockIdx.x, p.num_kv_heads);
   const int h = (int)(blockIdx.x - row * p.num_kv_heads);
   int32_t* out = p.pages_out + (int64_t)blockIdx.x * p.keep;
-  int b = -1;
-  int64_t pos = -1;
-  if (p.q_off) {
-    int32_t a, e;
-    b = find_seq(p.q_off, p.batch, row, lane, &a, &e);
-    if (b >= 0 && !(a >= 0 && row < e && e <= p.total_new && e - a <= p.n_new)) b = -1;
-    if (b >= 0) pos = (int64_t)p.start_pos[b] + (row - a);
-  } else {
-    b = (int)over(row, p.n_new);
-    pos = (int64_t)p.start_pos[b] + (row - (int64_t)b * p.n_new);
-  }
   if (p.q_off && blockIdx.x == 0)
     for (int i = tid; i < p.batch; i += kThreads)
       if (new_rows(p, i).n < 0 && p.err) atomicOr(p.err, CAI_DEVERR_LENGTH);
-  const int lg = page_log2(p.page_size);
-  const bool ok = b >= 0 && pos >= 0 && pos < (int64_t)p.max_pages << lg;
-  if (!ok) {
-    if (b >= 0 && tid == 0 && p.err) atomicOr(p.err, CAI_DEVERR_LENGTH);
-    for (int i = tid; i < p.keep; i += kThreads) out[i] = -1;
-    if (h == 0 && tid == 0) p.len_out[row] = 0;
-    return;
+  const Row r = find_row(p, row, lane);
+  const int n = r.n;
+  if (tid == 0) {
+    if (n == 0 && r.b >= 0 && p.err) atomicOr(p.err, CAI_DEVERR_LENGTH);
+    if (h == 0) p.len_out[row] = n ? row_length(p, r) : 0;
   }
-  const int n = (int)(pos >> lg) + 1;
-  const int32_t* table = p.table + (int64_t)b * p.max_pages;
+  if (n <= p.keep) return take_all(p, r, h, out, tid, kThreads);
+  const int32_t* table = p.table + (int64_t)r.b * p.max_pages;
   const auto bad = [&](int32_t page) { return (uint32_t)page >= (uint32_t)p.num_pages[h]; };
-  if (h == 0 && tid == 0) p.len_out[row] = n <= p.keep ? (int)pos + 1 : ((p.keep - 1) << lg) + (int)(pos & (p.page_size - 1)) + 1;
-  if (n <= p.keep) {
-    for (int i = tid; i < p.keep; i += kThreads) {
-      const int32_t page = i < n ? table[i] : -1;
-      if (i < n && bad(page) && p.err) atomicOr(p.err, CAI_DEVERR_PAGE);
-      out[i] = page;
-    }
-    return;
-  }
   const float* scores = p.scores + (int64_t)blockIdx.x * p.stride;
   const int lo = p.first, hi = n - p.last;
   uint32_t least = 0xFFFFFFFFu, ties = 0;  // taken: scores above `least`, and the first `ties` of it
@@ -449,9 +682,13 @@ cudaError_t launch_select(const SelectParams& p, cudaStream_t stream) {
     const cudaError_t e = launch_pdl(score_kernel, dim3((unsigned)grid), dim3(kThreads), smem, stream, p, per, spans, span);
     if (e != cudaSuccess) return e;
   }
-  const int64_t grid = rows * p.num_kv_heads;
-  if (grid > 2147483647ll) return cudaErrorInvalidValue;
-  return launch_pdl(select_kernel, dim3((unsigned)grid), dim3(kThreads), 0, stream, p);
+  const int64_t units = rows * p.num_kv_heads, warps = (units + kWarps - 1) / kWarps;
+  if (units > 2147483647ll) return cudaErrorInvalidValue;
+  const auto by_warps = [&](auto kernel) { return launch_pdl(kernel, dim3((unsigned)warps), dim3(kThreads), 0, stream, p, units); };
+  if (p.max_pages <= 256) return by_warps(select_warp_kernel<8>);
+  if (p.max_pages <= 1024) return by_warps(select_warp_kernel<32>);
+  if (p.max_pages <= 32 * kThreads) return launch_pdl(select_block_kernel<32>, dim3((unsigned)units), dim3(kThreads), 0, stream, p);
+  return launch_pdl(select_kernel, dim3((unsigned)units), dim3(kThreads), 0, stream, p);
 }
 
 }  // namespace cai

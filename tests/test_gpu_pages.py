@@ -227,8 +227,11 @@ def test_select_ties_go_to_the_lower_page():
     check_select(1, 4, 16, [3000, 700], [2, 2], 40, 0, 1, ties=True, packed=False, size=0.0)  # zero queries: all scores 0
 
 
-def test_select_long_context():
-    check_select(1, 16, 16, [131071, 100000], [1, 2], 128, 1, 2, seed=5)
+@pytest.mark.parametrize("context", [4100, 16000, 131071, 300000])
+def test_select_long_context(context):
+    """A table of each kernel's range: a warp a row, a block, and contexts of any length."""
+    check_select(1, 16, 16, [context, 900, context - 3], [1, 2, 1], 128, 1, 2, seed=5)
+    check_select(1, 2, 16, [context, 2000], [1, 2], 33, 1, 2, seed=6, ties=True)
 
 
 def test_select_extreme_queries():
