@@ -86,35 +86,33 @@ __device__ __forceinline__ RowTile find_tile(const SelectParams& p, int64_t tile
   return *found;
 }
 
-// The largest of t_c D_c over columns c0 .. c0 + gp - 1 (8 N of them) of this thread's page.
+__device__ __forceinline__ uint32_t half2_max0(uint32_t x) {
+  uint32_t y;
+  asm("max.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0u));
+  return y;
+}
+__device__ __forceinline__ uint32_t half2_min0(uint32_t x) {
+  uint32_t y;
+  asm("min.f16x2 %0, %1, %2;" : "=r"(y) : "r"(x), "r"(0u));
+  return y;
+}
+
+// The largest of m and t_c D_c, over N columns.
 template <int N>
-__device__ __forceinline__ float largest(uint32_t tmem, const float* scale_of, int gp) {
-  float m = -INFINITY;
-  for (int c = 0; c < gp; c += N) {
-    uint32_t r[N];
-    if constexpr (N == 32) tmem_ld_32x32b_x32(tmem + c, r);
-    else if constexpr (N == 16) tmem_ld_32x32b_x16(tmem + c, r);
-    else tmem_ld_32x32b_x8(tmem + c, r);
-    tmem_wait_ld();
+__device__ __forceinline__ float largest(float m, const uint32_t (&r)[N], const float* scale_of) {
 #pragma unroll
-    for (int e = 0; e < N; e += 4) {
-      const float4 t = *reinterpret_cast<const float4*>(scale_of + c + e);
-      float z[4];
-      f2_split(f2_mul(f2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), f2(t.x, t.y)), z[0], z[1]);
-      f2_split(f2_mul(f2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), f2(t.z, t.w)), z[2], z[3]);
-      m = fmax3(fmax3(m, z[0], z[1]), z[2], z[3]);
-    }
+  for (int e = 0; e < N; e += 4) {
+    const float4 t = *reinterpret_cast<const float4*>(scale_of + e);
+    float z[4];
+    f2_split(f2_mul(f2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), f2(t.x, t.y)), z[0], z[1]);
+    f2_split(f2_mul(f2(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])), f2(t.z, t.w)), z[2], z[3]);
+    m = fmax3(fmax3(m, z[0], z[1]), z[2], z[3]);
   }
   return m;
 }
 
-// rint(x / t), the division IEEE: by the inverse, and by the division itself where that may round the other way.
-__device__ __forceinline__ float whole(float x, float t, float inv) {
-  const float y = x * inv;
-  float c = rintf(y);
-  if (!(fabsf(y - c) < 0.499f)) c = rintf(__fdiv_rn(x, t));
-  return fminf(fmaxf(c, -127.0f), 127.0f);
-}
+// rint(x / t) clamped, the division IEEE.
+__device__ __forceinline__ float whole(float x, float t) { return fminf(fmaxf(rintf(__fdiv_rn(x, t)), -127.0f), 127.0f); }
 
 // Scores of a tile of rows over `span` tiles of their pages.  Block: (row tile, K/V head, span), the span fastest.
 __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constant__ SelectParams p, int per, int spans, int span) {
@@ -157,7 +155,9 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
   };
   // This lane's 64 codes, 16 of every 64, of pages (quarter, half) 16 + g and + 8 of a tile.
   uint4 a[2][4];
+  const auto there = [&](int base) { return base + 32 * quarter + 16 * half < c1; };  // (this warp has pages of the tile)
   const auto load = [&](int base) {
+    if (!there(base)) return;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int32_t page = page_of(base + 32 * quarter + 16 * half + g + 8 * r);
@@ -182,25 +182,41 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
       for (int k = 0; k < 2; ++k)
         w[c][k] = i < rt.n ? __ldg(reinterpret_cast<const uint4*>(p.q + ((rt.row0 + i) * p.num_q_heads + h * G + head) * kHeadDim + 64 * c + 16 * t4) + k)
                            : make_uint4(0u, 0u, 0u, 0u);
-    float amax = 0.0f;
+    float y[32], amax = 0.0f;
 #pragma unroll
     for (int x = 0; x < 16; ++x) {
       const uint4& v = w[x >> 3][x >> 2 & 1];
       const uint32_t u = (x & 3) == 0 ? v.x : (x & 3) == 1 ? v.y : (x & 3) == 2 ? v.z : v.w;
-      amax = fmax3(amax, fabsf(__uint_as_float(u << 16)), fabsf(__uint_as_float(u & 0xFFFF0000u)));
+      y[2 * x] = __uint_as_float(u << 16);
+      y[2 * x + 1] = __uint_as_float(u & 0xFFFF0000u);
+      amax = fmax3(amax, fabsf(y[2 * x]), fabsf(y[2 * x + 1]));
     }
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-    const float t = __fdiv_rn(amax, 127.0f), inv = __frcp_rn(t);
+    // x / t as the IEEE division rounds it, by one correction of the product with the rounded inverse (Markstein, 1990);
+    // for bf16 numerators and t = amax / 127 every pair of significands was tried.  (A product alone is wrong for 24 pairs
+    // of 188480, near halves: x = amax / 2 is one.)  Below 2^-100, where the correction may be subnormal, the division itself.
+    const float t = __fdiv_rn(amax, 127.0f), inv = t >= 0x1p-100f ? __frcp_rn(t) : 0.0f;
+    const uint64_t inv2 = f2(inv, inv), t2 = f2(-t, -t), magic = f2(12582912.0f, 12582912.0f), unmagic = f2(-12582912.0f, -12582912.0f);  // 3 2^22
     uint32_t* dst = reinterpret_cast<uint32_t*>(cols + (n0 >> 3) * (8 * kColBytes) + g * 16 + t4 * 4);
 #pragma unroll
     for (int x = 0; x < 16; ++x) {
-      const uint4& v = w[x >> 3][x >> 2 & 1];
-      const uint32_t u = (x & 3) == 0 ? v.x : (x & 3) == 1 ? v.y : (x & 3) == 2 ? v.z : v.w;
-      const float q0 = t > 0.0f ? whole(__uint_as_float(u << 16), t, inv) : 0.0f;
-      const float q1 = t > 0.0f ? whole(__uint_as_float(u & 0xFFFF0000u), t, inv) : 0.0f;
-      dst[x * 32] = pack_f16x2(fmaxf(q0, 0.0f), fmaxf(q1, 0.0f));
-      dst[(16 + x) * 32] = pack_f16x2(fminf(q0, 0.0f), fminf(q1, 0.0f));
+      const uint64_t y2 = f2(y[2 * x], y[2 * x + 1]), z = f2_mul(y2, inv2);
+      float q0, q1;
+      f2_split(f2_add(f2_add(f2_fma(f2_fma(z, t2, y2), inv2, z), magic), unmagic), q0, q1);
+      const uint32_t q2 = pack_f16x2(q0, q1);
+      dst[x * 32] = half2_max0(q2);
+      dst[(16 + x) * 32] = half2_min0(q2);
+    }
+    if (t > 0.0f && inv == 0.0f) {
+      const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q + ((rt.row0 + i) * p.num_q_heads + h * G + head) * kHeadDim + 16 * t4);
+#pragma unroll 1
+      for (int x = 0; x < 16; ++x) {
+        const uint32_t u = __ldg(src + (x >> 3) * 32 + (x & 7));
+        const uint32_t q2 = pack_f16x2(whole(__uint_as_float(u << 16), t), whole(__uint_as_float(u & 0xFFFF0000u), t));
+        dst[x * 32] = half2_max0(q2);
+        dst[(16 + x) * 32] = half2_min0(q2);
+      }
     }
     if (t4 == 0) scale_of[n] = t;
   }
@@ -216,9 +232,11 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
   bool ok = true;
   int phase = 0;
   for (int base = c0; base < c1; base += kTilePages, phase ^= 1) {
-    // ---- A: column 32 c + 4 e + t holds channels 64 c + 16 t + 2 e, + 1 of the 256 codes.
+    // ---- A: column 32 c + 4 e + t holds channels 64 c + 16 t + 2 e, + 1 of the 256 codes.  (Rows of pages that are not
+    // there keep what they held: D's rows are independent.)
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
+      if (!there(base)) break;
       uint32_t r[16];
       const uint32_t x[4] = {a[0][c].x, a[0][c].y, a[0][c].z, a[0][c].w}, y[4] = {a[1][c].x, a[1][c].y, a[1][c].z, a[1][c].w};
 #pragma unroll
@@ -244,7 +262,7 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
     const int32_t page = page_of(blk);
     const float s = page >= 0 ? __ldg(scales + page) : 0.0f;
     if (page < 0 && half == 0 && p.err) atomicOr(p.err, CAI_DEVERR_PAGE);
-    if (base + kTilePages < c1) load(base + kTilePages);
+    load(base + kTilePages);
     ok = mbar_wait_lean(&done, phase, wctl) && ok;
     __syncwarp();
     tc_fence_after();
@@ -254,11 +272,28 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
         p.scores[((rt.row0 + i) * p.num_kv_heads + h) * p.stride + blk] =
             page >= 0 ? __fadd_rn(__fmul_rn(best, s), 0.0f) : -INFINITY;  // (-0 becomes 0)
     };
-    if (gp >= 8) {
+    if (base + 32 * quarter >= c1) {
+    } else if ((gp & 31) == 0) {
       for (int i = half; i < rt.n; i += 2) {
-        const uint32_t at = mine + kColD + i * gp;
-        const float* t = scale_of + i * gp;
-        put(i, (gp & 31) == 0 ? largest<32>(at, t, gp) : (gp & 15) == 0 ? largest<16>(at, t, gp) : largest<8>(at, t, gp));
+        float m = -INFINITY;
+        for (int c = 0; c < gp; c += 32) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(mine + kColD + i * gp + c, r);
+          tmem_wait_ld();
+          m = largest(m, r, scale_of + i * gp + c);
+        }
+        put(i, m);
+      }
+    } else if (gp >= 8) {
+      for (int i = half; i < rt.n; i += 2) {
+        float m = -INFINITY;
+        for (int c = 0; c < gp; c += 8) {
+          uint32_t r[8];
+          tmem_ld_32x32b_x8(mine + kColD + i * gp + c, r);
+          tmem_wait_ld();
+          m = largest(m, r, scale_of + i * gp + c);
+        }
+        put(i, m);
       }
     } else {
       for (int n0 = 8 * half; n0 < rt.n * gp; n0 += 16) {
@@ -303,6 +338,9 @@ __device__ __forceinline__ uint32_t order_of(float x) {
   return u ^ (u >> 31 ? 0xFFFFFFFFu : 0x80000000u);
 }
 
+// A score among values of which 0 means none and 0xFFFFFFFF one that is taken anyhow (both are orders of NaNs).
+__device__ __forceinline__ uint32_t looked_at(uint32_t x) { return min(max(x, 1u), 0xFFFFFFFEu); }
+
 // What a row takes.  b < 0: no sequence has it; n = 0: nothing (flagged by the caller where b >= 0).
 struct Row {
   int b, n;
@@ -339,94 +377,202 @@ __device__ __forceinline__ void take_all(const SelectParams& p, const Row& r, in
   if (bad && p.err) atomicOr(p.err, CAI_DEVERR_PAGE);
 }
 
-// The m-th largest of the values of a group of threads, kItems each (0: none): the values above `least` and the first
-// `ties` of it are the m largest.  Bit by bit from the first in which the values differ: as soon as a prefix has exactly m
-// values at or above it these are they, so rows of distinct scores rarely need all 32 bits.
+// The m-th largest of a group of threads' values, kItems each (0: none, 0xFFFFFFFF: not looked at): the values above
+// `least` and the first `ties` of it are the m largest.  The eight bits from the first in which the values differ are
+// counted in shared memory; the bin of the m-th largest holds few values, which are gathered and ranked, a thread each
+// (more than the group has threads: the next eight bits).  Ranks are by value, then by place, so the order of
+// gathering does not matter.
+struct Found {
+  uint32_t bin, need, total;  // of the values in the bin `need` are among the m largest
+};
 template <int kItems, class Group>
-__device__ __forceinline__ void find_least(const Group& group, const uint32_t (&x)[kItems], int items, int m, uint32_t& least, uint32_t& ties) {
+__device__ __forceinline__ void find_least(const Group& group, const uint32_t (&x)[kItems], int items, uint32_t m, uint32_t& least, uint32_t& ties) {
   uint32_t low = 0xFFFFFFFFu, high = 0u;
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
     if (k >= items) break;
-    high = max(high, x[k]);
-    low = min(low, x[k] ? x[k] : 0xFFFFFFFFu);
+    low = min(low, x[k] - 1u);           // (none: the largest)
+    high = max(high, x[k] + 1u);         // (not looked at: 0)
   }
   group.range(low, high);
-  const auto count = [&](uint32_t c) {  // values at or above c
-    uint32_t n = 0;
-#pragma unroll
-    for (int k = 0; k < kItems; ++k) {
-      if (k >= items) break;
-      n += x[k] >= c ? 1u : 0u;
-    }
-    return (int)group.sum(n);
-  };
-  least = high;
+  low += 1u;
+  high -= 1u;
+  uint32_t prefix = high, mask = 0xFFFFFFFFu;  // bits that are known
   if (low != high) {
     const int top = 31 - __clz(low ^ high);
-    least = high & ~((2u << top) - 1u);  // at least m values are at or above it
-    for (int bit = top; bit >= 0; --bit) {
-      const uint32_t c = least | 1u << bit;
-      const int n = count(c);
-      if (n >= m) least = c;
-      if (n == m) {
-        least -= 1;  // all values at or above c, none of the ones below
-        ties = 0;
+    mask = ~((2u << top) - 1u);
+    prefix = high & mask;
+    for (int shift = max(top - 7, 0);; shift = max(shift - 8, 0)) {
+      const uint32_t digit = ~mask >> shift;  // (as many ones as bits are unknown from `shift` up: 255 at most)
+      group.clear();
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        if (k >= items) break;
+        if ((x[k] & mask) == prefix && x[k] + 1u > 1u) atomicAdd(group.hist + ((x[k] >> shift) & digit), 1u);
+      }
+      const Found f = group.scan(m);
+      prefix |= f.bin << shift;
+      mask = ~((1u << shift) - 1u);
+      m = f.need;
+      if (shift == 0) break;
+      if (f.total <= (uint32_t)Group::kThreadsIn) {
+        // Gathered: the value, its place in the order of pages.
+#pragma unroll
+        for (int k = 0; k < kItems; ++k) {
+          if (k >= items) break;
+          if ((x[k] & mask) == prefix && x[k] + 1u > 1u) group.list[atomicAdd(group.count, 1u)] = make_uint2(x[k], k * Group::kThreadsIn + group.thread());
+        }
+        group.rank(f.total, m, least, ties);
         return;
       }
     }
   }
-  ties = (uint32_t)(m - (least == 0xFFFFFFFFu ? 0 : count(least + 1)));
+  least = prefix;  // all bits are known
+  ties = m;
+}
+// Bins of 256, from the largest on: that of the m-th value.  One warp; `hist` is read, not changed.
+__device__ __forceinline__ Found scan_bins(const uint32_t* hist, uint32_t m, int lane) {
+  uint32_t c[8], sum = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum += c[e] = hist[255 - 8 * lane - e];
+  uint32_t incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  uint32_t before = incl - sum;
+  Found f = {0, 0, 0};
+  bool found = false;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    if (!found && before < m && before + c[e] >= m) {
+      f = {(uint32_t)(255 - 8 * lane - e), m - before, c[e]};
+      found = true;
+    }
+    before += c[e];
+  }
+  const int who = 31 - __clz(__ballot_sync(0xffffffffu, found) | 1u);  // (one lane)
+  f.bin = __shfl_sync(0xffffffffu, f.bin, who);
+  f.need = __shfl_sync(0xffffffffu, f.need, who);
+  f.total = __shfl_sync(0xffffffffu, f.total, who);
+  return f;
 }
 struct WarpGroup {
+  static constexpr int kThreadsIn = 32;
+  uint32_t* hist;   // [256]
+  uint32_t* count;
+  uint2* list;      // [kThreadsIn]
+  __device__ __forceinline__ int thread() const { return threadIdx.x & 31; }
   __device__ __forceinline__ void range(uint32_t& low, uint32_t& high) const {
     low = __reduce_min_sync(0xffffffffu, low);
     high = __reduce_max_sync(0xffffffffu, high);
   }
-  __device__ __forceinline__ uint32_t sum(uint32_t n) const { return __reduce_add_sync(0xffffffffu, n); }
+  __device__ __forceinline__ void clear() const {
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) reinterpret_cast<uint4*>(hist)[32 * i + thread()] = make_uint4(0u, 0u, 0u, 0u);
+    if (thread() == 0) *count = 0u;
+    __syncwarp();
+  }
+  __device__ __forceinline__ Found scan(uint32_t m) const {
+    __syncwarp();
+    return scan_bins(hist, m, thread());
+  }
+  __device__ __forceinline__ void rank(uint32_t total, uint32_t need, uint32_t& least, uint32_t& ties) const {
+    __syncwarp();
+    const bool have = (uint32_t)thread() < total;
+    const uint2 mine = have ? list[thread()] : make_uint2(0u, 0u);
+    uint32_t before = 0;  // values ahead of this one
+#pragma unroll 4
+    for (uint32_t i = 0; i < total; ++i) {
+      const uint2 v = list[i];
+      before += v.x > mine.x || (v.x == mine.x && v.y < mine.y) ? 1u : 0u;
+    }
+    const uint32_t who = __ballot_sync(0xffffffffu, have && before == need - 1);
+    least = __shfl_sync(0xffffffffu, mine.x, 31 - __clz(who | 1u));
+    const uint32_t above = __popc(__ballot_sync(0xffffffffu, have && mine.x > least)), equal = __popc(__ballot_sync(0xffffffffu, have && mine.x == least));
+    ties = need - above;
+    if (ties == equal) least -= 1, ties = 0;  // all of them are taken
+  }
 };
-// A block: the warps' parts through shared memory, two buffers in turn so that one barrier a step is enough.
 struct BlockGroup {
-  uint32_t (*part)[2 * kWarps];
-  mutable int turn = 0;
+  static constexpr int kThreadsIn = kThreads;
+  uint32_t* hist;   // [256], then [2 kWarps] of the range, [3] of the scan, [3] of the rank
+  uint32_t* count;
+  uint2* list;
+  __device__ __forceinline__ int thread() const { return threadIdx.x; }
   __device__ __forceinline__ void range(uint32_t& low, uint32_t& high) const {
-    WarpGroup{}.range(low, high);
-    uint32_t* mine = part[turn];
-    turn ^= 1;
+    low = __reduce_min_sync(0xffffffffu, low);
+    high = __reduce_max_sync(0xffffffffu, high);
+    uint32_t* part = hist + 256;
     if ((threadIdx.x & 31) == 0) {
-      mine[threadIdx.x >> 5] = low;
-      mine[kWarps + (threadIdx.x >> 5)] = high;
+      part[threadIdx.x >> 5] = low;
+      part[kWarps + (threadIdx.x >> 5)] = high;
     }
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      low = min(low, mine[w]);
-      high = max(high, mine[kWarps + w]);
+      low = min(low, part[w]);
+      high = max(high, part[kWarps + w]);
     }
   }
-  __device__ __forceinline__ uint32_t sum(uint32_t n) const {
-    n = WarpGroup{}.sum(n);
-    uint32_t* mine = part[turn];
-    turn ^= 1;
-    if ((threadIdx.x & 31) == 0) mine[threadIdx.x >> 5] = n;
+  __device__ __forceinline__ void clear() const {
+    hist[threadIdx.x] = 0u;  // (read before the scan's barrier, if at all)
+    if (threadIdx.x == 0) *count = 0u;
+    if (threadIdx.x < 3) hist[256 + 2 * kWarps + 3 + threadIdx.x] = 0u;
     __syncthreads();
-    n = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) n += mine[w];
-    return n;
+  }
+  __device__ __forceinline__ Found scan(uint32_t m) const {
+    __syncthreads();
+    uint32_t* got = hist + 256 + 2 * kWarps;
+    if (threadIdx.x < 32) {
+      const Found f = scan_bins(hist, m, threadIdx.x);
+      if (threadIdx.x == 0) got[0] = f.bin, got[1] = f.need, got[2] = f.total;
+    }
+    __syncthreads();
+    return Found{got[0], got[1], got[2]};
+  }
+  __device__ __forceinline__ void rank(uint32_t total, uint32_t need, uint32_t& least, uint32_t& ties) const {
+    uint32_t* got = hist + 256 + 2 * kWarps + 3;  // the least value; of the gathered ones, those above it and equal
+    __syncthreads();
+    const bool have = threadIdx.x < total;
+    const uint2 mine = have ? list[threadIdx.x] : make_uint2(0u, 0u);
+    if (have) {
+      uint32_t before = 0;
+#pragma unroll 4
+      for (uint32_t i = 0; i < total; ++i) {
+        const uint2 v = list[i];
+        before += v.x > mine.x || (v.x == mine.x && v.y < mine.y) ? 1u : 0u;
+      }
+      if (before == need - 1) got[0] = mine.x;
+    }
+    __syncthreads();
+    least = got[0];
+    const uint32_t above = __popc(__ballot_sync(0xffffffffu, have && mine.x > least)), equal = __popc(__ballot_sync(0xffffffffu, have && mine.x == least));
+    if ((threadIdx.x & 31) == 0 && (above | equal)) {
+      atomicAdd(got + 1, above);
+      atomicAdd(got + 2, equal);
+    }
+    __syncthreads();
+    ties = need - got[1];
+    if (ties == got[2]) least -= 1, ties = 0;
   }
 };
 
 // A warp per (row, K/V head), for contexts of up to 32 kItems pages: the scores stay in registers, page 32 k + l in lane l.
 template <int kItems>
-__global__ void __launch_bounds__(kThreads) select_warp_kernel(const __grid_constant__ SelectParams p, int64_t units) {
+__global__ void __launch_bounds__(kThreads, 4) select_warp_kernel(const __grid_constant__ SelectParams p, int64_t units) {
+  __shared__ __align__(16) uint32_t hist[kWarps][256];
+  __shared__ uint32_t gathered[kWarps];
+  __shared__ uint2 list[kWarps][32];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int tid = threadIdx.x, lane = tid & 31;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (p.q_off && blockIdx.x == 0)
     for (int i = tid; i < p.batch; i += kThreads)
       if (new_rows(p, i).n < 0 && p.err) atomicOr(p.err, CAI_DEVERR_LENGTH);
-  const int64_t unit = (int64_t)blockIdx.x * kWarps + (tid >> 5);
+  const int64_t unit = (int64_t)blockIdx.x * kWarps + warp;
   if (unit >= units) return;
   const int64_t row = over(unit, p.num_kv_heads);
   const int h = (int)(unit - row * p.num_kv_heads);
@@ -443,10 +589,10 @@ __global__ void __launch_bounds__(kThreads) select_warp_kernel(const __grid_cons
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
     const int i = 32 * k + lane;
-    x[k] = i >= lo && i < hi ? order_of(__ldcs(scores + i)) : 0u;
+    x[k] = i >= lo && i < hi ? looked_at(order_of(__ldcs(scores + i))) : i < r.n ? 0xFFFFFFFFu : 0u;
   }
-  uint32_t least = 0xFFFFFFFFu, ties = 0;
-  if (p.keep > p.first + p.last) find_least(WarpGroup{}, x, items, p.keep - p.first - p.last, least, ties);
+  uint32_t least = 0xFFFFFFFEu, ties = 0;
+  if (p.keep > p.first + p.last) find_least(WarpGroup{hist[warp], gathered + warp, list[warp]}, x, items, p.keep - p.first - p.last, least, ties);
   const int32_t* table = p.table + (int64_t)r.b * p.max_pages;
   const uint32_t below = (1u << lane) - 1u;
   int at = 0;
@@ -456,9 +602,9 @@ __global__ void __launch_bounds__(kThreads) select_warp_kernel(const __grid_cons
   for (int k = 0; k < kItems; ++k) {
     if (k >= items) break;
     const int i = 32 * k + lane;
-    bool take = i < r.n && (i < lo || i >= hi || x[k] > least);
+    bool take = x[k] > least;
     if (ties > tied) {  // (the same in the whole warp)
-      const bool tie = i >= lo && i < hi && x[k] == least;
+      const bool tie = x[k] == least;
       const uint32_t m = __ballot_sync(0xffffffffu, tie);
       take |= tie && tied + __popc(m & below) < ties;
       tied += __popc(m);
@@ -478,7 +624,9 @@ __global__ void __launch_bounds__(kThreads) select_warp_kernel(const __grid_cons
 // A block per (row, K/V head), for contexts of up to 256 kItems pages: page 256 k + t in thread t.
 template <int kItems>
 __global__ void __launch_bounds__(kThreads) select_block_kernel(const __grid_constant__ SelectParams p) {
-  __shared__ uint32_t part[2][2 * kWarps];
+  __shared__ uint32_t hist[256 + 2 * kWarps + 6];
+  __shared__ uint32_t gathered;
+  __shared__ uint2 list[kThreads];
   __shared__ uint32_t counts[kItems * kWarps];  // pages taken, and of the least score, of item k in warp w: low and high half
   grid_dependency_wait();
   grid_launch_dependents();
@@ -501,19 +649,16 @@ __global__ void __launch_bounds__(kThreads) select_block_kernel(const __grid_con
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
     const int i = kThreads * k + tid;
-    x[k] = i >= lo && i < hi ? order_of(__ldcs(scores + i)) : 0u;
+    x[k] = i >= lo && i < hi ? looked_at(order_of(__ldcs(scores + i))) : i < r.n ? 0xFFFFFFFFu : 0u;
   }
-  uint32_t least = 0xFFFFFFFFu, ties = 0;
-  const BlockGroup group = {part};
-  if (p.keep > p.first + p.last) find_least(group, x, items, p.keep - p.first - p.last, least, ties);
+  uint32_t least = 0xFFFFFFFEu, ties = 0;
+  if (p.keep > p.first + p.last) find_least(BlockGroup{hist, &gathered, list}, x, items, p.keep - p.first - p.last, least, ties);
   // Every (item, warp)'s counts, then what comes before it.
   const uint32_t below = (1u << lane) - 1u;
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
     if (k >= items) break;
-    const int i = kThreads * k + tid;
-    const bool sure = i < r.n && (i < lo || i >= hi || x[k] > least);
-    const bool tie = ties > 0 && i >= lo && i < hi && x[k] == least;
+    const bool sure = x[k] > least, tie = ties > 0 && x[k] == least;
     const uint32_t ms = __ballot_sync(0xffffffffu, sure), mt = __ballot_sync(0xffffffffu, tie);
     if (lane == 0) counts[k * kWarps + warp] = (uint32_t)__popc(ms) | (uint32_t)__popc(mt) << 16;
   }
@@ -541,16 +686,14 @@ __global__ void __launch_bounds__(kThreads) select_block_kernel(const __grid_con
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
     if (k >= items) break;
-    const int i = kThreads * k + tid;
-    const bool sure = i < r.n && (i < lo || i >= hi || x[k] > least);
-    const bool tie = ties > 0 && i >= lo && i < hi && x[k] == least;
+    const bool sure = x[k] > least, tie = ties > 0 && x[k] == least;
     const uint32_t ms = __ballot_sync(0xffffffffu, sure), mt = __ballot_sync(0xffffffffu, tie);
     if (!(ms | mt)) continue;
     const uint32_t before = counts[k * kWarps + warp];
     const uint32_t rank = (before >> 16) + __popc(mt & below);           // ties before this page
     const uint32_t to = (before & 0xFFFFu) + __popc(ms & below) + min(rank, ties);
     if ((sure || (tie && rank < ties)) && to < (uint32_t)p.keep) {
-      const int32_t page = __ldg(table + i);
+      const int32_t page = __ldg(table + kThreads * k + tid);
       bad |= (uint32_t)page >= (uint32_t)p.num_pages[h];
       out[to] = page;
     }

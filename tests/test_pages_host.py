@@ -87,6 +87,20 @@ def test_scores_bound_the_logits():
     assert (logit <= got + slack).all()
 
 
+def test_corrected_quotients_are_the_divisions():
+    """The kernel's x / t: one correction of the product with the rounded inverse, for every pair of bf16 significands."""
+    f, wide = np.float32, np.longdouble
+    amax = np.arange(128, 256, dtype=np.float32)[:, None]
+    t = amax / f(127)
+    inv = f(1) / t
+    for e in range(12):  # (smaller numerators round to 0)
+        x = np.arange(128, 256, dtype=np.float32)[None] * f(2.0 ** -e)
+        q = x * inv
+        r = (x.astype(wide) - q.astype(wide) * t.astype(wide)).astype(f)  # (exact before its rounding, as a fused product)
+        q = (q.astype(wide) + r.astype(wide) * inv.astype(wide)).astype(f)
+        assert np.array_equal(np.where(x <= amax, q, 0), np.where(x <= amax, x / t, 0))
+
+
 def test_selection_takes_ends_and_ties():
     codes, scale = np.zeros((20, 256), np.int8), np.ones(20, np.float32)
     blocks, tokens = pages.select(np.ones((2, 128), np.float32), codes, scale, 19 * 16 + 3, 16, 6, 1, 2)
