@@ -21,6 +21,7 @@ namespace cai {
 namespace {
 
 constexpr int kSumWarps = 8;
+constexpr int kSumBlocks = 4;  // blocks of an SM
 
 __device__ __forceinline__ float fmin3(float a, float b, float c) {
   float r;
@@ -177,7 +178,7 @@ __device__ __forceinline__ void summarize_page(const SummarizeParams& p, int b, 
 
 // A warp looks through its share of the (sequence, page, K/V head) triples, 32 at a time, for those with new tokens.
 template <bool kFour>
-__global__ void __launch_bounds__(kSumWarps * 32, 4) summarize_kernel(const __grid_constant__ SummarizeParams p) {
+__global__ void __launch_bounds__(kSumWarps * 32, kSumBlocks) summarize_kernel(const __grid_constant__ SummarizeParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
   const int lane = threadIdx.x & 31;
@@ -208,8 +209,10 @@ __global__ void __launch_bounds__(kSumWarps * 32, 4) summarize_kernel(const __gr
 cudaError_t launch_summarize(SummarizeParams p, bool four, cudaStream_t stream) {
   p.groups = (int32_t)(((int64_t)p.n_new + 2 * p.page_size - 2) / p.page_size);  // from any position in a page
   const int64_t items = (int64_t)p.batch * p.groups * p.num_kv_heads;
-  const int64_t blocks = (items + kSumWarps - 1) / kSumWarps, wave = (int64_t)num_sms() * 4;
-  const dim3 grid((unsigned)std::min(blocks, wave));
+  // At most four waves of warps, each with a share of the triples: 64 dialogues of up to 8192 tokens, 4-bit, four K/V heads
+  // 32 us (one wave 37, eight 36, a warp for each triple 39); int8 likewise (23; 25, 25, 30).
+  const int64_t blocks = (items + kSumWarps - 1) / kSumWarps, wave = (int64_t)num_sms() * kSumBlocks;
+  const dim3 grid((unsigned)std::min(blocks, 4 * wave));
   return four ? launch_pdl(summarize_kernel<true>, grid, dim3(kSumWarps * 32), 0, stream, p)
               : launch_pdl(summarize_kernel<false>, grid, dim3(kSumWarps * 32), 0, stream, p);
 }
