@@ -170,7 +170,7 @@ struct Decode4Params {
   // block c and goes on in the next, {-1, -1} if nothing does.  A sequence counts piece_tiles more than it has.
   // chunk > 0: every sequence is cut into `splits` ranges of chunk keys; slot (unit * splits + range).
   int32_t head_groups, ranges, chunk, splits, piece_tiles;
-  int32_t eight;           // the int8 cache (attend8.cu): set before plan_decode4
+  int32_t eight;           // the int8 cache (lists only, attend.cu); set, as lists is, before plan_decode4
   int2* meta;
   float* ws_o;             // [slot][query heads of a K/V head][128] normalised partial outputs
   float* ws_lse;           // [slot][query heads of a K/V head] log2 units

@@ -499,7 +499,7 @@ int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
 
 size_t plan_decode4(Decode4Params& p, int32_t num_splits) {
   const int G = p.num_heads / p.num_kv_heads, tc = tensor_heads(p);
-  const int blocks = num_sms() * (tc ? 1 : kBlocks4);
+  const int blocks = num_sms() * (!tc ? kBlocks4 : p.lists ? 2 : 1);  // (lists: a range for each set of a block's warps)
   p.head_groups = tc ? (G + tc - 1) / tc : 1;
   // What the start and merge of a piece cost, in tiles, fitted from the times of blocks with different numbers of
   // tiles and pieces.  (Lognormal contexts of 32 heads: 77.5 us with one tile, 73.6 with five; 96 sequences of 8 heads:
@@ -540,7 +540,7 @@ void place_decode4(Decode4Params& p, void* workspace) {
 }
 
 cudaError_t launch_decode4(const Decode4Params& p, cudaStream_t stream) {
-  const cudaError_t e = p.eight ? launch_attend8(p, stream) : tensor_heads(p) ? launch_decode4_tc(p, stream) : launch_heads8(p, stream);
+  const cudaError_t e = !tensor_heads(p) ? launch_heads8(p, stream) : p.lists ? launch_attend(p, stream) : launch_decode4_tc(p, stream);
   if (e != cudaSuccess || (p.chunk > 0 && p.splits <= 1)) return e;
   const int64_t G = p.num_heads / p.num_kv_heads, items = p.chunk == 0 ? p.ranges : (int64_t)p.batch * p.num_kv_heads;
   return launch_pdl(combine4_kernel, dim3((unsigned)(items * ((G + kCombineHeads - 1) / kCombineHeads))),

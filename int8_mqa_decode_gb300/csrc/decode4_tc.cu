@@ -208,7 +208,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) decode4_tc_kernel(const __grid_
       for (int pi = 0; pi < count && ok; ++pi) {
         const Piece4 pc = pieces[pi];
         const int nt = piece_tiles(pc);
-        const int32_t* table = piece_table(p, pc);
+        const int32_t* table = p.table + (int64_t)pc.b * p.max_pages;
         const uint8_t* pages = p.pages[pc.kvh];
         const int num_pages = p.num_pages[pc.kvh];
         const int first = pc.start / kBlk, last = (pc.end - 1) / kBlk;  // groups of 16 keys that the piece needs

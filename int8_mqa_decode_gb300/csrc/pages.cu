@@ -67,6 +67,7 @@ size_t attend_bytes(int32_t rows, int32_t num_q_heads, int32_t num_kv_heads, int
   p.batch = rows;
   p.page_size = page_size;
   p.max_pages = width;
+  p.lists = 1;
   p.eight = eight;
   return plan_decode4(p, num_splits);
 }
