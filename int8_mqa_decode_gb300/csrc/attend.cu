@@ -167,13 +167,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0) + set * S::kSetCols;
   grid_dependency_wait();
   grid_launch_dependents();
-#pragma unroll 1
-  for (int k = 0; k < kSets; ++k) {
-    List4& list = *reinterpret_cast<List4*>(smem + S::kOffPieces + k * S::kPiecesBytes + kPieces * sizeof(Piece4));
-    if (c0 + k < p.ranges) start_list<kThreads>(p, c0 + k, list, reinterpret_cast<int64_t*>(smem + S::kOffScan));
-    else if (threadIdx.x == 0) list.more = 0;
-  }
-  __syncthreads();
+  start_lists<kThreads, kSets>(p, c0, reinterpret_cast<List4*>(smem + S::kOffPieces + kPieces * sizeof(Piece4)), S::kPiecesBytes,
+                               reinterpret_cast<int64_t*>(smem + S::kOffScan));
 
   // Tiles (gt) and pieces with tiles (gp) of the set since the start; every role keeps its own count.
   int gt = 0, gp = 0;
@@ -356,8 +351,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     setmaxnreg_dec<S::kRegsConv>();
     lists([&](int count) {
       // ------------------------------------------------------------------ converters
-      // K of the next tile goes before V of this one where V has one buffer: V may have to wait for the products that its
-      // softmax comes before.  The waits are tried a step ahead (a wait costs 150 cycles and more even when its phase is
+      // K of the next tile goes before V of this one where V has one buffer and a third raw tile is on its way: V may have to
+      // wait for the products that its softmax comes before.  The waits are tried a step ahead (a wait costs 150 cycles and more even when its phase is
       // over), and a step's stores are waited for after the next one's loads.
       // A lane whose wait gave up carries on (on garbage) and releases nothing that it did not see land; the
       // lanes agree on stopping after each tile.
@@ -378,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       constexpr int kB = S::kVBufs;  // V^T's buffer was read by PV of tile n - kB
       // (n: the tile whose V is converted, n + kAhead: K.  Loops are kept rolled: the roles' instructions together pass the
       // cache's size soon, unrolled twice as far this cost 20%.)
-      constexpr int kAhead = kB == 1 ? 1 : 0;
+      constexpr int kAhead = kB == 1 && NS > 2 ? 1 : 0;
       for (int n = gt - kAhead; n < end; ++n) {
         const int nk = n + kAhead;
         const bool has_k = nk < end, has_v = n >= gt;
@@ -732,19 +727,24 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           }
         }
         __syncwarp();
+        uint16_t* out = pc.slot < 0 ? p.out + row0 * kHeadDim + key : nullptr;
+        float* ws = p.ws_o + slot0 * kHeadDim + key;
 #pragma unroll 1
-        for (int h1 = 0; h1 < nh; h1 += 8) {
-          uint32_t r[8];
-          tmem_ld_32x32b_x8(tm + S::kColO + h1, r);
+        for (int h1 = 0; h1 < nh; h1 += 16) {
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(tm + S::kColO + h1, r);
           tmem_wait_ld();
-          const float4 fa = *reinterpret_cast<const float4*>(fac + h1), fb = *reinterpret_cast<const float4*>(fac + h1 + 4);
-          const float f[8] = {fa.x, fa.y, fa.z, fa.w, fb.x, fb.y, fb.z, fb.w};
 #pragma unroll
-          for (int h = 0; h < 8; ++h) {
-            const float x = f[h] != 0.0f ? __uint_as_float(r[h]) * f[h] : 0.0f;  // (nothing attended: whatever is there does not count)
-            if (h1 + h < nh) {
-              if (pc.slot < 0) p.out[(row0 + h1 + h) * kHeadDim + key] = (uint16_t)pack_bf16x2(x, 0.0f);
-              else p.ws_o[(slot0 + h1 + h) * kHeadDim + key] = x;
+          for (int h = 0; h < 16; h += 4) {
+            const float4 f4 = *reinterpret_cast<const float4*>(fac + h1 + h);
+            const float f[4] = {f4.x, f4.y, f4.z, f4.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float x = f[e] != 0.0f ? __uint_as_float(r[h + e]) * f[e] : 0.0f;  // (nothing attended: whatever is there does not count)
+              if (h1 + h + e < nh) {
+                if (out) out[(h1 + h + e) * kHeadDim] = (uint16_t)pack_bf16x2(x, 0.0f);
+                else ws[(h1 + h + e) * kHeadDim] = x;
+              }
             }
           }
         }

@@ -130,6 +130,74 @@ __device__ __forceinline__ void start_list(const Decode4Params& p, int c, List4&
   __syncthreads();
 }
 
+// start_list for kLists ranges c0 .. of one block at once, their lists `stride` bytes apart (those past the last range
+// stay empty): a block with several finds its place in one pass over the sequences.
+template <int kThreads, int kLists>
+__device__ __forceinline__ void start_lists(const Decode4Params& p, int c0, List4* first, int stride, int64_t* scan) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  auto list = [&](int k) -> List4& { return *reinterpret_cast<List4*>(reinterpret_cast<uint8_t*>(first) + k * stride); };
+  const bool mine_to_start = tid < kLists;
+  if (mine_to_start) {
+    list(tid).unit = c0 + tid;
+    list(tid).more = p.chunk > 0 && c0 + tid < p.ranges;
+    if (p.chunk == 0 && c0 + tid < p.ranges) p.meta[c0 + tid] = make_int2(-1, -1);
+  }
+  if (p.chunk > 0) {
+    __syncthreads();
+    return;
+  }
+  const int per = (p.batch + kThreads - 1) / kThreads;
+  const int b0 = min(p.batch, tid * per), b1 = min(p.batch, b0 + per);
+  int64_t sum = 0;
+  for (int b = b0; b < b1; b += 4) {
+    int w[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) w[u] = seq_tiles(p, min(b + u, b1 - 1));
+#pragma unroll
+    for (int u = 0; u < 4; ++u) sum += b + u < b1 ? unit_weight(p, w[u]) : 0;
+  }
+  int64_t incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) scan[warp] = incl;
+  __syncthreads();
+  int64_t before = 0, W = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += scan[w];
+    W += scan[w];
+  }
+  W *= p.num_kv_heads;
+  const int n = (int)(W < p.ranges ? W : p.ranges);  // every range gets a position
+  const int64_t mine = (before + incl - sum) * p.num_kv_heads;
+#pragma unroll 1
+  for (int k = 0; k < kLists; ++k) {
+    const int c = c0 + k;
+    if (c >= n) break;
+    const int64_t begin = quotient(W * c, n);
+    if (begin < mine || begin >= mine + sum * p.num_kv_heads) continue;  // one thread goes on
+    int64_t pos = mine;
+    int b = b0, w;
+    for (;; ++b) {
+      w = unit_weight(p, seq_tiles(p, b));
+      if (begin < pos + (int64_t)w * p.num_kv_heads) break;
+      pos += (int64_t)w * p.num_kv_heads;
+    }
+    const int kvh = (int)quotient(begin - pos, w);
+    List4& ls = list(k);
+    ls.unit = b * p.num_kv_heads + kvh;
+    ls.pos = pos + (int64_t)kvh * w;
+    ls.begin = begin;
+    ls.end = quotient(W * (c + 1), n);
+    ls.total = W;
+    ls.ranges = n;
+    ls.more = 1;
+  }
+  __syncthreads();
+}
+
 // Warp 0: the next pieces of this block, one unit (or item) per lane.
 __device__ __forceinline__ void next_pieces(const Decode4Params& p, int c, List4& ls, Piece4* list) {
   const int lane = threadIdx.x & 31;
