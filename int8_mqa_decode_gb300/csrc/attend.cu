@@ -60,7 +60,7 @@ struct Shape {
   static constexpr int kXSum = 4 * HN, kXRef = 8 * HN, kXFac = 12 * HN, kXFloats = 16 * HN;
   static constexpr int kOffTok = kOffX + kSets * kXFloats * 4;       // int8: [set][2 tiles][key] K's scale (log2 units), V's
   static constexpr int kOffBars = kOffTok + (kFour ? 0 : kSets * 2 * kT * 8);
-  static constexpr int kSetBars = 2 * kStages + 14;
+  static constexpr int kSetBars = 2 * kStages + 15;
   static constexpr int kOffInfo = (kOffBars + kSets * kSetBars * 8 + 15) & ~15;  // [set] int4 per tile
   static constexpr int kOffScan = kOffInfo + kSets * kInfo * 16;     // start_list's
   static constexpr int kOffWait = kOffScan + kThreads / 32 * 8;
@@ -122,7 +122,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   uint64_t* p_full = v_full + 2;                  // [2] softmax (4) -> issuer
   uint64_t* pv_done = p_full + 2;                 // [2] commit of PV -> softmax (P^T free), converters (V^T free)
   uint64_t* q_full = pv_done + 2;                 // [2] producer -> issuer: a piece's Q^T
-  uint64_t* o_free = q_full + 2;                  // [2] softmax (4) -> issuer, producer: a piece's O^T is read
+  uint64_t* q_raw = q_full + 2;                   // a query's bulk copy (tx bytes)
+  uint64_t* o_free = q_raw + 1;                  // [2] softmax (4) -> issuer, producer: a piece's O^T is read
   volatile int4* info = reinterpret_cast<volatile int4*>(smem + S::kOffInfo) + set * kInfo;  // tile: first and last + 1 key, groups landed
   volatile WaitState* wctl = reinterpret_cast<volatile WaitState*>(smem + S::kOffWait);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffSlot);
@@ -148,6 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     mbar_init(s_full, 1);
     mbar_init(s_read, 4);
     mbar_init(drain, 1);
+    mbar_init(q_raw, 1);
     for (int k = 0; k < 2; ++k) {
       mbar_init(&v_full[k], 4);
       mbar_init(&p_full[k], 4);
@@ -173,7 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   // Tiles (gt) and pieces with tiles (gp) of the set since the start; every role keeps its own count.
   int gt = 0, gp = 0;
   bool ok = true;  // no wait of this thread gave up
-  int issued = 0;  // producer: tiles up to this one were started
+  int issued = 0;  // producer: tiles up to this one were started,
+  int copies = 0;  // and copies of queries
 
   // Every role goes through its set's lists of pieces; `work` is its part of one.  (The roles are the outermost branch:
   // the compiler gives each the registers that its setmaxnreg names.)  A wait that gave up, in either set, stops a set at
@@ -198,15 +201,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       // ------------------------------------------------------------------ producer
       // Lane l: page l of a tile.
       const int P = p.page_size, per = P / kBlk, in_tile = kT / P;
-      // A piece's query as Q^T, in the order of K's columns.  The buffer is free once the S^T of the piece before (one
-      // buffer), or that of the one before it, are through.
-      auto write_q = [&](const Piece4& pc, int first_tile) {
-        if (S::kQBufs == 1 ? first_tile > 0 && !mbar_wait_lean_warp(s_full, (first_tile - 1) & 1, wctl)
-                           : gp > 1 && !mbar_wait_lean_warp(&o_free[gp & 1], ((gp >> 1) - 1) & 1, wctl)) {
+      // A piece's query as Q^T, in the order of K's columns.  One bulk copy brings its rows (by loads of one warp, which wait
+      // 2000 cycles each beside the tiles' copies, 64 heads took 10 k cycles) to where the first tile's P^T will be: free
+      // once PV of the tile before the last one there is done, and not written before the S^T that needs this query.
+      // Q^T's own buffer is free once the S^T of the piece before (one buffer), or that of the one before it, are through.
+      auto write_q = [&](const Piece4& pc) {
+        constexpr int kB = S::kPBufs;
+        if (S::kQBufs == 2 && gp > 1) ok = mbar_wait_lean_warp(&o_free[gp & 1], ((gp >> 1) - 1) & 1, wctl);
+        if (gt >= kB) ok = ok && mbar_wait_lean_warp(&pv_done[(gt - kB) & 1], ((gt - kB) >> 1) & 1, wctl);
+        if (S::kQBufs == 1 && gt > 0) ok = ok && mbar_wait_lean_warp(s_full, (gt - 1) & 1, wctl);
+        if (!ok) return;
+        uint8_t* src = pt + (kB == 2 ? gt & 1 : 0) * S::kPBytes;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(q_raw, (uint32_t)nh * kHeadDim * 2);
+          bulk_g2s(src, p.q + ((int64_t)pc.row * p.num_heads + (int64_t)pc.kvh * G + h0) * kHeadDim, (uint32_t)nh * kHeadDim * 2, q_raw);
+        }
+        __syncwarp();
+        const uint32_t phase = copies++ & 1;
+        if (!mbar_wait_lean_warp(q_raw, phase, wctl)) {
           ok = false;
           return;
         }
-        const uint16_t* q = p.q + ((int64_t)pc.row * p.num_heads + (int64_t)pc.kvh * G + h0) * kHeadDim;
         uint8_t* dst = qt + (S::kQBufs == 2 ? gp & 1 : 0) * S::kQBytes;
 #pragma unroll 4
         for (int u = lane; u < HN * 16; u += 32) {
@@ -214,16 +229,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             // Word t of 16-byte unit 4 j + i of a head holds channels 32 j + 8 t + 2 i, + 1.
             const int t = u & 3, j = u >> 5 & 3, h = (u >> 2 & 7) | (u >> 7 << 3);
             uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (h < nh) x = __ldg(reinterpret_cast<const uint4*>(q + h * kHeadDim + 32 * j + 8 * t));
+            if (h < nh) x = *reinterpret_cast<const uint4*>(src + h * 256 + 64 * j + 16 * t);
             uint32_t* y = reinterpret_cast<uint32_t*>(dst + (h >> 3) * 2048 + j * 512 + (h & 7) * 16 + t * 4);
             y[0] = bf16x2_to_f16x2(x.x);
             y[32] = bf16x2_to_f16x2(x.y);
             y[64] = bf16x2_to_f16x2(x.z);
             y[96] = bf16x2_to_f16x2(x.w);
           } else {
-            const int h = (u & 7) | (u >> 7 << 3), c8 = u >> 3 & 15;  // eight channels a unit
+            // Eight channels a unit; eight lanes take a diagonal of heads and units (banks of both sides).
+            const int h = (u & 7) | (u >> 7 << 3), c8 = ((u + (u >> 3)) & 7) | (u >> 3 & 8);
             uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (h < nh) x = __ldg(reinterpret_cast<const uint4*>(q + h * kHeadDim + 8 * c8));
+            if (h < nh) x = *reinterpret_cast<const uint4*>(src + h * 256 + 16 * c8);
             *reinterpret_cast<uint4*>(dst + (h >> 3) * 2048 + c8 * 128 + (h & 7) * 16) =
                 make_uint4(bf16x2_to_f16x2(x.x), bf16x2_to_f16x2(x.y), bf16x2_to_f16x2(x.z), bf16x2_to_f16x2(x.w));
           }
@@ -252,6 +268,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           return t < nt && lo < hi ? __ldg(table + ((pc.start / kT + t) * kT / P + lane)) : -1;
         };
         int32_t id_next = load_id(0);
+        // The query goes behind the copies of the tiles that have stages: all of them at the start, two ahead of the
+        // products later.
+        const int at_q = min(gp == 0 ? NS - 1 : NS - 2, nt - 1);
         for (int t = 0; t < nt; ++t) {
           const int x = gt + t, s = x % NS;
           const int32_t id = id_next;
@@ -289,9 +308,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
               }
             }
           }
-          // The query goes behind the piece's first copies.
-          if (t == 0) {
-            write_q(pc, gt);
+          if (t == at_q) {
+            write_q(pc);
             if (!ok) break;
           }
         }
@@ -561,13 +579,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             lv2 = f2(lv, lv);
             iv2 = f2(iv, iv);
           }
-          // Logits minus references of 16 heads, from S^T (which stays in tensor memory until the set says it is read).
-          auto logits16 = [&](int h1, float* z) {
-            uint32_t r[16];
-            tmem_ld_32x32b_x16(tm + S::kColS + h1, r);
-            tmem_wait_ld();
+          // Logits minus references of N heads, from S^T's columns r (S^T stays in tensor memory until the set says it is read).
+          auto logits = [&](auto& r, int h1, float* z) {
+            constexpr int N = sizeof(r) / 4;
 #pragma unroll
-            for (int h = 0; h < 16; h += 4) {
+            for (int h = 0; h < N; h += 4) {
               const float4 x4 = *reinterpret_cast<const float4*>(nref + h1 + h);
               uint64_t a = f2_fma(f2(__uint_as_float(r[h]), __uint_as_float(r[h + 1])), ks2, f2(x4.x, x4.y));
               uint64_t b = f2_fma(f2(__uint_as_float(r[h + 2]), __uint_as_float(r[h + 3])), ks2, f2(x4.z, x4.w));
@@ -580,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             }
             if (edge) {
 #pragma unroll
-              for (int h = 0; h < 16; ++h) z[h] = valid ? z[h] : -INFINITY;
+              for (int h = 0; h < N; ++h) z[h] = valid ? z[h] : -INFINITY;
             }
           };
           float sv[HN];
@@ -594,7 +610,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
 #pragma unroll 1
               for (int h1 = 0; h1 < HN; h1 += 16) {
                 float z[16], mine = -INFINITY;
-                logits16(h1, z);
+                uint32_t r[16];
+                tmem_ld_32x32b_x16(tm + S::kColS + h1, r);
+                tmem_wait_ld();
+                logits(r, h1, z);
 #pragma unroll
                 for (int h = 0; h < 16; ++h) {
                   float m;
@@ -644,8 +663,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
               have_ref = have_ref || any;
             }
             float mx = -INFINITY;
+            {
+              constexpr int N = HN < 32 ? HN : 32;
+              uint32_t r[HN / N][N];
 #pragma unroll
-            for (int h1 = 0; h1 < HN; h1 += 16) logits16(h1, sv + h1);
+              for (int i = 0; i < HN / N; ++i) {
+                if constexpr (N == 32) tmem_ld_32x32b_x32(tm + S::kColS + i * N, r[i]);
+                else tmem_ld_32x32b_x16(tm + S::kColS + i * N, r[i]);
+              }
+              tmem_wait_ld();
+#pragma unroll
+              for (int i = 0; i < HN / N; ++i) logits(r[i], i * N, sv + i * N);
+            }
 #pragma unroll
             for (int h = 0; h < HN; h += 2) mx = fmax3(mx, sv[h], sv[h + 1]);
             // P^T's buffer is free once PV of tile n - kPBufs is done.
@@ -762,6 +791,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   if (warp < kSets) {
     for (int x = max(0, issued - NS); x < issued; ++x)
       if (x != p.drop_stage) mbar_wait_drain(&raw_full[x % NS], (x / NS) & 1);
+    if (copies > 0) mbar_wait_drain(q_raw, (copies - 1) & 1);
   } else if (warp < kConv0) {
     if (elect_one()) mma_commit(drain);
     __syncwarp();
