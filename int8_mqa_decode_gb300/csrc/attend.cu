@@ -803,6 +803,80 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   if (warp == 0) tmem_dealloc(tmem, 512);  // (set 0's is the first column)
 }
 
+// The pieces' normalised outputs merged by their log2-sum-exp: as combine4_kernel (at most one row and K/V head starts in a
+// range and goes on into the next, so there is an item per range), for the few pieces that a list has: a warp takes two
+// heads and all of their pieces, a block 16 heads.  (With its four warps a head and two heads a block 64 heads took 15 us
+// here, most of it the start of 9728 blocks.)
+constexpr int kMergeWarps = 8, kMergeHeads = 2;
+__global__ void __launch_bounds__(32 * kMergeWarps) merge_kernel(const __grid_constant__ Decode4Params p) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int G = p.num_heads / p.num_kv_heads, groups = (G + kMergeWarps * kMergeHeads - 1) / (kMergeWarps * kMergeHeads);
+  const int item = blockIdx.x / groups, h0 = ((blockIdx.x - item * groups) * kMergeWarps + warp) * kMergeHeads;
+  grid_dependency_wait();
+  grid_launch_dependents();
+  int unit = item, n = 0;
+  if (p.chunk == 0) {
+    const int2 m = p.meta[item];  // the unit, and the last range with a piece of it
+    if (m.x < 0) return;
+    unit = m.x;
+    n = m.y - item + 1;
+  }
+  const int b = unit / p.num_kv_heads, kvh = unit - b * p.num_kv_heads;
+  int32_t row;
+  SeqSplits sp;
+  if (!seq_keys(p, b, row, sp)) return;
+  if (p.chunk > 0) n = sp.nsplit;
+  if (n <= 1 || h0 >= G) return;  // written by the attention kernel
+  auto slot = [&](int j) -> int64_t {
+    return (p.chunk > 0 ? (int64_t)unit * p.splits + j : 2ll * (item + j) + (j == 0 ? 1 : 0)) * G + h0;
+  };
+  float M[kMergeHeads], sum[kMergeHeads];
+  float4 acc[kMergeHeads];
+#pragma unroll
+  for (int k = 0; k < kMergeHeads; ++k) M[k] = -INFINITY, sum[k] = 0.0f, acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int j0 = 0; j0 < n; j0 += 4) {
+    float4 x[4][kMergeHeads];
+    float l[4][kMergeHeads];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int64_t at = j0 + u < n ? slot(j0 + u) : 0;
+#pragma unroll
+      for (int k = 0; k < kMergeHeads; ++k) {
+        const bool have = j0 + u < n && h0 + k < G;
+        l[u][k] = have ? p.ws_lse[at + k] : -INFINITY;
+        x[u][k] = have ? reinterpret_cast<const float4*>(p.ws_o + (at + k) * kHeadDim)[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kMergeHeads; ++k) {
+      const float m = fmaxf(fmaxf(fmaxf(l[0][k], l[1][k]), fmaxf(l[2][k], l[3][k])), M[k]);
+      if (m == -INFINITY) continue;
+      const float f = ex2_approx(M[k] - m);
+      M[k] = m;
+      sum[k] *= f;
+      acc[k] = make_float4(acc[k].x * f, acc[k].y * f, acc[k].z * f, acc[k].w * f);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const float w = ex2_approx(l[u][k] - m);
+        sum[k] += w;
+        acc[k].x = fmaf(w, x[u][k].x, acc[k].x);
+        acc[k].y = fmaf(w, x[u][k].y, acc[k].y);
+        acc[k].z = fmaf(w, x[u][k].z, acc[k].z);
+        acc[k].w = fmaf(w, x[u][k].w, acc[k].w);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kMergeHeads; ++k) {
+    if (h0 + k >= G) break;
+    const float inv = sum[k] > 0.0f ? 1.0f / sum[k] : 0.0f;
+    const int64_t at = (int64_t)row * p.num_heads + kvh * G + h0 + k;
+    reinterpret_cast<uint2*>(p.out + at * kHeadDim)[lane] =
+        make_uint2(pack_bf16x2(acc[k].x * inv, acc[k].y * inv), pack_bf16x2(acc[k].z * inv, acc[k].w * inv));
+    if (p.lse_out && lane == 0) p.lse_out[at] = sum[k] > 0.0f ? (M[k] + log2f(sum[k])) * kLn2 : -INFINITY;
+  }
+}
+
 template <bool kFour, int HN>
 cudaError_t launch_hn(const Decode4Params& p, cudaStream_t stream) {
   using S = Shape<kFour, HN>;
@@ -836,6 +910,12 @@ cudaError_t launch_heads(const Decode4Params& p, cudaStream_t stream) {
 
 cudaError_t launch_attend(const Decode4Params& p, cudaStream_t stream) {
   return p.eight ? launch_heads<false>(p, stream) : launch_heads<true>(p, stream);
+}
+
+cudaError_t launch_merge(const Decode4Params& p, cudaStream_t stream) {
+  const int G = p.num_heads / p.num_kv_heads, groups = (G + kMergeWarps * kMergeHeads - 1) / (kMergeWarps * kMergeHeads);
+  const int64_t items = p.chunk == 0 ? p.ranges : (int64_t)p.batch * p.num_kv_heads;
+  return launch_pdl(merge_kernel, dim3((unsigned)(items * groups)), dim3(32 * kMergeWarps), 0, stream, p);
 }
 
 }  // namespace cai

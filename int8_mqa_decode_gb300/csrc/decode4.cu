@@ -542,6 +542,7 @@ void place_decode4(Decode4Params& p, void* workspace) {
 cudaError_t launch_decode4(const Decode4Params& p, cudaStream_t stream) {
   const cudaError_t e = !tensor_heads(p) ? launch_heads8(p, stream) : p.lists ? launch_attend(p, stream) : launch_decode4_tc(p, stream);
   if (e != cudaSuccess || (p.chunk > 0 && p.splits <= 1)) return e;
+  if (p.lists) return launch_merge(p, stream);
   const int64_t G = p.num_heads / p.num_kv_heads, items = p.chunk == 0 ? p.ranges : (int64_t)p.batch * p.num_kv_heads;
   return launch_pdl(combine4_kernel, dim3((unsigned)(items * ((G + kCombineHeads - 1) / kCombineHeads))),
                     dim3(kCombineWarps * kCombineHeads * 32), 0, stream, p);

@@ -277,6 +277,7 @@ __device__ __forceinline__ void next_pieces(const Decode4Params& p, int c, List4
 int decode4_tc_heads(int group);   // query heads per block of the tcgen05 kernel (0: the group is not its)
 cudaError_t launch_decode4_tc(const Decode4Params& p, cudaStream_t stream);
 cudaError_t launch_attend(const Decode4Params& p, cudaStream_t stream);  // (attend.cu: lists of pages; int8, any group)
+cudaError_t launch_merge(const Decode4Params& p, cudaStream_t stream);   // (its pieces' merge, for any lists)
 inline int tensor_heads(const Decode4Params& p) {
   const int G = p.num_heads / p.num_kv_heads;
   return p.eight && G <= 8 ? 16 : decode4_tc_heads(G);
