@@ -173,15 +173,18 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
   // last head, columns past the rows are 0.
   const int G = p.num_q_heads / p.num_kv_heads, gp = padded_heads(G);
   const int used = (rt.n * gp + 15) / 16 * 16;
-  for (int n0 = 8 * warp; n0 < used; n0 += 8 * kWarps) {
+  uint4 w[2][2];
+  const auto load_q = [&](int n0) {
     const int n = n0 + g, i = n / gp, head = min(n - i * gp, G - 1);
-    uint4 w[2][2];
+    const uint4* q = reinterpret_cast<const uint4*>(p.q + ((rt.row0 + i) * p.num_q_heads + h * G + head) * kHeadDim + 16 * t4);
 #pragma unroll
     for (int c = 0; c < 2; ++c)
 #pragma unroll
-      for (int k = 0; k < 2; ++k)
-        w[c][k] = i < rt.n ? __ldg(reinterpret_cast<const uint4*>(p.q + ((rt.row0 + i) * p.num_q_heads + h * G + head) * kHeadDim + 64 * c + 16 * t4) + k)
-                           : make_uint4(0u, 0u, 0u, 0u);
+      for (int k = 0; k < 2; ++k) w[c][k] = n0 < used && i < rt.n ? __ldg(q + 8 * c + k) : make_uint4(0u, 0u, 0u, 0u);
+  };
+  load_q(8 * warp);
+  for (int n0 = 8 * warp; n0 < used; n0 += 8 * kWarps) {
+    const int n = n0 + g, i = n / gp, head = min(n - i * gp, G - 1);
     float y[32], amax = 0.0f;
 #pragma unroll
     for (int x = 0; x < 16; ++x) {
@@ -191,6 +194,7 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
       y[2 * x + 1] = __uint_as_float(u & 0xFFFF0000u);
       amax = fmax3(amax, fabsf(y[2 * x]), fabsf(y[2 * x + 1]));
     }
+    load_q(n0 + 8 * kWarps);  // (under way while these are turned)
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
     amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
     // x / t as the IEEE division rounds it, by one correction of the product with the rounded inverse (Markstein, 1990);
