@@ -149,24 +149,31 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
   const int32_t* table = p.table + (int64_t)rt.b * p.max_pages;
   const uint8_t* data = p.data[h];
   const float* scales = reinterpret_cast<const float*>(data + (int64_t)p.num_pages[h] * (2 * kHeadDim));
-  const auto page_of = [&](int blk) -> int32_t {
-    const int32_t page = blk < c1 ? __ldg(table + blk) : 0;
-    return (uint32_t)page < (uint32_t)p.num_pages[h] ? page : -1;
-  };
-  // This lane's 64 codes, 16 of every 64, of pages (quarter, half) 16 + g and + 8 of a tile.
+  const auto page_of = [&](int blk) -> int32_t { return blk < c1 ? __ldg(table + blk) : 0; };
+  const auto in_pool = [&](int32_t page) { return (uint32_t)page < (uint32_t)p.num_pages[h]; };
+  // This lane's 64 codes, 16 of every 64, of pages (quarter, half) 16 + g and + 8 of a tile; their ids are loaded a tile ahead
+  // of the codes, these a tile ahead of their use.
   uint4 a[2][4];
-  const auto there = [&](int base) { return base + 32 * quarter + 16 * half < c1; };  // (this warp has pages of the tile)
+  int32_t id[2];
+  const int first = 32 * quarter + 16 * half;
+  const auto there = [&](int base) { return base + first < c1; };  // (this warp has pages of the tile)
+  const auto load_ids = [&](int base) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) id[r] = page_of(base + first + g + 8 * r);
+  };
   const auto load = [&](int base) {
     if (!there(base)) return;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      const int32_t page = page_of(base + 32 * quarter + 16 * half + g + 8 * r);
-      const uint4* row = reinterpret_cast<const uint4*>(data + (int64_t)max(page, 0) * (2 * kHeadDim)) + t4;
+      const uint4* row = reinterpret_cast<const uint4*>(data + (int64_t)(in_pool(id[r]) ? id[r] : 0) * (2 * kHeadDim)) + t4;
 #pragma unroll
       for (int c = 0; c < 4; ++c) a[r][c] = __ldg(row + 4 * c);
     }
   };
+  load_ids(c0);
+  int32_t page_next = page_of(c0 + 32 * quarter + lane);  // of this thread's page of D
   load(c0);
+  load_ids(c0 + kTilePages);
 
   // Columns: whole numbers of the rows' heads, eight columns a warp, lane (g, t) channels 64 c + 16 t .. + 15 of column g: they
   // stand at words t of units 8 c + e (q+) and 16 + 8 c + e (q-).  A group that does not fill its columns repeats its
@@ -236,6 +243,12 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
   bool ok = true;
   int phase = 0;
   for (int base = c0; base < c1; base += kTilePages, phase ^= 1) {
+    const int blk = base + 32 * quarter + lane;  // this thread's page of D
+    const int32_t page = page_next;
+    const bool good = in_pool(page);
+    const float s = good ? __ldg(scales + page) : 0.0f;
+    if (!good && half == 0 && p.err) atomicOr(p.err, CAI_DEVERR_PAGE);
+    page_next = page_of(blk + kTilePages);
     // ---- A: column 32 c + 4 e + t holds channels 64 c + 16 t + 2 e, + 1 of the 256 codes.  (Rows of pages that are not
     // there keep what they held: D's rows are independent.)
 #pragma unroll
@@ -262,11 +275,8 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
       }
       __syncwarp();
     }
-    const int blk = base + 32 * quarter + lane;  // this thread's page of D
-    const int32_t page = page_of(blk);
-    const float s = page >= 0 ? __ldg(scales + page) : 0.0f;
-    if (page < 0 && half == 0 && p.err) atomicOr(p.err, CAI_DEVERR_PAGE);
     load(base + kTilePages);
+    load_ids(base + 2 * kTilePages);
     ok = mbar_wait_lean(&done, phase, wctl) && ok;
     __syncwarp();
     tc_fence_after();
@@ -274,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
     const auto put = [&](int i, float best) {
       if (i < rt.n && blk < c1)
         p.scores[((rt.row0 + i) * p.num_kv_heads + h) * p.stride + blk] =
-            page >= 0 ? __fadd_rn(__fmul_rn(best, s), 0.0f) : -INFINITY;  // (-0 becomes 0)
+            good ? __fadd_rn(__fmul_rn(best, s), 0.0f) : -INFINITY;  // (-0 becomes 0)
     };
     if (base + 32 * quarter >= c1) {
     } else if ((gp & 31) == 0) {
