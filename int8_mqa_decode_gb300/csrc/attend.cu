@@ -60,7 +60,7 @@ struct Shape {
   static constexpr int kXSum = 4 * HN, kXRef = 8 * HN, kXFac = 12 * HN, kXFloats = 16 * HN;
   static constexpr int kOffTok = kOffX + kSets * kXFloats * 4;       // int8: [set][2 tiles][key] K's scale (log2 units), V's
   static constexpr int kOffBars = kOffTok + (kFour ? 0 : kSets * 2 * kT * 8);
-  static constexpr int kSetBars = 2 * kStages + 15;
+  static constexpr int kSetBars = 2 * kStages + 16;
   static constexpr int kOffInfo = (kOffBars + kSets * kSetBars * 8 + 15) & ~15;  // [set] int4 per tile
   static constexpr int kOffScan = kOffInfo + kSets * kInfo * 16;     // start_list's
   static constexpr int kOffWait = kOffScan + kThreads / 32 * 8;
@@ -123,7 +123,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   uint64_t* pv_done = p_full + 2;                 // [2] commit of PV -> softmax (P^T free), converters (V^T free)
   uint64_t* q_full = pv_done + 2;                 // [2] producer -> issuer: a piece's Q^T
   uint64_t* q_raw = q_full + 2;                   // a query's bulk copy (tx bytes)
-  uint64_t* o_free = q_raw + 1;                  // [2] softmax (4) -> issuer, producer: a piece's O^T is read
+  uint64_t* q_room = q_raw + 1;                   // commit near a piece's end -> producer
+  uint64_t* o_free = q_room + 1;                  // [2] softmax (4) -> issuer: a piece's O^T is read
   volatile int4* info = reinterpret_cast<volatile int4*>(smem + S::kOffInfo) + set * kInfo;  // tile: first and last + 1 key, groups landed
   volatile WaitState* wctl = reinterpret_cast<volatile WaitState*>(smem + S::kOffWait);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + S::kOffSlot);
@@ -150,6 +151,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     mbar_init(s_read, 4);
     mbar_init(drain, 1);
     mbar_init(q_raw, 1);
+    mbar_init(q_room, 1);
     for (int k = 0; k < 2; ++k) {
       mbar_init(&v_full[k], 4);
       mbar_init(&p_full[k], 4);
@@ -202,16 +204,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       // Lane l: page l of a tile.
       const int P = p.page_size, per = P / kBlk, in_tile = kT / P;
       // A piece's query as Q^T, in the order of K's columns.  One bulk copy brings its rows (by loads of one warp, which wait
-      // 2000 cycles each beside the tiles' copies, 64 heads took 10 k cycles) to where the first tile's P^T will be: free
-      // once PV of the tile before the last one there is done, and not written before the S^T that needs this query.
-      // Q^T's own buffer is free once the S^T of the piece before (one buffer), or that of the one before it, are through.
+      // 2000 cycles each beside the tiles' copies, 64 heads took 10 k cycles) to where the first tile's P^T will be, which
+      // is not written before the S^T that needs this query.  That place and Q^T's buffer are free when the issuer says so
+      // for the piece before, whose phase this warp has not passed: a parity names the last phase or the one before, so
+      // the tiles' own barriers, of which several phases may pass between two pieces, would not do.
       auto write_q = [&](const Piece4& pc) {
-        constexpr int kB = S::kPBufs;
-        if (S::kQBufs == 2 && gp > 1) ok = mbar_wait_lean_warp(&o_free[gp & 1], ((gp >> 1) - 1) & 1, wctl);
-        if (gt >= kB) ok = ok && mbar_wait_lean_warp(&pv_done[(gt - kB) & 1], ((gt - kB) >> 1) & 1, wctl);
-        if (S::kQBufs == 1 && gt > 0) ok = ok && mbar_wait_lean_warp(s_full, (gt - 1) & 1, wctl);
-        if (!ok) return;
-        uint8_t* src = pt + (kB == 2 ? gt & 1 : 0) * S::kPBytes;
+        if (gp > 0 && !mbar_wait_lean_warp(q_room, (gp - 1) & 1, wctl)) {
+          ok = false;
+          return;
+        }
+        uint8_t* src = pt + (S::kPBufs == 2 ? gt & 1 : 0) * S::kPBytes;
         if (lane == 0) {
           mbar_arrive_expect_tx(q_raw, (uint32_t)nh * kHeadDim * 2);
           bulk_g2s(src, p.q + ((int64_t)pc.row * p.num_heads + (int64_t)pc.kvh * G + h0) * kHeadDim, (uint32_t)nh * kHeadDim * 2, q_raw);
@@ -336,6 +338,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         }
         __syncwarp();
       };
+      auto say_room = [&]() {
+        if (elect_one()) mma_commit(q_room);
+        __syncwarp();
+      };
       auto issue_pv = [&](int n, bool first) {
         const int k2 = n & 1;
         // (the piece's first PV starts the accumulator, once the last piece's has been read)
@@ -358,7 +364,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         issue_s(gt, true);
         for (int t = 0; t < nt && ok; ++t) {
           if (t + 1 < nt) issue_s(gt + t + 1, false);
+          // Once the products so far are done the next piece's query may come: all S^T of this piece are among them, and
+          // every PV but the last, or (one P^T buffer) that, too.
+          if (S::kPBufs == 2 && t == nt - 1 && ok) say_room();
           if (ok) issue_pv(gt + t, t == 0);
+          if (S::kPBufs == 1 && t == nt - 1 && ok) say_room();
         }
         gt += nt;
         ++gp;

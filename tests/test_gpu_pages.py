@@ -386,6 +386,46 @@ def test_attend_many_rows(four, g):
         assert np.array_equal(out, again[0]) and np.array_equal(lse, again[1])
 
 
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("g", [6, 16, 32, 64])
+@pytest.mark.parametrize("most", [300, 1500])
+def test_attend_more_rows_than_the_chip_takes_at_once(four, g, most):
+    """Rows of one tile and of many in turn, several to a block, cut wherever the blocks' shares end: every row against
+    a plain 64-bit formulation, and the same bits again."""
+    rng = np.random.default_rng(g)
+    d = Dialogues(four, [2000], 1, 16, seed=g)
+    rows, width = 1300, -(-most // 16)
+    lens = rng.integers(1, most + 1, rows)
+    lens[::3] = rng.integers(1, 200, len(lens[::3]))
+    lists = rng.choice(d.table_np[0, :125], (rows, 1, width))
+    q = dev(rng.normal(size=(rows, g, 128)).astype(np.float32), torch.bfloat16)
+    out, lse = attend(d, q, lists, lens)
+    k, v = (dev(x[0].reshape(-1, 128)) for x in page_values(d))
+    k, v = (torch.nan_to_num(x) for x in (k, v))
+    ids, t = dev(lists[:, 0]), torch.arange(width * 16, device=DEV)
+    n = dev(lens)
+    for a in range(0, rows, 100):
+        r = slice(a, min(rows, a + 100))
+        at = ids[r][:, t // 16] * 16 + t % 16
+        kk, vv, seen = k[at], v[at], t < n[r, None]
+        qd = q[r].double()
+        z = torch.einsum("rhd,rtd->rht", qd, kk) * SCALE
+        z = torch.where(seen[:, None], z, torch.full_like(z, -np.inf))
+        p = torch.softmax(z, -1)
+        ref, soft = torch.einsum("rht,rtd->rhd", p, vv), torch.einsum("rht,rtd->rhd", p, vv.abs())
+        top = torch.where(seen[..., None], vv.abs(), torch.zeros_like(vv)).amax((1, 2))[:, None, None]
+        bound = 2.0 ** -8 * ref.abs() + (1 + 2.0 ** -8) * ((2.0 ** -11 + 2.0 ** -12) * soft + n[r, None, None] * 2.0 ** -32 * top)
+        err = (dev(out[r]).double() - ref).abs()
+        bad = (err > bound).any(-1).any(-1).nonzero()[:, 0].tolist()
+        assert not bad, [(a + i, int(lens[a + i])) for i in bad]
+        rl = torch.logsumexp(z, -1)
+        big = (torch.einsum("rhd,rtd->rht", qd.abs(), kk.abs()) * SCALE * seen[:, None]).amax(-1)
+        lv = 0.0 if four else 20.0  # (|log2| of V's scales here, at most)
+        assert ((dev(lse[r]).double() - rl).abs() <= 2.0 ** -20 * (big + 1 + rl.abs() + lv)).all()
+    again = attend(d, q, lists, lens, poison=0)
+    assert np.array_equal(out, again[0]) and np.array_equal(lse, again[1])
+
+
 def test_attend_whole_contexts_is_the_decode():
     """Lists of all pages of a 4-bit context give what the decode gives: both within the bounds (their sums are cut
     differently, so not to the bit)."""
