@@ -490,7 +490,9 @@ size_t cai_kv_summary_bytes(int32_t num_pages, int32_t head_dim);
  * min(127, ceil(hi_c / s)) and max(-127, floor(lo_c / s)); all 0 when s is 0.
  *   kv_pools, summaries   host arrays [num_kv_heads], of the same page counts
  *   n_new, q_offsets      as for the append; q_offsets[batch] is not limited here
- * Bad positions, page ids and offsets as in cai_kv_append_rope; other summaries are not touched. */
+ * Sequences of one call that share a page must have the same number of its tokens (shared
+ * prefixes have whole pages).  Bad positions, page ids and offsets as in cai_kv_append_rope; other
+ * summaries are not touched. */
 cai_status cai_kv_summarize(const cai_kv_pool* kv_pools, const cai_kv_summary* summaries, int32_t num_kv_heads,
                             int32_t batch, int32_t n_new, const int32_t* q_offsets, const int32_t* block_table,
                             int32_t max_pages_per_seq, const int32_t* start_pos, int32_t* err_flag, void* stream);

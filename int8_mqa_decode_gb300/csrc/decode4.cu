@@ -504,7 +504,8 @@ size_t plan_decode4(Decode4Params& p, int32_t num_splits) {
   // What the start and merge of a piece cost, in tiles, fitted from the times of blocks with different numbers of
   // tiles and pieces.  (Lognormal contexts of 32 heads: 77.5 us with one tile, 73.6 with five; 96 sequences of 8 heads:
   // 195 us with two, 198 with one, 197 with four; 1024 short ones 119, 120, 135.)
-  p.piece_tiles = tc == 0 ? 2 : tc == 16 ? 4 : tc == 32 ? 5 : 8;
+  // (Lists: 1 to 12 tiles are within 3% of each other.)
+  p.piece_tiles = tc == 0 ? 2 : tc == 16 || p.lists ? 4 : tc == 32 ? 5 : 8;
   const int64_t units = (int64_t)p.batch * p.num_kv_heads;
   const int64_t cap = (int64_t)p.max_pages * p.page_size;
   const int64_t span = p.window > 0 && p.window < cap ? p.window : cap;

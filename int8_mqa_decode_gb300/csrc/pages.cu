@@ -154,6 +154,7 @@ cai_status cai_kv_select(const cai_kv_summary* summaries, int32_t num_kv_heads, 
   st = check_rows(batch, n_new, q_offsets, total_new, max_pages_per_seq, summaries[0].page_size, &rows);
   if (st != CAI_OK) return st;
   if ((int64_t)num_selected * summaries[0].page_size > (1ll << 30)) return CAI_ERR_UNSUPPORTED;
+  if ((rows + batch) * num_kv_heads > 2147483647ll) return CAI_ERR_UNSUPPORTED;  // blocks of a launch
   if (rows == 0) return CAI_OK;
   if (!q || !block_table || !start_pos || !pages_out || !len_out || !aligned16(q)) return CAI_ERR_INVALID_ARG;
   const size_t need = cai_kv_select_workspace_size(batch, (int32_t)rows, num_q_heads, num_kv_heads, max_pages_per_seq);

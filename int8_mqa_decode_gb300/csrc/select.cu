@@ -13,6 +13,12 @@
 // the columns' channels follows), one lane issues the products, and while they run the next tile's codes are on their
 // way; then a thread has a page and all columns, and takes the largest of each query row.  Two blocks share an SM, one
 // converting while the other's products run.
+//
+// Measured: 4096 rows of 32 heads over 528 pages 70 us, of them 60 the scores, 2000 cycles a tile of 128 columns: the
+// products take 1024 of them (64 cycles for M = N = 128, K = 16), the conversion 560, reading D 950, and two blocks
+// overlap them in part; 64 rows of 64 heads over 256 to 2048 pages 20 us, mostly latencies.  A persistent block with a
+// kind of warp for each of these steps took 58 us and 21, and contexts of middle length 51 us instead of 37: its readers of
+// D, with 80 registers a thread, became the longest step.
 #include <algorithm>
 
 #include "ptx.cuh"
