@@ -464,7 +464,9 @@ cai_status cai_kv4_prefill(const cai_kv4_pool* kv_pools, int32_t num_kv_heads, c
  * largest logits; cai_kv_attend_pages attends over the listed pages.  A decode step is
  * append, summarize, select, attend, each on the same block tables; a chunk of n_new tokens a
  * sequence is the same calls, every row with lists of its own.  Rows are given as in the
- * section on rotated appends (n_new a sequence, or packed by q_offsets). */
+ * section on rotated appends (n_new a sequence, or packed by q_offsets); a call with batch or
+ * n_new 0 does nothing.  Queries and cached keys are finite numbers: a query that is not selects any
+ * pages and gives its head any output, and does nothing to other heads and rows. */
 
 /* Summaries of one pool's pages: `data` holds int8 [num_pages][256], page by page the codes of
  * the 128 channels' largest keys and of their smallest, then fp32 [num_pages], the scales.  It
@@ -517,6 +519,7 @@ cai_status cai_kv4_summarize(const cai_kv4_pool* kv_pools, const cai_kv_summary*
  *   workspace     cai_kv_select_workspace_size() bytes for the call's rows (batch * n_new, or
  *                 total_new), 256-byte aligned; no preparation.  Calls that share it must not
  *                 overlap on the GPU
+ *   limits        (rows + batch) * num_kv_heads below 2^31
  *   pages_out     int32 [rows][num_kv_heads][num_selected]: page ids in the order of positions, -1
  *                 behind the last
  *   len_out       int32 [rows]: the tokens of these lists, the same for all K/V heads: all pages

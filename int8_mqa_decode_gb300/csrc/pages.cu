@@ -31,7 +31,8 @@ cai_status summarize(const Pool* pools, const cai_kv_summary* summaries, int32_t
     if (summaries[j].num_pages != pools[j].num_pages || summaries[j].page_size != pools[j].page_size)
       return CAI_ERR_INVALID_ARG;
   int64_t rows;
-  st = check_rows(batch, n_new, nullptr, 0, max_pages_per_seq, pools[0].page_size, &rows);
+  // (Packed, n_new may be a loose bound: the rows that a call may have, not batch * n_new, are limited.)
+  st = check_rows(batch, n_new, q_offsets, 1 << 30, max_pages_per_seq, pools[0].page_size, &rows);
   if (st != CAI_OK || rows == 0) return st;
   if (!block_table || !start_pos) return CAI_ERR_INVALID_ARG;
   SummarizeParams p = {};
