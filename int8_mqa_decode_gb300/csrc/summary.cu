@@ -7,10 +7,12 @@
 // result is the same bits however the work is split.
 //
 // A page is computed anew from the cache whenever a token is added to it, so a summary never holds what an earlier
-// owner of the page wrote.  Bound by HBM where whole dialogues are summarized (the keys, half of the cache's bytes, are
-// read once), by latency for the one page of a decode step.  A warp has a page of one K/V head: int8, a lane four
-// channels and 16 tokens' words under way at a time; 4-bit, a lane eight channels of every other token, in fp16 pairs.
-// A page that is not full reads its last token again in place of those that are not there.
+// owner of the page wrote.  Bound by instructions where whole dialogues are summarized (the keys, half of the cache's
+// bytes, are read once: 64 dialogues of up to 8192 tokens, pages of 32, four K/V heads, 4-bit, 24 us, 49 MB at 2.1 TB/s, 850
+// warp instructions a page of which the conversion and the minima take 400), by latency for the one page of a decode
+// step (2.7 us).  A warp has a page of one K/V head: int8, a lane four channels and 16 tokens' words under way at a time;
+// 4-bit, a lane eight channels of every other token, in fp16 pairs.  A page that is not full reads its last token
+// again in place of those that are not there.
 #include <algorithm>
 
 #include "kv4.cuh"
@@ -21,7 +23,7 @@ namespace cai {
 namespace {
 
 constexpr int kSumWarps = 8;
-constexpr int kSumBlocks = 4;  // blocks of an SM
+constexpr int kSumBlocks = 5;  // blocks of an SM
 
 __device__ __forceinline__ float fmin3(float a, float b, float c) {
   float r;
@@ -39,9 +41,58 @@ __device__ __forceinline__ uint32_t hmin2(uint32_t a, uint32_t b) {
   return y;
 }
 
-// Codes of a bound x under scale s > 0, away from the other bound.
-__device__ __forceinline__ uint32_t code_up(float x, float s) { return (uint32_t)min(127, __float2int_ru(__fdiv_rn(x, s))) & 0xFFu; }
-__device__ __forceinline__ uint32_t code_down(float x, float s) { return (uint32_t)max(-127, __float2int_rd(__fdiv_rn(x, s))) & 0xFFu; }
+__device__ __forceinline__ uint64_t f2_add_up(uint64_t a, uint64_t b) {  // rounded up
+  uint64_t r;
+  asm("add.rp.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// The scale of a page whose largest magnitude is amax, and how its quotients are computed.
+struct PageScale {
+  float s, inv;  // inv 0: by divisions
+};
+__device__ __forceinline__ PageScale page_scale(float amax) {
+  PageScale c;
+  c.s = __fdiv_rn(amax, 127.0f);
+  c.inv = c.s >= 0x1p-100f && c.s <= 1.0f ? __frcp_rn(c.s) : 0.0f;
+  return c;
+}
+
+// Codes of four bounds: min(127, ceil(x / s)) with sign 1, max(-127, floor(x / s)) = -min(127, ceil(x / -s)) with -1.
+// The quotients are rounded as the IEEE division does: twice corrected by their remainders, the second time from
+// within an ulp, with the rounded inverse (Markstein, 1990).  Remainders and quotients of a page of scale 2^-100 to 1 are not
+// subnormal where they count; other pages take divisions (an IEEE division for each of eight channels took a
+// quarter of a page's instructions).
+__device__ __forceinline__ uint32_t codes_of(const float* x, const PageScale& c, float sign) {
+  uint32_t y[4];
+  if (c.inv != 0.0f) {
+    const uint64_t inv = f2(sign * c.inv, sign * c.inv), ns = f2(-sign * c.s, -sign * c.s);
+    const uint64_t magic = f2(12582912.0f, 12582912.0f), sg = f2(sign, sign);  // 3 2^22: whole numbers in the low bits
+    const uint64_t back = f2(12582912.0f * (1.0f - sign), 12582912.0f * (1.0f - sign));
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      const uint64_t x2 = f2(x[e], x[e + 1]);
+      uint64_t q = f2_mul(x2, inv);
+      q = f2_fma(f2_fma(q, ns, x2), inv, q);
+      q = f2_fma(f2_fma(q, ns, x2), inv, q);
+      float a, b;
+      f2_split(q, a, b);
+      f2_split(f2_fma(f2_add_up(f2(fminf(a, 127.0f), fminf(b, 127.0f)), magic), sg, back), a, b);
+      y[e] = __float_as_uint(a);
+      y[e + 1] = __float_as_uint(b);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int up = c.s != 0.0f ? min(127, __float2int_ru(__fdiv_rn(sign * x[e], c.s))) : 0;
+      y[e] = (uint32_t)(sign < 0.0f ? -up : up);
+    }
+  }
+  return __byte_perm(__byte_perm(y[0], y[1], 0x0040), __byte_perm(y[2], y[3], 0x0040), 0x5410);
+}
+
+// The largest of the warp's magnitudes (not NaN: not negative, they are ordered as whole numbers).
+__device__ __forceinline__ float largest(float x) { return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x))); }
 
 // Largest and smallest keys of the first `fill` (1 .. P) tokens of a page -> its record.
 __device__ __forceinline__ void page8(const uint8_t* pg, int P, int fill, uint8_t* codes, float* scale, int lane) {
@@ -78,20 +129,10 @@ __device__ __forceinline__ void page8(const uint8_t* pg, int P, int fill, uint8_
   float amax = 0.0f;
 #pragma unroll
   for (int e = 0; e < 4; ++e) amax = fmax3(amax, fabsf(hi[e]), fabsf(lo[e]));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const float s = __fdiv_rn(amax, 127.0f);
-  uint32_t up = 0, down = 0;
-  if (s != 0.0f) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      up |= code_up(hi[e], s) << (8 * e);
-      down |= code_down(lo[e], s) << (8 * e);
-    }
-  }
-  reinterpret_cast<uint32_t*>(codes)[lane] = up;
-  reinterpret_cast<uint32_t*>(codes + kHeadDim)[lane] = down;
-  if (lane == 0) *scale = s;
+  const PageScale c = page_scale(largest(amax));
+  reinterpret_cast<uint32_t*>(codes)[lane] = codes_of(hi, c, 1.0f);
+  reinterpret_cast<uint32_t*>(codes + kHeadDim)[lane] = codes_of(lo, c, -1.0f);
+  if (lane == 0) *scale = c.s;
 }
 
 __device__ __forceinline__ void page4(const uint8_t* pg, int fill, uint8_t* codes, float* scale, int lane) {
@@ -101,13 +142,23 @@ __device__ __forceinline__ void page4(const uint8_t* pg, int fill, uint8_t* code
   for (int i = 0; i < 4; ++i) hi[i] = 0xFC00FC00u, lo[i] = 0x7C007C00u;
   for (int t0 = 0; t0 < fill; t0 += kBlk) {
     const uint8_t* blk = pg + t0 / kBlk * kBlkBytes;
-    const int last = min(fill - t0, kBlk) - 1;
+    const int last = fill - t0 - 1;
     uint32_t w[8], s[8];
+    const uint8_t* pw = blk + half * 64 + word * 4;
+    const uint8_t* ps = blk + kBlkKs + half * 8 + j * 2;
+    if (last >= kBlk - 1) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = min(2 * i + half, last);
-      w[i] = *reinterpret_cast<const uint32_t*>(blk + r * 64 + word * 4);
-      s[i] = *reinterpret_cast<const uint16_t*>(blk + kBlkKs + r * 8 + j * 2);
+      for (int i = 0; i < 8; ++i) {
+        w[i] = *reinterpret_cast<const uint32_t*>(pw + i * 128);
+        s[i] = *reinterpret_cast<const uint16_t*>(ps + i * 16);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = min(2 * i + half, last) - half;
+        w[i] = *reinterpret_cast<const uint32_t*>(pw + r * 64);
+        s[i] = *reinterpret_cast<const uint16_t*>(ps + r * 8);
+      }
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -132,74 +183,57 @@ __device__ __forceinline__ void page4(const uint8_t* pg, int fill, uint8_t* code
     x[2 * e + 1] = f.y;
     amax = fmax3(amax, fabsf(f.x), fabsf(f.y));
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const float s = __fdiv_rn(amax, 127.0f);
-  uint32_t c[2] = {0u, 0u};
-  if (s != 0.0f) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) c[e >> 2] |= (half ? code_down(x[e], s) : code_up(x[e], s)) << (8 * (e & 3));
-  }
-  *reinterpret_cast<uint2*>(codes + half * kHeadDim + 32 * j + 8 * (word >> 2)) = make_uint2(c[0], c[1]);
-  if (lane == 0) *scale = s;
+  const PageScale c = page_scale(largest(amax));
+  const float sign = half ? -1.0f : 1.0f;
+  *reinterpret_cast<uint2*>(codes + half * kHeadDim + 32 * j + 8 * (word >> 2)) = make_uint2(codes_of(x, c, sign), codes_of(x + 4, c, sign));
+  if (lane == 0) *scale = c.s;
 }
 
-// Whether sequence b's new tokens reach its u-th page, counted from the first new token's.
-__device__ __forceinline__ bool has_page(const SummarizeParams& p, int b, int64_t u) {
-  const int n = new_rows(p, b).n;
-  const int64_t start = n > 0 ? p.start_pos[b] : 0;
-  const int lg = page_log2(p.page_size);
-  return n > 0 && start + n > (((start >> lg) + u) << lg);
-}
-
-template <bool kFour>
-__device__ __forceinline__ void summarize_page(const SummarizeParams& p, int b, int64_t u, int h, int lane) {
-  const int P = p.page_size, lg = page_log2(P);
-  const int64_t start = p.start_pos[b], end = start + new_rows(p, b).n;
-  const int64_t at = (start >> lg) + u;  // (floor, also below 0)
-  if (at < 0 || at >= p.max_pages) {
-    if (lane == 0 && p.err) atomicOr(p.err, CAI_DEVERR_LENGTH);
-    return;
-  }
-  const int32_t page = p.table[(int64_t)b * p.max_pages + at];
-  if (page < 0 || page >= p.num_pages[h]) {
-    if (lane == 0 && p.err) atomicOr(p.err, CAI_DEVERR_PAGE);
-    return;
-  }
-  const int64_t left = end - (at << lg);
-  const int fill = (int)(left < P ? left : P);
-  uint8_t* codes = p.data[h] + (int64_t)page * (2 * kHeadDim);
-  float* scale = reinterpret_cast<float*>(p.data[h] + (int64_t)p.num_pages[h] * (2 * kHeadDim)) + page;
-  if constexpr (kFour)
-    page4(p.pages[h] + (int64_t)page * page_bytes4(P), fill, codes, scale, lane);
-  else
-    page8(p.pages[h] + (int64_t)page * page_bytes(P), P, fill, codes, scale, lane);
-}
-
-// A warp looks through its share of the (sequence, page, K/V head) triples, 32 at a time, for those with new tokens.
+// A warp looks through its share of the (sequence, page, K/V head) triples, 32 at a time: a lane finds the place of one, and
+// the warp goes through those that have new tokens.
 template <bool kFour>
 __global__ void __launch_bounds__(kSumWarps * 32, kSumBlocks) summarize_kernel(const __grid_constant__ SummarizeParams p) {
   grid_dependency_wait();
   grid_launch_dependents();
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31, P = p.page_size, lg = page_log2(P);
   const int64_t per_seq = (int64_t)p.groups * p.num_kv_heads, items = p.batch * per_seq;
   const int64_t step = (int64_t)gridDim.x * kSumWarps;
-  for (int64_t w = (int64_t)blockIdx.x * kSumWarps + (threadIdx.x >> 5); w < items; w += 32 * step) {
+  for (int64_t w = blockIdx.x + (int64_t)gridDim.x * (threadIdx.x >> 5); w < items; w += 32 * step) {
     const int64_t mine = w + lane * step;
-    int b = 0, h = 0;
-    int64_t u = 0;
-    bool there = false;
+    int32_t page = -1;
+    int h = 0, fill = 0;
     if (mine < items) {
       const int64_t i = over(mine, p.num_kv_heads);
       h = (int)(mine - i * p.num_kv_heads);
-      b = (int)over(i, p.groups);
-      u = i - (int64_t)b * p.groups;
-      there = has_page(p, b, u);
-      if (u == 0 && h == 0 && new_rows(p, b).n < 0 && p.err) atomicOr(p.err, CAI_DEVERR_LENGTH);
+      const int b = (int)over(i, p.groups);
+      const int64_t u = i - (int64_t)b * p.groups;  // counted from the first new token's page
+      const int n = new_rows(p, b).n;
+      if (n > 0) {
+        const int64_t start = p.start_pos[b], at = (start >> lg) + u, left = start + n - (at << lg);  // (floor, also below 0)
+        int bits = 0;
+        if (left <= 0) {  // the tokens end before this page
+        } else if (at < 0 || at >= p.max_pages) {
+          bits = CAI_DEVERR_LENGTH;
+        } else {
+          page = p.table[(int64_t)b * p.max_pages + at];
+          if (page < 0 || page >= p.num_pages[h]) bits = CAI_DEVERR_PAGE, page = -1;
+        }
+        fill = (int)(left < P ? left : P);
+        if (bits && p.err) atomicOr(p.err, bits);
+      } else if (n < 0 && u == 0 && h == 0 && p.err) {
+        atomicOr(p.err, CAI_DEVERR_LENGTH);
+      }
     }
-    for (uint32_t m = __ballot_sync(0xffffffffu, there); m; m &= m - 1) {
-      const int k = __ffs(m) - 1;
-      summarize_page<kFour>(p, __shfl_sync(0xffffffffu, b, k), __shfl_sync(0xffffffffu, u, k), __shfl_sync(0xffffffffu, h, k), lane);
+    const int what = h << 8 | fill;
+    for (uint32_t m = __ballot_sync(0xffffffffu, page >= 0); m; m &= m - 1) {
+      const int k = __ffs(m) - 1, pg = __shfl_sync(0xffffffffu, page, k), hf = __shfl_sync(0xffffffffu, what, k);
+      const int hk = hf >> 8, f = hf & 255;
+      uint8_t* codes = p.data[hk] + (int64_t)pg * (2 * kHeadDim);
+      float* scale = reinterpret_cast<float*>(p.data[hk] + (int64_t)p.num_pages[hk] * (2 * kHeadDim)) + pg;
+      if constexpr (kFour)
+        page4(p.pages[hk] + (int64_t)pg * page_bytes4(P), f, codes, scale, lane);
+      else
+        page8(p.pages[hk] + (int64_t)pg * page_bytes(P), P, f, codes, scale, lane);
     }
   }
 }
@@ -209,10 +243,11 @@ __global__ void __launch_bounds__(kSumWarps * 32, kSumBlocks) summarize_kernel(c
 cudaError_t launch_summarize(SummarizeParams p, bool four, cudaStream_t stream) {
   p.groups = (int32_t)(((int64_t)p.n_new + 2 * p.page_size - 2) / p.page_size);  // from any position in a page
   const int64_t items = (int64_t)p.batch * p.groups * p.num_kv_heads;
-  // At most four waves of warps, each with a share of the triples: 64 dialogues of up to 8192 tokens, 4-bit, four K/V heads
-  // 32 us (one wave 37, eight 36, a warp for each triple 39); int8 likewise (23; 25, 25, 30).
+  // One wave of warps, each with a share of the triples: the dialogues above take 23.7 us, with two waves 25.4, with four 27.5
+  // (int8 18.3; 18.9, 21.1).  The warps of a block take triples far apart: those of one sequence are there, or are not,
+  // together, and a block of neighbours has twice as many pages as another.
   const int64_t blocks = (items + kSumWarps - 1) / kSumWarps, wave = (int64_t)num_sms() * kSumBlocks;
-  const dim3 grid((unsigned)std::min(blocks, 4 * wave));
+  const dim3 grid((unsigned)std::min(blocks, wave));
   return four ? launch_pdl(summarize_kernel<true>, grid, dim3(kSumWarps * 32), 0, stream, p)
               : launch_pdl(summarize_kernel<false>, grid, dim3(kSumWarps * 32), 0, stream, p);
 }

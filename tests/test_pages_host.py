@@ -101,6 +101,31 @@ def test_corrected_quotients_are_the_divisions():
         assert np.array_equal(np.where(x <= amax, q, 0), np.where(x <= amax, x / t, 0))
 
 
+@pytest.mark.parametrize("least,most", [(-99, -60), (-20, 0)])  # scales from 2^-100 to 1
+def test_twice_corrected_quotients_are_the_divisions(least, most):
+    """A summary's x / s: two corrections of the product with the rounded inverse, for fp32 x anywhere in [-127 s, 127 s] and
+    within some ulps of whole multiples of s."""
+    f, wide = np.float32, np.longdouble
+    rng = np.random.default_rng(3)
+    amax = (rng.uniform(64, 128, 4000) * 2.0 ** rng.integers(least, most + 1, 4000)).astype(f)[:, None]
+    s = amax / f(127)
+    inv = f(1) / s
+    near = (rng.integers(-127, 128, (4000, 300)) * s.astype(np.float64)).astype(f)
+    steps = rng.integers(-3, 4, near.shape)
+    for k in range(3):
+        near = np.where(np.abs(steps) > k, np.nextafter(near, np.where(steps > 0, f(np.inf), f(-np.inf))), near)
+    wild = amax * np.ldexp(rng.uniform(-1, 1, (4000, 300)), -rng.integers(0, 30, (4000, 300))).astype(f)
+    x = np.clip(np.concatenate([near, wild, amax, -amax], 1), -amax, amax)
+    q = x * inv
+    for _ in range(2):
+        r = (x.astype(wide) - q.astype(wide) * s.astype(wide)).astype(f)
+        q = (q.astype(wide) + r.astype(wide) * inv.astype(wide)).astype(f)
+    # A remainder is a multiple of ulp(q) ulp(s), 2^-149 or more for |q| >= 2^-3 and s >= 2^-100; a smaller quotient, whose
+    # remainder may be rounded, counts by its sign alone.
+    whole = np.abs(x) >= s * f(2.0 ** -3)
+    assert np.array_equal(q[whole], (x / s)[whole]) and np.array_equal(np.ceil(q), np.ceil(x / s))
+
+
 def test_selection_takes_ends_and_ties():
     codes, scale = np.zeros((20, 256), np.int8), np.ones(20, np.float32)
     blocks, tokens = pages.select(np.ones((2, 128), np.float32), codes, scale, 19 * 16 + 3, 16, 6, 1, 2)
@@ -152,6 +177,7 @@ def test_select_refusals(lib):
     assert call(pages_out=None) == 1 and call(len_out=None) == 1
     assert call(ws=None) == 3 and call(ws_bytes=need - 1) == 3 and call(ws=FAKE + 64) == 3
     assert call(batch=-1) == 1 and call(n=-1) == 1 and call(off=FAKE, total=-1) == 1 and call(maxp=0) == 1 and call(batch=65536) == 2
+    assert call(off=FAKE, total=1 << 30, n=1 << 22) == 2  # a block of a launch for each row and K/V head
     for bad in ((0, 2, 8, 2, 64), (2, -1, 8, 2, 64), (2, 2, 7, 2, 64), (2, 2, 8, 9, 64), (2, 2, 8, 2, 0), (65536, 2, 8, 2, 64)):
         assert cai.cai_kv_select_workspace_size(*bad) == 0
 
