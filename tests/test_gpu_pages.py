@@ -152,6 +152,17 @@ def test_summaries_bad_arguments_on_the_device(four):
         assert changed == {int(d.table_np[b, p // 16]) for b, lo, hi in done for p in range(lo, hi)}
 
 
+@pytest.mark.parametrize("four", [False, True])
+def test_summaries_of_many_sequences_with_a_loose_bound(four):
+    """The largest n_new that a call may give, beside 300 short sequences."""
+    new = [int(n) for n in np.random.default_rng(5).integers(0, 40, 300)]
+    d = Dialogues(four, new, 1, 16, seed=6)
+    sums, err = d.summaries(), flag()
+    d.summarize(sums, [0] * 300, 1 << 22, np.concatenate([[0], np.cumsum(new)]), err)
+    assert err.item() == 0
+    same(sums, d.want([0] * 300, new))
+
+
 # ----------------------------------------------------------------------------------- selection
 
 def random_summaries(rng, hkv, num_pages, page, ties=False):
@@ -505,6 +516,56 @@ def test_attend_bad_arguments_on_the_device(four, g):
     broken[1, 0, 3:] = 1 << 29  # behind the length: not read
     out, lse = attend(d, q, broken, [160, 48, 16, 31])
     check_attend(d, q, broken, [160, 48, 16, 31], out, lse)
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("g", [4, 32, 64])
+def test_attend_rows_of_bad_pages_alone(four, g):
+    """A row none of whose pages is in the pool has nothing to attend, in one piece or cut; its neighbours do not notice."""
+    rng = np.random.default_rng(16)
+    d = Dialogues(four, [3000], 1, 16, seed=17)
+    lists = np.repeat(d.table_np[:, None, :180], 3, 0).astype(np.int64)
+    lists[1] = d.num_pages + rng.integers(0, 9, 180)
+    q = dev(rng.normal(size=(3, g, 128)).astype(np.float32), torch.bfloat16)
+    for lens, splits in (([70, 90, 100], 0), ([2880, 2880, 2000], 0), ([2880, 2880, 2000], 5)):
+        out, lse = attend(d, q, lists, lens, splits=splits, bits=cai.CAI_DEVERR_PAGE)
+        assert (out[1] == 0).all() and (lse[1] == -np.inf).all()
+        check_attend(d, q, lists, lens, out, lse, skip=(1,))
+
+
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("g", [4, 32])
+def test_attend_graphs_share_a_workspace(four, g):
+    """Two captured calls of different shapes in turn on one workspace, replayed: the bits of calls on their own."""
+    rng = np.random.default_rng(18)
+    d = Dialogues(four, [900, 700], 2, 16, seed=19)
+    size = cai.cai_kv4_attend_pages_workspace_size if four else cai.cai_kv_attend_pages_workspace_size
+    f = cai.cai_kv4_attend_pages if four else cai.cai_kv_attend_pages
+    calls = []
+    for rows, width in ((3, 50), (200, 7)):
+        lens = rng.integers(0, 16 * width + 1, rows)
+        lists = random_lists(rng, d, rows, width, lens)
+        q = dev(rng.normal(size=(rows, 2 * g, 128)).astype(np.float32), torch.bfloat16)
+        calls.append((q, lists, lens, attend(d, q, lists, lens), size(rows, 2 * g, 2, width, 16)))
+    ws = torch.full((max(c[4] for c in calls),), 0xFF, dtype=torch.uint8, device=DEV)
+    graphs = []
+    for q, lists, lens, _, _ in calls:
+        args = [q, dev(np.ascontiguousarray(lists, np.int32)), dev(np.array(lens, np.int32))]
+        out, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], device=DEV)
+        f(d.pools, *args, SCALE, 0, ws, out, lse)
+        graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=stream):
+            f(d.pools, *args, SCALE, 0, ws, out, lse)
+        graphs.append((graph, out, lse, args))
+    for _ in range(3):
+        for graph, out, lse, _ in graphs:
+            out.fill_(float("nan"))
+            lse.fill_(float("nan"))
+            graph.replay()
+        torch.cuda.synchronize()
+        for (_, out, lse, _), (_, _, _, want, _) in zip(graphs, calls):
+            assert np.array_equal(host(out), want[0]) and np.array_equal(host(lse), want[1])
 
 
 @pytest.mark.parametrize("g", [4, 32, 64])
