@@ -14,11 +14,14 @@
 // way; then a thread has a page and all columns, and takes the largest of each query row.  Two blocks share an SM, one
 // converting while the other's products run.
 //
-// Measured: 4096 rows of 32 heads over 528 pages 70 us, of them 60 the scores, 2000 cycles a tile of 128 columns: the
-// products take 1024 of them (64 cycles for M = N = 128, K = 16), the conversion 560, reading D 950, and two blocks
-// overlap them in part; 64 rows of 64 heads over 256 to 2048 pages 20 us, mostly latencies.  A persistent block with a
-// kind of warp for each of these steps took 58 us and 21, and contexts of middle length 51 us instead of 37: its readers of
-// D, with 80 registers a thread, became the longest step.
+// Measured: 4096 rows of 32 heads over 528 pages 69 us, of them 55 the scores: a block takes 7 thousand cycles until its first
+// products (positions, page ids, codes and queries come one behind the other; what needs no position is loaded first, 71 us
+// without that) and 3600 a tile of 128 columns, two blocks side by side: conversion 1300, products 1000 to 1400, of which
+// the tensor pipe needs 1024, reading D 1000.  64 rows of 64 heads over 256 to 2048 pages 21 us, mostly latencies.
+// Products in halves of the channels and columns, so that conversion and reading run beside them, changed nothing (70 us, 37 to
+// 39 at middle lengths): 4800 warp instructions a tile are what the four schedulers issue.  A persistent block with a kind of warp
+// for each step took 58 us and 21, and contexts of middle length 51 us instead of 37: its readers of D, with 80 registers a
+// thread, became the longest step.
 #include <algorithm>
 
 #include "ptx.cuh"
@@ -137,55 +140,11 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
   const int h = (int)(item - tile * p.num_kv_heads);
   const RowTile rt = find_tile(p, tile, per, shared);
   if (rt.n == 0) return;
-  const int lg = page_log2(p.page_size);
-  const int64_t last_pos = min(rt.pos0 + rt.n, (int64_t)p.max_pages << lg);  // (positions past the table are refused by the selection)
-  if (last_pos <= 0) return;
-  const int blocks = (int)((last_pos - 1) >> lg) + 1;  // of the last row
-  const int c0 = (int)(blockIdx.x - item * spans) * span * kTilePages, c1 = min(c0 + span * kTilePages, blocks - p.last);
-  if (blocks <= p.keep || c0 >= c1) return;
-
-  if (warp == 0) tmem_alloc(&slot, kTmem);
-  if (tid == 0) {
-    mbar_init(&done, 1);
-    wait.abort = 0;
-    wait.limit_ns = p.wait_ns;
-    fence_barrier_init();
-  }
-  const int g = lane >> 2, t4 = lane & 3, quarter = warp & 3, half = warp >> 2;
-  const int32_t* table = p.table + (int64_t)rt.b * p.max_pages;
-  const uint8_t* data = p.data[h];
-  const float* scales = reinterpret_cast<const float*>(data + (int64_t)p.num_pages[h] * (2 * kHeadDim));
-  const auto page_of = [&](int blk) -> int32_t { return blk < c1 ? __ldg(table + blk) : 0; };
-  const auto in_pool = [&](int32_t page) { return (uint32_t)page < (uint32_t)p.num_pages[h]; };
-  // This lane's 64 codes, 16 of every 64, of pages (quarter, half) 16 + g and + 8 of a tile; their ids are loaded a tile ahead
-  // of the codes, these a tile ahead of their use.
-  uint4 a[2][4];
-  int32_t id[2];
-  const int first = 32 * quarter + 16 * half;
-  const auto there = [&](int base) { return base + first < c1; };  // (this warp has pages of the tile)
-  const auto load_ids = [&](int base) {
-#pragma unroll
-    for (int r = 0; r < 2; ++r) id[r] = page_of(base + first + g + 8 * r);
-  };
-  const auto load = [&](int base) {
-    if (!there(base)) return;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const uint4* row = reinterpret_cast<const uint4*>(data + (int64_t)(in_pool(id[r]) ? id[r] : 0) * (2 * kHeadDim)) + t4;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) a[r][c] = __ldg(row + 4 * c);
-    }
-  };
-  load_ids(c0);
-  int32_t page_next = page_of(c0 + 32 * quarter + lane);  // of this thread's page of D
-  load(c0);
-  load_ids(c0 + kTilePages);
-
-  // Columns: whole numbers of the rows' heads, eight columns a warp, lane (g, t) channels 64 c + 16 t .. + 15 of column g: they
-  // stand at words t of units 8 c + e (q+) and 16 + 8 c + e (q-).  A group that does not fill its columns repeats its
-  // last head, columns past the rows are 0.
+  // What does not depend on the position is loaded first: the columns' queries and the first pages' ids (of table entries that may
+  // be past the context; these are not used).
   const int G = p.num_q_heads / p.num_kv_heads, gp = padded_heads(G);
   const int used = (rt.n * gp + 15) / 16 * 16;
+  const int g = lane >> 2, t4 = lane & 3, quarter = warp & 3, half = warp >> 2;
   uint4 w[2][2];
   const auto load_q = [&](int n0) {
     const int n = n0 + g, i = n / gp, head = min(n - i * gp, G - 1);
@@ -195,7 +154,56 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
 #pragma unroll
       for (int k = 0; k < 2; ++k) w[c][k] = n0 < used && i < rt.n ? __ldg(q + 8 * c + k) : make_uint4(0u, 0u, 0u, 0u);
   };
+  const int c0 = (int)(blockIdx.x - item * spans) * span * kTilePages;
+  const int32_t* table = p.table + (int64_t)rt.b * p.max_pages;
+  const int first = 32 * quarter + 16 * half;
+  int c1 = p.max_pages;
+  const auto page_of = [&](int blk) -> int32_t { return blk < c1 ? __ldg(table + blk) : 0; };
+  int32_t id[2];
+  const auto load_ids = [&](int base) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) id[r] = page_of(base + first + g + 8 * r);
+  };
+  load_ids(c0);
+  int32_t page_next = page_of(c0 + 32 * quarter + lane);  // of this thread's page of D
   load_q(8 * warp);
+
+  const int lg = page_log2(p.page_size);
+  const int64_t last_pos = min(rt.pos0 + rt.n, (int64_t)p.max_pages << lg);  // (positions past the table are refused by the selection)
+  if (last_pos <= 0) return;
+  const int blocks = (int)((last_pos - 1) >> lg) + 1;  // of the last row
+  c1 = min(c0 + span * kTilePages, blocks - p.last);
+  if (blocks <= p.keep || c0 >= c1) return;
+
+  if (warp == 0) tmem_alloc(&slot, kTmem);
+  if (tid == 0) {
+    mbar_init(&done, 1);
+    wait.abort = 0;
+    wait.limit_ns = p.wait_ns;
+    fence_barrier_init();
+  }
+  const uint8_t* data = p.data[h];
+  const float* scales = reinterpret_cast<const float*>(data + (int64_t)p.num_pages[h] * (2 * kHeadDim));
+  const auto in_pool = [&](int32_t page) { return (uint32_t)page < (uint32_t)p.num_pages[h]; };
+  // This lane's 64 codes, 16 of every 64, of pages (quarter, half) 16 + g and + 8 of a tile; their ids are loaded a tile ahead
+  // of the codes, these a tile ahead of their use.
+  uint4 a[2][4];
+  const auto there = [&](int base) { return base + first < c1; };  // (this warp has pages of the tile)
+  const auto load = [&](int base) {
+    if (!there(base)) return;
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const uint4* row = reinterpret_cast<const uint4*>(data + (int64_t)(in_pool(id[r]) ? id[r] : 0) * (2 * kHeadDim)) + t4;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) a[r][c] = __ldg(row + 4 * c);
+    }
+  };
+  load(c0);
+  load_ids(c0 + kTilePages);
+
+  // Columns: whole numbers of the rows' heads, eight columns a warp, lane (g, t) channels 64 c + 16 t .. + 15 of column g: they
+  // stand at words t of units 8 c + e (q+) and 16 + 8 c + e (q-).  A group that does not fill its columns repeats its
+  // last head, columns past the rows are 0.
   for (int n0 = 8 * warp; n0 < used; n0 += 8 * kWarps) {
     const int n = n0 + g, i = n / gp, head = min(n - i * gp, G - 1);
     float y[32], amax = 0.0f;
@@ -253,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
     const int32_t page = page_next;
     const bool good = in_pool(page);
     const float s = good ? __ldg(scales + page) : 0.0f;
-    if (!good && half == 0 && p.err) atomicOr(p.err, CAI_DEVERR_PAGE);
+    if (!good && blk < c1 && half == 0 && p.err) atomicOr(p.err, CAI_DEVERR_PAGE);
     page_next = page_of(blk + kTilePages);
     // ---- A: column 32 c + 4 e + t holds channels 64 c + 16 t + 2 e, + 1 of the 256 codes.  (Rows of pages that are not
     // there keep what they held: D's rows are independent.)

@@ -276,7 +276,7 @@ def test_select_padded_batch_and_bad_arguments():
 
 
 def test_select_leaves_its_neighbours_alone():
-    """Outputs are written within their bounds, and no row of the table past the context is looked at."""
+    """Outputs are written within their bounds, and no table entry past the context counts."""
     rng = np.random.default_rng(8)
     sums, _ = random_summaries(rng, 1, 40, 16)
     table = np.full((1, 500), 1 << 30, np.int32)
