@@ -418,7 +418,7 @@ __device__ __forceinline__ void find_least(const Group& group, const uint32_t (&
   uint32_t low = 0xFFFFFFFFu, high = 0u;
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
-    if (k >= items) break;
+    if (k % 4 == 0 && k >= items) break;
     low = min(low, x[k] - 1u);           // (none: the largest)
     high = max(high, x[k] + 1u);         // (not looked at: 0)
   }
@@ -435,7 +435,7 @@ __device__ __forceinline__ void find_least(const Group& group, const uint32_t (&
       group.clear();
 #pragma unroll
       for (int k = 0; k < kItems; ++k) {
-        if (k >= items) break;
+        if (k % 4 == 0 && k >= items) break;
         if ((x[k] & mask) == prefix && x[k] + 1u > 1u) atomicAdd(group.hist + ((x[k] >> shift) & digit), 1u);
       }
       const Found f = group.scan(m);
@@ -447,8 +447,8 @@ __device__ __forceinline__ void find_least(const Group& group, const uint32_t (&
         // Gathered: the value, its place in the order of pages.
 #pragma unroll
         for (int k = 0; k < kItems; ++k) {
-          if (k >= items) break;
-          if ((x[k] & mask) == prefix && x[k] + 1u > 1u) group.list[atomicAdd(group.count, 1u)] = make_uint2(x[k], k * Group::kThreadsIn + group.thread());
+          if (k % 4 == 0 && k >= items) break;
+          group.gather((x[k] & mask) == prefix && x[k] + 1u > 1u, make_uint2(x[k], k * Group::kThreadsIn + group.thread()));
         }
         group.rank(f.total, m, least, ties);
         return;
@@ -489,8 +489,13 @@ __device__ __forceinline__ Found scan_bins(const uint32_t* hist, uint32_t m, int
 struct WarpGroup {
   static constexpr int kThreadsIn = 32;
   uint32_t* hist;   // [256]
-  uint32_t* count;
   uint2* list;      // [kThreadsIn]
+  mutable uint32_t gathered;
+  __device__ __forceinline__ void gather(bool have, uint2 v) const {
+    const uint32_t m = __ballot_sync(0xffffffffu, have);
+    if (have) list[gathered + __popc(m & ((1u << thread()) - 1u))] = v;
+    gathered += __popc(m);
+  }
   __device__ __forceinline__ int thread() const { return threadIdx.x & 31; }
   __device__ __forceinline__ void range(uint32_t& low, uint32_t& high) const {
     low = __reduce_min_sync(0xffffffffu, low);
@@ -500,7 +505,6 @@ struct WarpGroup {
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < 2; ++i) reinterpret_cast<uint4*>(hist)[32 * i + thread()] = make_uint4(0u, 0u, 0u, 0u);
-    if (thread() == 0) *count = 0u;
     __syncwarp();
   }
   __device__ __forceinline__ Found scan(uint32_t m) const {
@@ -529,6 +533,9 @@ struct BlockGroup {
   uint32_t* hist;   // [256], then [2 kWarps] of the range, [3] of the scan, [3] of the rank
   uint32_t* count;
   uint2* list;
+  __device__ __forceinline__ void gather(bool have, uint2 v) const {
+    if (have) list[atomicAdd(count, 1u)] = v;
+  }
   __device__ __forceinline__ int thread() const { return threadIdx.x; }
   __device__ __forceinline__ void range(uint32_t& low, uint32_t& high) const {
     low = __reduce_min_sync(0xffffffffu, low);
@@ -592,7 +599,6 @@ struct BlockGroup {
 template <int kItems>
 __global__ void __launch_bounds__(kThreads, 4) select_warp_kernel(const __grid_constant__ SelectParams p, int64_t units) {
   __shared__ __align__(16) uint32_t hist[kWarps][256];
-  __shared__ uint32_t gathered[kWarps];
   __shared__ uint2 list[kWarps][32];
   __shared__ uint16_t taken[kWarps][32 * kItems];  // the pages' numbers, in order
   grid_dependency_wait();
@@ -606,22 +612,27 @@ __global__ void __launch_bounds__(kThreads, 4) select_warp_kernel(const __grid_c
   const int64_t row = over(unit, p.num_kv_heads);
   const int h = (int)(unit - row * p.num_kv_heads);
   int32_t* out = p.pages_out + unit * p.keep;
+  const float* scores = p.scores + unit * p.stride;
+  uint32_t x[kItems];
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {  // (under way while the row is found; those past its pages are not looked at)
+    const int i = 32 * k + lane;
+    x[k] = i < p.max_pages ? __float_as_uint(__ldcs(scores + i)) : 0u;
+  }
   const Row r = find_row(p, row, lane);
   if (lane == 0) {
     if (r.n == 0 && r.b >= 0 && p.err) atomicOr(p.err, CAI_DEVERR_LENGTH);
     if (h == 0) p.len_out[row] = r.n ? row_length(p, r) : 0;
   }
   if (r.n <= p.keep) return take_all(p, r, h, out, lane, 32);
-  const float* scores = p.scores + unit * p.stride;
   const int lo = p.first, hi = r.n - p.last, items = (r.n + 31) / 32;
-  uint32_t x[kItems];
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
     const int i = 32 * k + lane;
-    x[k] = i >= lo && i < hi ? looked_at(order_of(__ldcs(scores + i))) : i < r.n ? 0xFFFFFFFFu : 0u;
+    x[k] = i >= lo && i < hi ? looked_at(order_of(__uint_as_float(x[k]))) : i < r.n ? 0xFFFFFFFFu : 0u;
   }
   uint32_t least = 0xFFFFFFFEu, ties = 0;
-  if (p.keep > p.first + p.last) find_least(WarpGroup{hist[warp], gathered + warp, list[warp]}, x, items, p.keep - p.first - p.last, least, ties);
+  if (p.keep > p.first + p.last) find_least(WarpGroup{hist[warp], list[warp], 0u}, x, items, p.keep - p.first - p.last, least, ties);
   const int32_t* table = p.table + (int64_t)r.b * p.max_pages;
   const uint32_t below = (1u << lane) - 1u;
   int at = 0;
@@ -629,7 +640,7 @@ __global__ void __launch_bounds__(kThreads, 4) select_warp_kernel(const __grid_c
   bool bad = false;
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
-    if (k >= items) break;
+    if (k % 4 == 0 && k >= items) break;
     const int i = 32 * k + lane;
     bool take = x[k] > least;
     if (ties > tied) {  // (the same in the whole warp)
@@ -671,19 +682,24 @@ __global__ void __launch_bounds__(kThreads) select_block_kernel(const __grid_con
   if (p.q_off && blockIdx.x == 0)
     for (int i = tid; i < p.batch; i += kThreads)
       if (new_rows(p, i).n < 0 && p.err) atomicOr(p.err, CAI_DEVERR_LENGTH);
+  const float* scores = p.scores + (int64_t)blockIdx.x * p.stride;
+  uint32_t x[kItems];
+#pragma unroll
+  for (int k = 0; k < kItems; ++k) {  // (as above)
+    const int i = kThreads * k + tid;
+    x[k] = i < p.max_pages ? __float_as_uint(__ldcs(scores + i)) : 0u;
+  }
   const Row r = find_row(p, row, lane);
   if (tid == 0) {
     if (r.n == 0 && r.b >= 0 && p.err) atomicOr(p.err, CAI_DEVERR_LENGTH);
     if (h == 0) p.len_out[row] = r.n ? row_length(p, r) : 0;
   }
   if (r.n <= p.keep) return take_all(p, r, h, out, tid, kThreads);
-  const float* scores = p.scores + (int64_t)blockIdx.x * p.stride;
   const int lo = p.first, hi = r.n - p.last, items = (r.n + kThreads - 1) / kThreads;
-  uint32_t x[kItems];
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
     const int i = kThreads * k + tid;
-    x[k] = i >= lo && i < hi ? looked_at(order_of(__ldcs(scores + i))) : i < r.n ? 0xFFFFFFFFu : 0u;
+    x[k] = i >= lo && i < hi ? looked_at(order_of(__uint_as_float(x[k]))) : i < r.n ? 0xFFFFFFFFu : 0u;
   }
   uint32_t least = 0xFFFFFFFEu, ties = 0;
   if (p.keep > p.first + p.last) find_least(BlockGroup{hist, &gathered, list}, x, items, p.keep - p.first - p.last, least, ties);
@@ -691,7 +707,7 @@ __global__ void __launch_bounds__(kThreads) select_block_kernel(const __grid_con
   const uint32_t below = (1u << lane) - 1u;
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
-    if (k >= items) break;
+    if (k % 4 == 0 && k >= items) break;
     const bool sure = x[k] > least, tie = ties > 0 && x[k] == least;
     const uint32_t ms = __ballot_sync(0xffffffffu, sure), mt = __ballot_sync(0xffffffffu, tie);
     if (lane == 0) counts[k * kWarps + warp] = (uint32_t)__popc(ms) | (uint32_t)__popc(mt) << 16;
@@ -719,7 +735,7 @@ __global__ void __launch_bounds__(kThreads) select_block_kernel(const __grid_con
   bool bad = false;
 #pragma unroll
   for (int k = 0; k < kItems; ++k) {
-    if (k >= items) break;
+    if (k % 4 == 0 && k >= items) break;
     const bool sure = x[k] > least, tie = ties > 0 && x[k] == least;
     const uint32_t ms = __ballot_sync(0xffffffffu, sure), mt = __ballot_sync(0xffffffffu, tie);
     if (!(ms | mt)) continue;
