@@ -26,6 +26,7 @@
 // 142 us for 4.97 M keys, of 106 at the copy bandwidth).  The tensor memory kernel's products are padded
 // to 16 heads and its hand-offs cost more than they save there (172 us); at 16 heads this kernel, with
 // twice the mma, took 188.
+#include <algorithm>
 #include <cmath>
 
 #include "decode4.cuh"
@@ -497,6 +498,23 @@ int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
+// Lists are mostly full, so equal pieces of each row, one for every range or its rounds, are balanced by themselves: no
+// block looks for its share of all rows, and none holds the end of one and the start of another.  In tiles, with a piece's
+// start and end (piece_tiles): `whole` for equal pieces, `shared` for ranges that are cut anywhere.  64 rows of 32 tiles, 64
+// heads, int8: 35.6 us in four pieces, 41.0 shared; 128 rows 54.1 (two pieces), 56.1; 200 rows 81.4 (one), 72.8; 256 rows
+// 82.1, 87.4; 4 rows of 4 tiles, 8 heads: 8.8 in four, 11.6 whole.  0: shared.
+static int32_t list_splits(const Decode4Params& p, int64_t ranges, int64_t units, int64_t tiles, bool tc) {
+  if (units == 0) return 0;
+  int64_t s = std::max<int64_t>(1, std::min<int64_t>(std::min(tiles, ranges / units), kMaxSplits));
+  // Two tiles one after the other take no longer than a merge.  mma.sync, four blocks an SM, gains less from more pieces: 304
+  // rows of 8 tiles 14.8 us whole, 16.5 in two; 110 rows 11.9 whole, 10.8 in five.
+  if (tiles <= 2 || (!tc && s < 4)) s = 1;
+  const int64_t rounds = (units * s + ranges - 1) / ranges;
+  const int64_t whole = rounds * ((tiles + s - 1) / s + p.piece_tiles) - p.piece_tiles;
+  const int64_t shared = units * (tiles + p.piece_tiles) / ranges;
+  return whole <= shared + (s > 1 ? 2 : tc ? 4 : 6) ? (int32_t)s : 0;
+}
+
 size_t plan_decode4(Decode4Params& p, int32_t num_splits) {
   const int G = p.num_heads / p.num_kv_heads, tc = tensor_heads(p);
   const int blocks = num_sms() * (!tc ? kBlocks4 : p.lists ? 2 : 1);  // (lists: a range for each set of a block's warps)
@@ -514,6 +532,7 @@ size_t plan_decode4(Decode4Params& p, int32_t num_splits) {
   p.splits = 0;
   // Sequences of at most 512 keys are not cut: the merge's launch costs more than four tiles one after the other
   // (a step of four sequences of 64 to 512 keys: 8.3 us cut, 7.6 whole).
+  if (num_splits == 0 && p.lists) num_splits = list_splits(p, ranges, units, (span + kDecodeTile - 1) / kDecodeTile, tc != 0);
   if (num_splits == 0 && span <= 4 * kDecodeTile) num_splits = 1;
   if (num_splits > 0) {
     p.chunk = (int32_t)(((span + num_splits - 1) / num_splits + kDecodeTile - 1) / kDecodeTile * kDecodeTile);

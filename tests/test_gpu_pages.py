@@ -398,6 +398,24 @@ def test_attend_many_rows(four, g):
 
 
 @pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("g,rows", [(6, 430), (16, 170), (32, 170), (64, 75), (128, 30)])
+def test_attend_rows_cut_anywhere_and_in_equal_pieces(four, g, rows):
+    """Counts at which the blocks share all rows' tiles, and the same rows in equal pieces."""
+    rng = np.random.default_rng(g + 9)
+    d = Dialogues(four, [2500], 1, 16, seed=g + 2)
+    width = 128
+    lens = rng.integers(0, width * 16 + 1, rows)
+    lens[-1] = width * 16
+    lists = rng.choice(d.table_np[0, :156], (rows, 1, width))
+    q = dev(rng.normal(size=(rows, g, 128)).astype(np.float32), torch.bfloat16)
+    check = rng.choice(rows, 25, replace=False)
+    for splits in (0, 1, 3, 7):
+        out, lse = attend(d, q, lists, lens, splits=splits)
+        check_attend(d, q, lists, lens, out, lse, skip=set(range(rows)) - set(check.tolist()))
+        assert np.isfinite(out).all()
+
+
+@pytest.mark.parametrize("four", [False, True])
 @pytest.mark.parametrize("g", [6, 16, 32, 64])
 @pytest.mark.parametrize("most", [300, 1500])
 def test_attend_more_rows_than_the_chip_takes_at_once(four, g, most):
