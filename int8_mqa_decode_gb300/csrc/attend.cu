@@ -71,6 +71,9 @@ struct Shape {
   static constexpr int kOffPieces = kOffSlot + 16;                   // [set] pieces, then the list's state
   static constexpr int kPiecesBytes = (kPieces * (int)sizeof(Piece4) + (int)sizeof(List4) + 15) & ~15;
   static constexpr int kSmem = kOffPieces + kSets * kPiecesBytes;
+  // int8: a set's first query is turned by the softmax warps, which have nothing else to do yet, later ones by the producer (64
+  // rows of 4096 tokens, 64 heads: 36.0 us, without that 36.9; 4-bit chunks: 348 us, 335).
+  static constexpr bool kSoftTurns = !kFour;
   static_assert(kSmem <= 227 * 1024, "shared memory");
   static_assert(kTileBytes % 1024 == 0 || kFour, "swizzled rows");
   // Columns of a set: K 64, V^T 64 (two of them where they fit: V is then converted a tile ahead of its PV), S^T HN,
@@ -109,6 +112,7 @@ template <bool kFour, int HN>
 __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ AttendArgs args) {
   using S = Shape<kFour, HN>;
   constexpr int NS = S::kStages;
+  constexpr bool kSoftTurns = S::kSoftTurns;
   const Decode4Params& p = args.p;
   extern __shared__ __align__(1024) uint8_t smem[];  // (aligned by hand, it would be addressed as generic memory)
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -183,6 +187,31 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   int issued = 0;  // producer: tiles up to this one were started,
   int copies = 0;  // and copies of queries
 
+  // A query's rows as they came -> Q^T, in the order of K's columns, by `step` threads.
+  auto turn_query = [&](const uint8_t* src, uint8_t* dst, int first, int step) {
+#pragma unroll 4
+    for (int u = first; u < HN * 16; u += step) {
+      if constexpr (kFour) {
+        // Word t of 16-byte unit 4 j + i of a head holds channels 32 j + 8 t + 2 i, + 1.
+        const int t = u & 3, j = u >> 5 & 3, h = (u >> 2 & 7) | (u >> 7 << 3);
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (h < nh) x = *reinterpret_cast<const uint4*>(src + h * 256 + 64 * j + 16 * t);
+        uint32_t* y = reinterpret_cast<uint32_t*>(dst + (h >> 3) * 2048 + j * 512 + (h & 7) * 16 + t * 4);
+        y[0] = bf16x2_to_f16x2(x.x);
+        y[32] = bf16x2_to_f16x2(x.y);
+        y[64] = bf16x2_to_f16x2(x.z);
+        y[96] = bf16x2_to_f16x2(x.w);
+      } else {
+        // Eight channels a unit; eight lanes take a diagonal of heads and units (banks of both sides).
+        const int h = (u & 7) | (u >> 7 << 3), c8 = ((u + (u >> 3)) & 7) | (u >> 3 & 8);
+        uint4 x = make_uint4(0u, 0u, 0u, 0u);
+        if (h < nh) x = *reinterpret_cast<const uint4*>(src + h * 256 + 16 * c8);
+        *reinterpret_cast<uint4*>(dst + (h >> 3) * 2048 + c8 * 128 + (h & 7) * 16) =
+            make_uint4(bf16x2_to_f16x2(x.x), bf16x2_to_f16x2(x.y), bf16x2_to_f16x2(x.z), bf16x2_to_f16x2(x.w));
+      }
+    }
+  };
+
   // Every role goes through its set's lists of pieces; `work` is its part of one.  (The roles are the outermost branch:
   // the compiler gives each the registers that its setmaxnreg names.)  A wait that gave up, in either set, stops a set at
   // the end of a list: its warps agree there, by one barrier-reduction.
@@ -223,32 +252,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         }
         __syncwarp();
         const uint32_t phase = copies++ & 1;
+        if (kSoftTurns && gp == 0) return;
         if (!mbar_wait_lean_warp(q_raw, phase, wctl)) {
           ok = false;
           return;
         }
         uint8_t* dst = qt + (S::kQBufs == 2 ? gp & 1 : 0) * S::kQBytes;
-#pragma unroll 4
-        for (int u = lane; u < HN * 16; u += 32) {
-          if constexpr (kFour) {
-            // Word t of 16-byte unit 4 j + i of a head holds channels 32 j + 8 t + 2 i, + 1.
-            const int t = u & 3, j = u >> 5 & 3, h = (u >> 2 & 7) | (u >> 7 << 3);
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (h < nh) x = *reinterpret_cast<const uint4*>(src + h * 256 + 64 * j + 16 * t);
-            uint32_t* y = reinterpret_cast<uint32_t*>(dst + (h >> 3) * 2048 + j * 512 + (h & 7) * 16 + t * 4);
-            y[0] = bf16x2_to_f16x2(x.x);
-            y[32] = bf16x2_to_f16x2(x.y);
-            y[64] = bf16x2_to_f16x2(x.z);
-            y[96] = bf16x2_to_f16x2(x.w);
-          } else {
-            // Eight channels a unit; eight lanes take a diagonal of heads and units (banks of both sides).
-            const int h = (u & 7) | (u >> 7 << 3), c8 = ((u + (u >> 3)) & 7) | (u >> 3 & 8);
-            uint4 x = make_uint4(0u, 0u, 0u, 0u);
-            if (h < nh) x = *reinterpret_cast<const uint4*>(src + h * 256 + 16 * c8);
-            *reinterpret_cast<uint4*>(dst + (h >> 3) * 2048 + c8 * 128 + (h & 7) * 16) =
-                make_uint4(bf16x2_to_f16x2(x.x), bf16x2_to_f16x2(x.y), bf16x2_to_f16x2(x.z), bf16x2_to_f16x2(x.w));
-          }
-        }
+        turn_query(src, dst, lane, 32);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[gp & 1]);
@@ -566,6 +576,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           if (p.lse_out && key < nh) p.lse_out[row0 + key] = -INFINITY;
           continue;
         }
+        if (kSoftTurns && gp == 0) {
+          ok = mbar_wait_lean(q_raw, 0, wctl) && ok;
+          __syncwarp();
+          turn_query(pt, qt, key, 128);
+          fence_proxy_async_smem();
+          named_barrier_sync(bar, 128);
+          if (key == 0) mbar_arrive(&q_full[0]);
+        }
         if (lane < HN / 4) reinterpret_cast<float4*>(nref)[lane] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         __syncwarp();
         uint64_t l[HN / 2];     // this key's sums, per head pair
@@ -690,6 +708,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             }
 #pragma unroll
             for (int h = 0; h < HN; h += 2) mx = fmax3(mx, sv[h], sv[h + 1]);
+            if (!raised) {
+              raise = bar_red_or(bar, 128, !ok || mx > kRaise);
+              if (raise) continue;
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(s_read);  // the next S^T may come while these become weights
             // P^T's buffer is free once PV of tile n - kPBufs is done.
             constexpr int kB = S::kPBufs;
             if (n >= kB) ok = mbar_wait_lean(&pv_done[(n - kB) & 1], ((n - kB) >> 1) & 1, wctl) && ok;
@@ -708,9 +733,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
               }
               *reinterpret_cast<uint4*>(dst + i * 2048) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            if (raised) break;
-            raise = bar_red_or(bar, 128, !ok || mx > kRaise);
-            if (!raise) break;
+            break;
           }
           if (stop) {
             ok = false;
@@ -719,10 +742,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           fence_proxy_async_smem();
           tc_fence_before();
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(s_read);
-            mbar_arrive(&p_full[n & 1]);
-          }
+          if (lane == 0) mbar_arrive(&p_full[n & 1]);
 #pragma unroll
           for (int h = 0; h < HN; h += 2)
             l[h / 2] = kFour ? f2_add(l[h / 2], f2(sv[h], sv[h + 1])) : f2_fma(f2(sv[h], sv[h + 1]), iv2, l[h / 2]);

@@ -208,7 +208,7 @@ __device__ __forceinline__ void next_pieces(const Decode4Params& p, int c, List4
     const int64_t item = ls.unit + (int64_t)lane * p.ranges;
     const int64_t items = (int64_t)units * p.splits;
     if (item < items) {
-      const int split = (int)(item / units), unit = (int)(item - (int64_t)split * units);
+      const int split = (int)quotient(item, units), unit = (int)(item - (int64_t)split * units);
       x.b = unit / p.num_kv_heads;
       x.kvh = unit - x.b * p.num_kv_heads;
       SeqSplits sp;
