@@ -283,9 +283,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           return t < nt && lo < hi ? __ldg(table + ((pc.start / kT + t) * kT / P + lane)) : -1;
         };
         int32_t id_next = load_id(0);
-        // The query goes behind the copies of the tiles that have stages: all of them at the start, two ahead of the
-        // products later.
-        const int at_q = min(gp == 0 ? NS - 1 : NS - 2, nt - 1);
+        // The first query is asked for first, later ones go behind the copies of the tiles that have stages, two ahead of the
+        // products.  (4-bit: the first one behind all, as this warp waits for it.)
+        if (kSoftTurns && gp == 0) write_q(pc);
+        const int at_q = kSoftTurns && gp == 0 ? -1 : min(gp == 0 ? NS - 1 : NS - 2, nt - 1);
         for (int t = 0; t < nt; ++t) {
           const int x = gt + t, s = x % NS;
           const int32_t id = id_next;
