@@ -240,25 +240,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       // is not written before the S^T that needs this query.  That place and Q^T's buffer are free when the issuer says so
       // for the piece before, whose phase this warp has not passed: a parity names the last phase or the one before, so
       // the tiles' own barriers, of which several phases may pass between two pieces, would not do.
-      auto write_q = [&](const Piece4& pc) {
+      auto ask_q = [&](const Piece4& pc) {
         if (gp > 0 && !mbar_wait_lean_warp(q_room, (gp - 1) & 1, wctl)) {
           ok = false;
           return;
         }
-        uint8_t* src = pt + (S::kPBufs == 2 ? gt & 1 : 0) * S::kPBytes;
         if (lane == 0) {
           mbar_arrive_expect_tx(q_raw, (uint32_t)nh * kHeadDim * 2);
-          bulk_g2s(src, p.q + ((int64_t)pc.row * p.num_heads + (int64_t)pc.kvh * G + h0) * kHeadDim, (uint32_t)nh * kHeadDim * 2, q_raw);
+          bulk_g2s(pt + (S::kPBufs == 2 ? gt & 1 : 0) * S::kPBytes,
+                   p.q + ((int64_t)pc.row * p.num_heads + (int64_t)pc.kvh * G + h0) * kHeadDim, (uint32_t)nh * kHeadDim * 2, q_raw);
         }
         __syncwarp();
-        const uint32_t phase = copies++ & 1;
+        ++copies;
+      };
+      auto write_q = [&]() {
         if (kSoftTurns && gp == 0) return;
-        if (!mbar_wait_lean_warp(q_raw, phase, wctl)) {
+        if (!mbar_wait_lean_warp(q_raw, (copies - 1) & 1, wctl)) {
           ok = false;
           return;
         }
-        uint8_t* dst = qt + (S::kQBufs == 2 ? gp & 1 : 0) * S::kQBytes;
-        turn_query(src, dst, lane, 32);
+        turn_query(pt + (S::kPBufs == 2 ? gt & 1 : 0) * S::kPBytes, qt + (S::kQBufs == 2 ? gp & 1 : 0) * S::kQBytes, lane, 32);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[gp & 1]);
@@ -283,10 +284,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           return t < nt && lo < hi ? __ldg(table + ((pc.start / kT + t) * kT / P + lane)) : -1;
         };
         int32_t id_next = load_id(0);
-        // The first query is asked for first, later ones go behind the copies of the tiles that have stages, two ahead of the
-        // products.  (4-bit: the first one behind all, as this warp waits for it.)
-        if (kSoftTurns && gp == 0) write_q(pc);
-        const int at_q = kSoftTurns && gp == 0 ? -1 : min(gp == 0 ? NS - 1 : NS - 2, nt - 1);
+        // The first query is asked for first, later ones behind the copies of the tiles that have stages, two ahead of the
+        // products.
+        const int at_q = min(gp == 0 ? NS - 1 : NS - 2, nt - 1);
+        if (gp == 0) ask_q(pc);
         for (int t = 0; t < nt; ++t) {
           const int x = gt + t, s = x % NS;
           const int32_t id = id_next;
@@ -325,7 +326,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             }
           }
           if (t == at_q) {
-            write_q(pc);
+            if (gp > 0) ask_q(pc);
+            if (ok) write_q();
             if (!ok) break;
           }
         }
