@@ -499,7 +499,7 @@ int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
 }  // namespace
 
 // Lists are mostly full, so equal pieces of each row, one for every range or its rounds, are balanced by themselves: no
-// block looks for its share of all rows, and none holds the end of one and the start of another.  In tiles, with a piece's
+// block looks for its share of all rows, and none holds the end of one row and the start of another.  In tiles, with a piece's
 // start and end (piece_tiles): `whole` for equal pieces, `shared` for ranges that are cut anywhere.  64 rows of 32 tiles, 64
 // heads, int8: 35.6 us in four pieces, 41.0 shared; 128 rows 54.1 (two pieces), 56.1; 200 rows 81.4 (one), 72.8; 256 rows
 // 82.1, 87.4; 4 rows of 4 tiles, 8 heads: 8.8 in four, 11.6 whole.  0: shared.

@@ -14,10 +14,10 @@
 // way; then a thread has a page and all columns, and takes the largest of each query row.  Two blocks share an SM, one
 // converting while the other's products run.
 //
-// Measured: 4096 rows of 32 heads over 528 pages 69 us, of them 55 the scores: a block takes 7 thousand cycles until its first
+// Measured: 4096 rows of 32 heads over 528 pages 67 us, of them 55 the scores: a block takes 7 thousand cycles until its first
 // products (positions, page ids, codes and queries come one behind the other; what needs no position is loaded first, 71 us
 // without that) and 3600 a tile of 128 columns, two blocks side by side: conversion 1300, products 1000 to 1400, of which
-// the tensor pipe needs 1024, reading D 1000.  64 rows of 64 heads over 256 to 2048 pages 21 us, mostly latencies.
+// the tensor pipe needs 1024, reading D 1000.  64 rows of 64 heads over 256 to 2048 pages 20 us, mostly latencies.
 // Products in halves of the channels and columns, so that conversion and reading run beside them, changed nothing (70 us, 37 to
 // 39 at middle lengths): 4800 warp instructions a tile are what the four schedulers issue.  A persistent block with a kind of warp
 // for each step took 58 us and 21, and contexts of middle length 51 us instead of 37: its readers of D, with 80 registers a
