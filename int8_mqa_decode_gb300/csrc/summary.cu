@@ -8,7 +8,7 @@
 //
 // A page is computed anew from the cache whenever a token is added to it, so a summary never holds what an earlier
 // owner of the page wrote.  Bound by instructions where whole dialogues are summarized (the keys, half of the cache's
-// bytes, are read once: 64 dialogues of up to 8192 tokens, pages of 32, four K/V heads, 4-bit, 24 us, 49 MB at 2.1 TB/s, 850
+// bytes, are read once: 64 dialogues of up to 8192 tokens, pages of 32, four K/V heads, 4-bit, 24 us, 49 MB at 2.1 TB/s, 720
 // warp instructions a page of which the conversion and the minima take 400), by latency for the one page of a decode
 // step (2.7 us).  A warp has a page of one K/V head: int8, a lane four channels and 16 tokens' words under way at a time;
 // 4-bit, a lane eight channels of every other token, in fp16 pairs.  A page that is not full reads its last token

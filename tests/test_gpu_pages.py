@@ -537,6 +537,27 @@ def test_attend_bad_arguments_on_the_device(four, g):
 
 
 @pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("g,rows", [(6, 430), (32, 170), (64, 75)])
+def test_attend_bad_rows_among_many(four, g, rows):
+    """Counts at which the blocks share all rows' tiles: invalid lengths, empty rows and bad page ids between the others."""
+    rng = np.random.default_rng(g + 20)
+    d = Dialogues(four, [2500], 1, 16, seed=g + 3)
+    width = 128
+    lens = rng.integers(0, width * 16 + 1, rows)
+    wrong = rng.choice(rows, 40, replace=False)
+    lens[wrong[:10]], lens[wrong[10:20]], lens[wrong[20:30]] = -5, width * 16 + 1, 0
+    lists = rng.choice(d.table_np[0, :156], (rows, 1, width)).astype(np.int64)
+    lists[wrong[30:]] = d.num_pages + 3
+    lens[wrong[30:]] = np.maximum(lens[wrong[30:]], 1)
+    q = dev(rng.normal(size=(rows, g, 128)).astype(np.float32), torch.bfloat16)
+    out, lse = attend(d, q, lists, lens, bits=cai.CAI_DEVERR_LENGTH | cai.CAI_DEVERR_PAGE)
+    assert (out[wrong] == 0).all() and (lse[wrong] == -np.inf).all()
+    check = set(rng.choice(np.setdiff1d(np.arange(rows), wrong), 20, replace=False).tolist())
+    check_attend(d, q, lists, lens, out, lse, skip=set(range(rows)) - check)
+    assert np.isfinite(out).all()
+
+
+@pytest.mark.parametrize("four", [False, True])
 @pytest.mark.parametrize("g", [4, 32, 64])
 def test_attend_rows_of_bad_pages_alone(four, g):
     """A row none of whose pages is in the pool has nothing to attend, in one piece or cut; its neighbours do not notice."""
