@@ -965,7 +965,7 @@ def _attend_pages(entry: str, kind, pools, q, pages, lengths, softmax_scale, num
 
 
 def cai_kv_attend_pages(pools: Sequence[KVPool], q: torch.Tensor, pages: torch.Tensor, lengths: torch.Tensor,
-                        softmax_scale: float, num_splits: int, workspace: torch.Tensor, out: torch.Tensor,
+                        softmax_scale: float, num_splits: int, workspace: Optional[torch.Tensor], out: torch.Tensor,
                         lse_out: Optional[torch.Tensor] = None, err_flag: Optional[torch.Tensor] = None,
                         stream=None) -> None:
     """Attention of q bf16 [rows][Hq][128] -> out bf16 over the first lengths[r] tokens of the pages that row r lists for

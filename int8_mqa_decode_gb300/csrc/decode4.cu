@@ -498,20 +498,20 @@ int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
 
 }  // namespace
 
-// Lists are mostly full, so equal pieces of each row, one for every range or its rounds, are balanced by themselves: no
-// block looks for its share of all rows, and none holds the end of one row and the start of another.  In tiles, with a piece's
+// Lists are mostly full, so equal pieces of each row, one for every range, are balanced by themselves: no block looks
+// for its share of all rows, and none holds the end of one row and the start of another.  In tiles, with a piece's
 // start and end (piece_tiles): `whole` for equal pieces, `shared` for ranges that are cut anywhere.  64 rows of 32 tiles, 64
-// heads, int8: 35.6 us in four pieces, 41.0 shared; 128 rows 54.1 (two pieces), 56.1; 200 rows 81.4 (one), 72.8; 256 rows
-// 82.1, 87.4; 4 rows of 4 tiles, 8 heads: 8.8 in four, 11.6 whole.  0: shared.
+// heads, int8: 31.3 us in four pieces, 34.8 shared; 128 rows 48.5 (two pieces), 51.3; 256 rows 75.3 (one), 83.0; 256 rows of 16
+// tiles, 32 heads, 33.4 and 40.7; 4 rows of 4 tiles, 8 heads: 8.8 in four, 11.6 whole.  (Rows of random lengths: 29.6 and 28.3,
+// 45.9 and 37.0, 69.8 and 55.8, 30.4 and 29.6.)  Several rows a range, one behind the other, gain 10% where all
+// lists are full and lose up to 60% where they are not: shared.  0: shared.
 static int32_t list_splits(const Decode4Params& p, int64_t ranges, int64_t units, int64_t tiles, bool tc) {
-  if (units == 0) return 0;
-  int64_t s = std::max<int64_t>(1, std::min<int64_t>(std::min(tiles, ranges / units), kMaxSplits));
+  if (units == 0 || units > ranges) return 0;
+  int64_t s = std::min<int64_t>(std::min(tiles, ranges / units), kMaxSplits);
   // Two tiles one after the other take no longer than a merge.  mma.sync, four blocks an SM, gains less from more pieces: 304
   // rows of 8 tiles 14.8 us whole, 16.5 in two; 110 rows 11.9 whole, 10.8 in five.
   if (tiles <= 2 || (!tc && s < 4)) s = 1;
-  const int64_t rounds = (units * s + ranges - 1) / ranges;
-  const int64_t whole = rounds * ((tiles + s - 1) / s + p.piece_tiles) - p.piece_tiles;
-  const int64_t shared = units * (tiles + p.piece_tiles) / ranges;
+  const int64_t whole = (tiles + s - 1) / s, shared = units * (tiles + p.piece_tiles) / ranges;
   return whole <= shared + (s > 1 ? 2 : tc ? 4 : 6) ? (int32_t)s : 0;
 }
 
