@@ -129,6 +129,16 @@ def test_summaries_of_zeros_and_of_one_sign(four):
             assert np.array_equal(got[table[b, i]], code) and ((code >= 0).all() if b == 0 else (code <= 0).all())
 
 
+@pytest.mark.parametrize("size", [3e-38, 1e-33, 1e-30, 1e-3, 1e3, 1e30])
+def test_summaries_of_keys_of_any_size(size):
+    """int8: scales on both sides of those whose quotients are computed by products; zeros beside the smallest numbers."""
+    d = Dialogues(False, [100, 7], 2, 32, seed=21, size=lambda b, n: np.where(np.arange(n) % 5 == 4, 0.0, size))
+    sums, err = d.summaries(), flag()
+    d.summarize(sums, [0, 0], 100, [0, 100, 107], err)
+    assert err.item() == 0
+    same(sums, d.want([0, 0], [100, 7]))
+
+
 @pytest.mark.parametrize("four", [False, True])
 def test_summaries_bad_arguments_on_the_device(four):
     """Positions outside the table, page ids outside the pool, offsets out of order: flagged, other pages done."""
