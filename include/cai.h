@@ -550,7 +550,8 @@ cai_status cai_kv_select(const cai_kv_summary* summaries, int32_t num_kv_heads, 
  *                 aligned, no preparation; may be null when that is 0.  Calls that share it must not
  *                 overlap on the GPU
  *   num_splits, softmax_scale, roundings and errors otherwise as cai_kv4_decode, for the int8 cache, too
- *   (there a V scale below 2^-100 counts as 2^-100). */
+ *   (there a V scale below 2^-100, or below 2^-50 of the largest of the list's, may count as that: the output is off by
+ *   2^-93, or by 2^-50 of the largest |V|, at most). */
 size_t cai_kv_attend_pages_workspace_size(int32_t rows, int32_t num_q_heads, int32_t num_kv_heads, int32_t width,
                                           int32_t page_size, int32_t num_splits);
 cai_status cai_kv_attend_pages(const cai_kv_pool* kv_pools, int32_t num_kv_heads, const uint16_t* q, int32_t rows,

@@ -22,8 +22,13 @@
 // V's scale goes into the exponent: with v the token's scale, the weight that multiplies V's codes is 2^(z + log2 v - r),
 // r the reference, chosen so that the largest such weight is 2^7 to 2^15; the sum of the softmax takes it over v, in fp32.  So
 // the weights keep fp16's eleven bits whatever the size of V: scaled after the exponential, a cache of small values
-// (v about 2^-17) would leave them among the subnormals.  Scales below 2^-100 count as 2^-100, and so does that of a
-// token whose V is 0: its codes are 0, and it moves no reference.
+// (v about 2^-17) would leave them among the subnormals.
+//
+// A weight below 2^-126 is 0, and its share of the sum with it; so scales count as 2^-60 U at least, those of zero vectors among
+// them, with U a bound of the piece's scales so far: 2^-40, and when one passes it 2^10 times the largest of its tile.  A key of
+// scale U or less set the reference at a weight of 2^7, so that it has z >= r + 7 - log2 U; a key whose weight is lost has
+// z < r - 126 - log2 U + 60, a share below 2^-73 of that one's.  The output is off by 2^-50 max |V| at most, or 2^-93.  (With
+// 2^-100 as the least scale of any list, zeros were lost beside scales of 2^26 and more.)
 //
 // Roundings: the query to fp16 (exact for magnitudes from 2^-17 to 65504, below that off by 2^-25 at most), a weight to
 // fp16 for its product with V (2^-11 of it, or 2^-32 of the largest), the output to bf16 once; the rest is fp32.
@@ -63,10 +68,11 @@ struct Shape {
   // [4 quarters][HN] maxima, sums, references and factors of a raise (the latter two a copy per quarter)
   static constexpr int kXSum = 4 * HN, kXRef = 8 * HN, kXFac = 12 * HN, kXFloats = 16 * HN;
   static constexpr int kOffTok = kOffX + kSets * kXFloats * 4;       // int8: [set][2 tiles][key] K's scale (log2 units), V's
-  static constexpr int kOffBars = kOffTok + (kFour ? 0 : kSets * 2 * kT * 8);
+  static constexpr int kOffTop = kOffTok + (kFour ? 0 : kSets * 2 * kT * 8);  // int8: [set][quarter] V's largest scale in a tile
+  static constexpr int kOffBars = kOffTop + (kFour ? 0 : kSets * 16);
   static constexpr int kSetBars = 2 * kStages + 16;
   static constexpr int kOffInfo = (kOffBars + kSets * kSetBars * 8 + 15) & ~15;  // [set] int4 per tile
-  static constexpr int kOffScan = kOffInfo + kSets * kInfo * 16;     // start_list's
+  static constexpr int kOffScan = kOffInfo + kSets * kInfo * 16;     // start_lists'
   static constexpr int kOffWait = kOffScan + kThreads / 32 * 8;
   static constexpr int kOffSlot = kOffWait + 16;
   static constexpr int kOffPieces = kOffSlot + 16;                   // [set] pieces, then the list's state
@@ -104,6 +110,10 @@ __device__ __forceinline__ void codes8(const uint4& w, uint32_t* r) {
   i8x4_to_f16x4(w.z, r[4], r[5]);
   i8x4_to_f16x4(w.w, r[6], r[7]);
 }
+
+// int8: the bound U of V's scales, as the bits of 2^-60 U, 2^-100 at a piece's start.
+constexpr int kLeastScale = (127 - 100) << 23;
+constexpr int kScaleRange = 60 << 23, kScaleRoom = 10 << 23;
 
 __device__ __forceinline__ int piece_tiles(const Piece4& pc) {
   return pc.start < pc.end ? (pc.end - 1) / kT - pc.start / kT + 1 : 0;
@@ -569,12 +579,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       float* nref = xch + S::kXRef + quarter * HN; // negated references (log2 units)
       float* fac = xch + S::kXFac + quarter * HN;  // factors of a raise
       const float2* tok = reinterpret_cast<const float2*>(smem + S::kOffTok) + set * 2 * kT + key;
+      int* tops = reinterpret_cast<int*>(smem + S::kOffTop) + set * 4;
 
       for (int pi = 0; pi < count; ++pi) {
-        const Piece4 pc = pieces[pi];
-        const int nt = piece_tiles(pc);
-        const int64_t row0 = (int64_t)pc.row * p.num_heads + (int64_t)pc.kvh * G + h0;  // the block's first head row
+        const int nt = piece_tiles(pieces[pi]);
+        // The block's first head row.  (Read from the list where it is wanted: kept through the tiles it makes registers spill.)
+        auto first_row = [&]() { return (int64_t)pieces[pi].row * p.num_heads + (int64_t)pieces[pi].kvh * G + h0; };
         if (nt == 0) {  // nothing to attend, or an invalid length (flagged): out = 0, lse = -inf
+          const int64_t row0 = first_row();
           for (int i = key; i < nh * kHeadDim / 4; i += kT)
             reinterpret_cast<uint2*>(p.out + row0 * kHeadDim)[i] = make_uint2(0u, 0u);
           if (p.lse_out && key < nh) p.lse_out[row0 + key] = -INFINITY;
@@ -594,6 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
 #pragma unroll
         for (int h = 0; h < HN / 2; ++h) l[h] = 0ull;
         bool have_ref = false;  // some key was attended (the same in the whole set)
+        int least = kLeastScale;  // int8: what V's scales count as at least (the same in the whole set)
         for (int t = 0; t < nt; ++t) {
           const int n = gt + t;
           ok = mbar_wait_lean(s_full, n & 1, wctl) && ok;
@@ -608,8 +621,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             ks2 = f2(p.scale_log2, p.scale_log2);
           } else {
             const float2 sc = tok[(n & 1) * kT];
-            const float v = fmaxf(sc.y, 0x1p-100f);
-            const float ks = valid ? sc.x : 0.0f, lv = valid ? log2f(v) : 0.0f, iv = valid ? __fdividef(1.0f, v) : 0.0f;
+            const float v = fmaxf(sc.y, __int_as_float(least));
+            const bool above = __float_as_int(v) - least > kScaleRange;  // (U has to be raised, and the references with it)
+            const float ks = valid ? sc.x : 0.0f, lv = !valid ? 0.0f : above ? INFINITY : __log2f(v), iv = ex2_approx(-lv);
             ks2 = f2(ks, ks);
             lv2 = f2(lv, lv);
             iv2 = f2(iv, iv);
@@ -641,6 +655,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           while (true) {  // (one copy of the code: instruction cache)
             const bool raised = raise;
             if (raise) {
+              if constexpr (!kFour) {
+                const float x = valid ? tok[(n & 1) * kT].y : 0.0f;
+                const int most = __reduce_max_sync(0xffffffffu, __float_as_int(fmaxf(x, 0.0f)));
+                if (lane == 0) tops[quarter] = most;
+                named_barrier_sync(bar, 128);
+                const int4 t4 = *reinterpret_cast<const int4*>(tops);
+                const int top = max(max(t4.x, t4.y), max(t4.z, t4.w));
+                if (top - least > kScaleRange) least = top - (kScaleRange - kScaleRoom);
+                const float lv = valid ? __log2f(fmaxf(x, __int_as_float(least))) : 0.0f, iv = ex2_approx(-lv);
+                lv2 = f2(lv, lv);
+                iv2 = f2(iv, iv);
+              }
               // Raise the references that a weight passes by 2^15 (all of them at the first tile with a key).
 #pragma unroll 1
               for (int h1 = 0; h1 < HN; h1 += 16) {
@@ -668,7 +694,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
                 const float v = fmaxf(fmaxf(w[0], w[HN]), fmaxf(w[2 * HN], w[3 * HN]));
                 const float up = any && (!have_ref || v > kRaise) ? v - kWeightLift : 0.0f;
                 nref[h] -= up;
-                fac[h] = ex2_approx(-up);
+                // (int8: the sums so far, 2^115 times a weight of 1, count after a raise by more than 126, too: by its third, three
+                // times)
+                fac[h] = ex2_approx(kFour ? -up : up * (-1.0f / 3.0f));
               }
               __syncwarp();
               if (have_ref) {
@@ -684,14 +712,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
                   tmem_ld_32x32b_x8(tm + S::kColO + h1, r);
                   tmem_wait_ld();
 #pragma unroll
-                  for (int e = 0; e < 8; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f[e]);
+                  for (int e = 0; e < 8; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * (kFour ? f[e] : f[e] * f[e] * f[e]));
                   tmem_st_32x32b_x8(tm + S::kColO + h1, r);
                 }
+#pragma unroll 1
+                for (int times = kFour ? 1 : 3; times > 0; --times) {
 #pragma unroll
-                for (int h = 0; h < HN; h += 4) {
-                  const float4 f = *reinterpret_cast<const float4*>(fac + h);
-                  l[h / 2] = f2_mul(l[h / 2], f2(f.x, f.y));
-                  l[h / 2 + 1] = f2_mul(l[h / 2 + 1], f2(f.z, f.w));
+                  for (int h = 0; h < HN; h += 4) {
+                    const float4 f = *reinterpret_cast<const float4*>(fac + h);
+                    l[h / 2] = f2_mul(l[h / 2], f2(f.x, f.y));
+                    l[h / 2 + 1] = f2_mul(l[h / 2 + 1], f2(f.z, f.w));
+                  }
                 }
                 tmem_wait_st();
               }
@@ -780,7 +811,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         ok = mbar_wait_lean(&pv_done[(gt - 1) & 1], ((gt - 1) >> 1) & 1, wctl) && ok;
         __syncwarp();
         tc_fence_after();
-        const int64_t slot0 = (int64_t)pc.slot * G + h0;
+        const int slot = pieces[pi].slot;
+        const int64_t row0 = first_row(), slot0 = (int64_t)slot * G + h0;
 #pragma unroll 1
         for (int h = lane; h < HN; h += 32) {
           const float* y = xch + S::kXSum + h;
@@ -788,12 +820,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           fac[h] = have_ref && sum > 0.0f ? 1.0f / sum : 0.0f;
           if (quarter == 0 && h < nh) {
             const float lse2 = have_ref && sum > 0.0f ? log2f(sum) - nref[h] : -INFINITY;
-            if (pc.slot >= 0) p.ws_lse[slot0 + h] = lse2;
+            if (slot >= 0) p.ws_lse[slot0 + h] = lse2;
             else if (p.lse_out) p.lse_out[row0 + h] = lse2 * kLn2;
           }
         }
         __syncwarp();
-        uint16_t* out = pc.slot < 0 ? p.out + row0 * kHeadDim + key : nullptr;
+        uint16_t* out = slot < 0 ? p.out + row0 * kHeadDim + key : nullptr;
         float* ws = p.ws_o + slot0 * kHeadDim + key;
 #pragma unroll 1
         for (int h1 = 0; h1 < nh; h1 += 16) {
