@@ -114,6 +114,7 @@ __device__ __forceinline__ void codes8(const uint4& w, uint32_t* r) {
 // int8: the bound U of V's scales, as the bits of 2^-60 U, 2^-100 at a piece's start.
 constexpr int kLeastScale = (127 - 100) << 23;
 constexpr int kScaleRange = 60 << 23, kScaleRoom = 10 << 23;
+constexpr float kSumUnit = 0x1p-12f;  // int8: sums are smaller by it: those of 2^24 weights over scales of 2^-100 stay below 2^128
 
 __device__ __forceinline__ int piece_tiles(const Piece4& pc) {
   return pc.start < pc.end ? (pc.end - 1) / kT - pc.start / kT + 1 : 0;
@@ -623,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             const float2 sc = tok[(n & 1) * kT];
             const float v = fmaxf(sc.y, __int_as_float(least));
             const bool above = __float_as_int(v) - least > kScaleRange;  // (U has to be raised, and the references with it)
-            const float ks = valid ? sc.x : 0.0f, lv = !valid ? 0.0f : above ? INFINITY : __log2f(v), iv = ex2_approx(-lv);
+            const float ks = valid ? sc.x : 0.0f, lv = !valid ? 0.0f : above ? INFINITY : __log2f(v), iv = ex2_approx(-lv) * kSumUnit;
             ks2 = f2(ks, ks);
             lv2 = f2(lv, lv);
             iv2 = f2(iv, iv);
@@ -663,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
                 const int4 t4 = *reinterpret_cast<const int4*>(tops);
                 const int top = max(max(t4.x, t4.y), max(t4.z, t4.w));
                 if (top - least > kScaleRange) least = top - (kScaleRange - kScaleRoom);
-                const float lv = valid ? __log2f(fmaxf(x, __int_as_float(least))) : 0.0f, iv = ex2_approx(-lv);
+                const float lv = valid ? __log2f(fmaxf(x, __int_as_float(least))) : 0.0f, iv = ex2_approx(-lv) * kSumUnit;
                 lv2 = f2(lv, lv);
                 iv2 = f2(iv, iv);
               }
@@ -694,7 +695,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
                 const float v = fmaxf(fmaxf(w[0], w[HN]), fmaxf(w[2 * HN], w[3 * HN]));
                 const float up = any && (!have_ref || v > kRaise) ? v - kWeightLift : 0.0f;
                 nref[h] -= up;
-                // (int8: the sums so far, 2^115 times a weight of 1, count after a raise by more than 126, too: by its third, three
+                // (int8: the sums so far, over scales of 2^-100, count after a raise by more than 126, too: by its third, three
                 // times)
                 fac[h] = ex2_approx(kFour ? -up : up * (-1.0f / 3.0f));
               }
@@ -819,7 +820,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           const float sum = (y[0] + y[HN]) + (y[2 * HN] + y[3 * HN]);
           fac[h] = have_ref && sum > 0.0f ? 1.0f / sum : 0.0f;
           if (quarter == 0 && h < nh) {
-            const float lse2 = have_ref && sum > 0.0f ? log2f(sum) - nref[h] : -INFINITY;
+            const float lse2 = have_ref && sum > 0.0f ? log2f(sum) + (kFour ? 0.0f : 12.0f) - nref[h] : -INFINITY;
             if (slot >= 0) p.ws_lse[slot0 + h] = lse2;
             else if (p.lse_out) p.lse_out[row0 + h] = lse2 * kLn2;
           }
@@ -838,7 +839,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             const float f[4] = {f4.x, f4.y, f4.z, f4.w};
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float x = f[e] != 0.0f ? __uint_as_float(r[h + e]) * f[e] : 0.0f;  // (nothing attended: whatever is there does not count)
+              const float x = f[e] != 0.0f ? __uint_as_float(r[h + e]) * (kFour ? 1.0f : kSumUnit) * f[e] : 0.0f;  // (nothing attended: whatever is there does not count)
               if (h1 + h + e < nh) {
                 if (out) out[(h1 + h + e) * kHeadDim] = (uint16_t)pack_bf16x2(x, 0.0f);
                 else ws[(h1 + h + e) * kHeadDim] = x;

@@ -66,3 +66,19 @@ def test_values_of_every_size(g, spread, order):
     e = e if order == "rising" else e[::-1] if order == "falling" else rng.permutation(e)
     e = np.where(rng.random(n) < 0.1, -np.inf, e)
     check(rng.normal(size=(n, 128)).astype(np.float32) * 3, sized(rng, n, e), g, splits=(0, 1, 3), scale=128 ** -0.5, rng=rng)
+
+
+@pytest.mark.parametrize("g", [4, 32, 64])
+@pytest.mark.parametrize("size", [0.0, 2.0 ** -92])
+def test_long_lists_of_the_smallest_values(g, size):
+    """20000 tokens whose weights over V's scale, 2^-100 at least, are as large as they get: 2^7 in the first tile and
+    2^7.8 times that in all others."""
+    rng = np.random.default_rng(7)
+    k = np.zeros((32, 128), np.float32)
+    k[16:] = 5.4  # (logit: a power of e)
+    d = dialogue(k, (rng.uniform(0.9, 1.0, (32, 128)) * size).astype(np.float32))
+    lists = np.repeat(d.table_np[0, [0, 1]], [8, 1242])[None, None]
+    q = dev(np.ones((1, g, 128), np.float32), torch.bfloat16)
+    for splits in (1, 2):
+        out, lse = attend(d, q, lists, [20000], scale=1.0 / 128, splits=splits)
+        check_attend(d, q, lists, [20000], out, lse, scale=1.0 / 128)
