@@ -547,8 +547,9 @@ cai_status cai_kv_select(const cai_kv_summary* summaries, int32_t num_kv_heads, 
  *   out           bf16 bits [rows][num_q_heads][128], 16-byte aligned, rounded once from fp32
  *   lse_out       fp32 [rows][num_q_heads], nullable
  *   workspace     cai_kv_attend_pages_workspace_size() bytes (cai_kv4_... for the 4-bit cache), 256-byte
- *                 aligned, no preparation; may be null when that is 0.  Calls that share it must not
- *                 overlap on the GPU
+ *                 aligned, no preparation; may be null when that is 0.  Enough for every call with the
+ *                 same heads, page size and num_splits and as many rows and pages or fewer, on this
+ *                 device.  Calls that share it must not overlap on the GPU
  *   num_splits, softmax_scale, roundings and errors otherwise as cai_kv4_decode, for the int8 cache, too
  *   (there a V scale below 2^-100, or below 2^-50 of the largest of the list's, may count as that: the output is off by
  *   2^-93, or by 2^-50 of the largest |V|, at most). */

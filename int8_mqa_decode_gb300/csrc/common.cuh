@@ -292,6 +292,8 @@ cudaError_t launch_decode4(const Decode4Params& p, cudaStream_t stream);
 // Fills the split fields of p (batch, heads, page_size, max_pages and window given; num_splits 0: automatic) and
 // returns the workspace bytes that they need; place_decode4 then sets the workspace's pointers.
 size_t plan_decode4(Decode4Params& p, int32_t num_splits);
+// Lists: enough for every plan of this many rows and pages or fewer, with the same heads, page size and num_splits.
+size_t most_list_bytes(const Decode4Params& p, int32_t num_splits);
 void place_decode4(Decode4Params& p, void* workspace);
 
 }  // namespace cai

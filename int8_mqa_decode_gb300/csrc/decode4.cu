@@ -495,6 +495,8 @@ cudaError_t launch_heads8(const Decode4Params& p, cudaStream_t stream) {
 }
 
 int64_t up256(int64_t x) { return (x + 255) / 256 * 256; }
+// Partial outputs and their sums.
+int64_t partial_bytes(int64_t slots, int64_t G) { return up256(slots * G * kHeadDim * 4) + up256(slots * G * 4); }
 
 }  // namespace
 
@@ -515,9 +517,12 @@ static int32_t list_splits(const Decode4Params& p, int64_t ranges, int64_t units
   return whole <= shared + (s > 1 ? 2 : tc ? 4 : 6) ? (int32_t)s : 0;
 }
 
+// Ranges of a launch that has work for all of them (lists: one for each set of a block's warps).
+static int launch_blocks(const Decode4Params& p, int tc) { return num_sms() * (!tc ? kBlocks4 : p.lists ? 2 : 1); }
+
 size_t plan_decode4(Decode4Params& p, int32_t num_splits) {
   const int G = p.num_heads / p.num_kv_heads, tc = tensor_heads(p);
-  const int blocks = num_sms() * (!tc ? kBlocks4 : p.lists ? 2 : 1);  // (lists: a range for each set of a block's warps)
+  const int blocks = launch_blocks(p, tc);
   p.head_groups = tc ? (G + tc - 1) / tc : 1;
   // What the start and merge of a piece cost, in tiles, fitted from the times of blocks with different numbers of
   // tiles and pieces.  (Lognormal contexts of 32 heads: 77.5 us with one tile, 73.6 with five; 96 sequences of 8 heads:
@@ -545,8 +550,27 @@ size_t plan_decode4(Decode4Params& p, int32_t num_splits) {
   }
   p.ranges = (int32_t)(ranges < most ? ranges : most);
   if (p.chunk == 0) slots = 2 * p.ranges;
-  const int64_t rows = slots * G;
-  return (size_t)((p.chunk == 0 ? up256(p.ranges * 8) : 0) + up256(rows * kHeadDim * 4) + up256(rows * 4));
+  return (size_t)((p.chunk == 0 ? up256(p.ranges * 8) : 0) + partial_bytes(slots, G));
+}
+
+// The plan of more rows may need less (rows cut in several pieces, whole ones, ranges that rows share), so this is not its
+// size but a bound of those of all plans of p.batch rows and p.max_pages pages or fewer.
+size_t most_list_bytes(const Decode4Params& p, int32_t num_splits) {
+  const int G = p.num_heads / p.num_kv_heads, tc = tensor_heads(p);
+  const int64_t units = (int64_t)p.batch * p.num_kv_heads, ranges = launch_blocks(p, tc) / (tc ? (G + tc - 1) / tc : 1);
+  const int64_t tiles = ((int64_t)p.max_pages * p.page_size + kDecodeTile - 1) / kDecodeTile;
+  int64_t slots = 0, bytes = 0;
+  if (num_splits > 0) {
+    slots = std::min<int64_t>(num_splits, tiles) * units;
+    if (num_splits == 1 || tiles == 1) slots = 0;
+  } else {
+    for (int64_t u = p.num_kv_heads; u <= std::min(units, ranges); u += p.num_kv_heads) {
+      const int64_t s = std::min<int64_t>(std::min(tiles, ranges / u), kMaxSplits);
+      if (s > 1) slots = std::max(slots, u * s);
+    }
+    if (tiles > 4) bytes = up256(ranges * 8) + partial_bytes(2 * ranges, G);  // (more ranges than rows have tiles are not launched)
+  }
+  return (size_t)std::max(bytes, partial_bytes(slots, G));
 }
 
 void place_decode4(Decode4Params& p, void* workspace) {

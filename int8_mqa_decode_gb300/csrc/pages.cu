@@ -70,7 +70,7 @@ size_t attend_bytes(int32_t rows, int32_t num_q_heads, int32_t num_kv_heads, int
   p.max_pages = width;
   p.lists = 1;
   p.eight = eight;
-  return plan_decode4(p, num_splits);
+  return most_list_bytes(p, num_splits);
 }
 
 template <class Pool>
