@@ -643,8 +643,8 @@ int32_t cai_ring_pages(int32_t window, int32_t page_size, int32_t max_new_tokens
 cai_status cai_ring_table_row(int32_t* row, int32_t max_pages_per_seq, const int32_t* ring_ids, int32_t ring,
                               int32_t hi, int32_t page_size);
 
-/* Limit, in nanoseconds, of every bounded wait inside the decode and prefill kernels
- * (process-wide, read at each launch; 0 restores the default of 2 s; a wait checks its
+/* Limit, in nanoseconds, of every bounded wait inside the kernels: of decode, prefill,
+ * attention over lists of pages and the selection's scores (process-wide, read at each launch; 0 restores the default of 2 s; a wait checks its
  * clock after each suspension of up to 1 ms, so shorter limits act as about 1 ms).  A
  * CTA whose wait runs out sets CAI_DEVERR_TIMEOUT, stops its work, waits for its own
  * copies and tensor-core operations in flight, frees its tensor memory and returns;
@@ -658,9 +658,11 @@ void cai_set_wait_limit_ns(uint64_t ns);
  * -1, the default, turns it off).  With stage = n >= 0, every CTA of the following
  * decode launches skips the load of its n-th K/V stage (64 tokens; over the 4-bit cache
  * its n-th tile of 128 keys, or, up to 8 heads per K/V head, each warp its n-th step of 32),
- * and every CTA of the following prefill launches skips the load of its n-th K tile (128
- * keys); the
- * waits for them run out after the wait limit and the launch reports
+ * every CTA of the following launches of attention over lists that of the n-th tile of
+ * 128 keys in each of its two halves (4-bit, up to 8 heads per K/V head: as the decode),
+ * and every CTA of the following prefill launches that of its n-th K tile (128 keys); a
+ * CTA of the selection's scores does not hear of its products with the n-th tile of 128
+ * pages.  The waits for them run out after the wait limit and the launch reports
  * CAI_DEVERR_TIMEOUT.  Nothing faults: the load is simply never issued.  A CTA with
  * fewer stages than n + 1 is not affected. */
 void cai_set_fault_injection(int32_t stage);

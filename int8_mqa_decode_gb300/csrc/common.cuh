@@ -212,6 +212,7 @@ struct SelectParams {
   int32_t* len_out;             // [rows]
   int32_t* err;
   uint64_t wait_ns;
+  int32_t drop_stage;           // fault injection: the tile of pages whose products no block hears of (-1: none)
 };
 
 struct PrefillLaunch {

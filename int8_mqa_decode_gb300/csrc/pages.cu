@@ -185,6 +185,7 @@ cai_status cai_kv_select(const cai_kv_summary* summaries, int32_t num_kv_heads, 
   p.len_out = len_out;
   p.err = err_flag;
   p.wait_ns = wait_limit_ns();
+  p.drop_stage = fault_drop_stage();
   return cuda_status(launch_select(p, static_cast<cudaStream_t>(stream)));
 }
 

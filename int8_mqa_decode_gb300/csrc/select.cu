@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
   extern __shared__ __align__(128) uint8_t cols[];  // column n, channels of unit u (8 of K's 256): (n / 8) 4096 + 128 u + 16 (n % 8)
   __shared__ __align__(16) float scale_of[kCols];
   __shared__ __align__(16) int shared[2 * kWarps + (sizeof(RowTile) + 3) / 4];
-  __shared__ uint64_t done;  // a tile's products
+  __shared__ uint64_t done, drain;  // a tile's products; all products of a block that gives up
   __shared__ WaitState wait;
   __shared__ uint32_t slot;
   volatile WaitState* wctl = &wait;
@@ -178,6 +178,7 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
   if (warp == 0) tmem_alloc(&slot, kTmem);
   if (tid == 0) {
     mbar_init(&done, 1);
+    mbar_init(&drain, 1);
     wait.abort = 0;
     wait.limit_ns = p.wait_ns;
     fence_barrier_init();
@@ -285,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
       if (elect_one()) {
 #pragma unroll
         for (int k = 0; k < 16; ++k) mma_f16_ts(tmem + kColD, tmem + 8 * k, dq + (uint64_t)(k * 16), idesc, k > 0 ? 1u : 0u);
-        mma_commit(&done);
+        if ((base - c0) / kTilePages != p.drop_stage) mma_commit(&done);  // (fault injection: never said)
       }
       __syncwarp();
     }
@@ -354,7 +355,11 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
   if (tid == 0 && wctl->abort && p.err) atomicOr(p.err, CAI_DEVERR_TIMEOUT);
   tc_fence_after();
   if (warp == 0) {
-    if (!ok) mbar_wait_drain(&done, phase);  // the products have ended before tensor memory goes
+    if (__any_sync(0xffffffffu, !ok)) {  // the products have ended before tensor memory goes
+      if (elect_one()) mma_commit(&drain);
+      __syncwarp();
+      mbar_wait_drain(&drain, 0);
+    }
     __syncwarp();
     tmem_dealloc(tmem, kTmem);
   }
