@@ -169,8 +169,8 @@ __global__ void __launch_bounds__(kThreads, 2) score_kernel(const __grid_constan
   load_q(8 * warp);
 
   const int lg = page_log2(p.page_size);
-  const int64_t last_pos = min(rt.pos0 + rt.n, (int64_t)p.max_pages << lg);  // (positions past the table are refused by the selection)
-  if (last_pos <= 0) return;
+  const int64_t room = (int64_t)p.max_pages << lg, last_pos = min(rt.pos0 + rt.n, room);  // (rows outside are refused by the selection)
+  if (last_pos <= 0 || rt.pos0 >= room) return;
   const int blocks = (int)((last_pos - 1) >> lg) + 1;  // of the last row
   c1 = min(c0 + span * kTilePages, blocks - p.last);
   if (blocks <= p.keep || c0 >= c1) return;
