@@ -539,7 +539,9 @@ cai_status cai_kv_select(const cai_kv_summary* summaries, int32_t num_kv_heads, 
 /* Attention of rows of queries over lists of pages, a list for each K/V head: over the tokens of
  * the listed pages in turn, the first len[r] of them.  The lists of cai_kv_select, or any other:
  * a page that stands in a list twice counts twice, and no token is masked but by len.
- *   q             bf16 bits [rows][num_q_heads][128], 16-byte aligned; rows <= 65535
+ *   q             bf16 bits [rows][num_q_heads][128], 16-byte aligned; rows <= 65535, as every call's
+ *                 batch (no row depends on another: more of them, as cai_kv_select takes, are
+ *                 given in several calls)
  *   num_q_heads   a multiple of num_kv_heads; up to 128 query heads per K/V head
  *   pages         int32 [rows][num_kv_heads][width]; entries behind ceil(len[r] / P) are not read
  *   len           int32 [rows]; 0: out = 0, lse = -inf.  Outside [0, width * P]: the same, and

@@ -938,11 +938,13 @@ def cai_kv_select(summaries: Sequence[KVSummary], q: torch.Tensor, block_table: 
 
 def cai_kv_attend_pages_workspace_size(rows: int, num_q_heads: int, num_kv_heads: int, width: int, page_size: int,
                                        num_splits: int = 0) -> int:
+    """Bytes for a call of these rows and lists of this width, or of fewer and shorter ones."""
     return int(load().cai_kv_attend_pages_workspace_size(rows, num_q_heads, num_kv_heads, width, page_size, num_splits))
 
 
 def cai_kv4_attend_pages_workspace_size(rows: int, num_q_heads: int, num_kv_heads: int, width: int, page_size: int,
                                         num_splits: int = 0) -> int:
+    """cai_kv_attend_pages_workspace_size for the 4-bit cache."""
     return int(load().cai_kv4_attend_pages_workspace_size(rows, num_q_heads, num_kv_heads, width, page_size, num_splits))
 
 

@@ -8,9 +8,9 @@
 // pieces count: a block's two sets of warps (a producer, an issuer, four converting and four softmax warps each) have
 // pieces of their own and nothing in common but the block's entry and exit; while one set starts a row or
 // merges it (5 k cycles), the other one's products run.  (Both sets on one piece, every other tile each, as in the decode:
-// 4096 rows of 2048 tokens, 32 heads, 374 us 4-bit and 454 us int8; so 334 and 354.)  What bounds these is the issue
+// 4096 rows of 2048 tokens, 32 heads, 374 us 4-bit and 454 us int8; so 337 and 353.)  What bounds these is the issue
 // slots (74% at 1200 cycles a tile): the conversion of codes, 500 instructions a warp and tile, and the softmax, 250.
-// 64 rows of 4096 tokens, 64 heads, take 32 us int8 and 30 4-bit (71 MB at 2.2 TB/s): 5 k cycles until a set knows its
+// 64 rows of 4096 tokens, 64 heads, take 33 us int8 and 30 4-bit (71 MB at 2.2 TB/s): 5 k cycles until a set knows its
 // piece, 8 k until its query and first tile are there (all sets ask at once), 4 k a tile, of which the converters of a set
 // need 3, and 8 k for the sums and the partial output, which all sets write at once.
 //

@@ -503,9 +503,9 @@ int64_t partial_bytes(int64_t slots, int64_t G) { return up256(slots * G * kHead
 // Lists are mostly full, so equal pieces of each row, one for every range, are balanced by themselves: no block looks
 // for its share of all rows, and none holds the end of one row and the start of another.  In tiles, with a piece's
 // start and end (piece_tiles): `whole` for equal pieces, `shared` for ranges that are cut anywhere.  64 rows of 32 tiles, 64
-// heads, int8: 31.3 us in four pieces, 34.8 shared; 128 rows 48.5 (two pieces), 51.3; 256 rows 75.3 (one), 83.0; 256 rows of 16
-// tiles, 32 heads, 33.4 and 40.7; 4 rows of 4 tiles, 8 heads: 8.8 in four, 11.6 whole.  (Rows of random lengths: 29.6 and 28.3,
-// 45.9 and 37.0, 69.8 and 55.8, 30.4 and 29.6.)  Several rows a range, one behind the other, gain 10% where all
+// heads, int8: 32.5 us in four pieces, 35.0 shared; 128 rows 48.7 (two pieces), 51.5; 256 rows 76.2 (one), 82.5; 256 rows of 16
+// tiles, 32 heads, 33.3 and 40.5; 4 rows of 4 tiles, 8 heads: 8.7 in four, 10.7 shared.  (Rows of random lengths, which the host
+// does not know: 30.0 and 28.9, 46.5 and 37.5, 69.6 and 55.9, 30.1 and 30.0.)  Several rows a range, one behind the other, gain 10% where all
 // lists are full and lose up to 60% where they are not: shared.  0: shared.
 static int32_t list_splits(const Decode4Params& p, int64_t ranges, int64_t units, int64_t tiles, bool tc) {
   if (units == 0 || units > ranges) return 0;

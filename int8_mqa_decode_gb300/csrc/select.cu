@@ -601,6 +601,7 @@ struct BlockGroup {
 };
 
 // A warp per (row, K/V head), for contexts of up to 32 kItems pages: the scores stay in registers, page 32 k + l in lane l.
+// (Four blocks an SM leave 64 registers: with 1024 pages a thread spills 56 bytes.)
 template <int kItems>
 __global__ void __launch_bounds__(kThreads, 4) select_warp_kernel(const __grid_constant__ SelectParams p, int64_t units) {
   __shared__ __align__(16) uint32_t hist[kWarps][256];
