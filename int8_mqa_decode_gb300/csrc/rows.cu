@@ -435,8 +435,8 @@ __device__ __forceinline__ void append_group(const AppendRowsParams& p, int b, i
   }
 }
 
-// (Four blocks an SM at 64 registers, of which some forms spill up to 20 bytes, or three at 77: 6353 rows of 32 heads 30.2 or 34.5 us, a decode step of
-// 256 sequences 5.0 or 5.6.)
+// (Four blocks an SM at 64 registers, of which some forms spill up to 20 bytes, or three at 77: 6353 rows of 32 heads 30.2
+// or 34.5 us, a decode step of 256 sequences 5.0 or 5.6.)
 // kMany: there are fewer blocks than groups that every sequence might have; a block looks through its share of these, 32
 // at a time, for those with rows.  (A prompt of 4096 tokens beside 135 single ones, 8 K/V heads: 44 us, a block for each
 // possible group 350.)
